@@ -58,7 +58,9 @@ typedef enum os_status {
   OS_ERR_MISALIGNED = 2,       /* a base address or leading dimension is not 16-byte aligned */
   OS_ERR_UNSUPPORTED = 3,      /* a valid request this version does not implement */
   OS_ERR_CUDA = 4,             /* a CUDA runtime or driver call failed (launch, attribute, ...) */
-  OS_ERR_TIMEOUT = 5           /* a kernel gave up on a bounded wait (os_check_device_error) */
+  OS_ERR_TIMEOUT = 5,          /* a kernel gave up on a bounded wait (os_check_device_error) */
+  OS_ERR_BAD_INDEX = 6         /* a kernel met a page or position outside its cache
+                                  (os_check_device_error) */
 } os_status;
 
 /*
@@ -468,6 +470,189 @@ OSS_API os_status os_merge_partials(const float* part_m, const float* part_l, co
                             void* stream);
 
 /*
+ * A paged key-value cache. The pool holds num_pages pages of page_size token
+ * slots for each of `heads` key heads; the tokens of sequence b are its pages
+ * in the order of the page table: token t lies in slot t % page_size of page
+ * page_table[b * ld_table + t / page_size]. Several sequences may name the
+ * same page (a shared prefix) as long as nothing is written to it.
+ *
+ *   k_pages, v_pages  the pools: element (page, head, slot, d) at
+ *                     page * ld_page + head * ld_head + slot * ld_slot + d, the
+ *                     same strides (in elements) for both. Any order of the
+ *                     three is allowed ([page, head, slot, d] or [page, slot,
+ *                     head, d], or K and V pages side by side).
+ *   page_table        [batch, max_pages] int32, DEVICE, row stride ld_table;
+ *                     only the entries of a sequence's ceil(len / page_size)
+ *                     first pages are read.
+ *   kv_len            [batch] int32, DEVICE; a value outside 0 .. max_pages *
+ *                     page_size is clamped to it on the device.
+ *   page_size a power of two, 16 .. 1024 (others: OS_ERR_UNSUPPORTED).
+ *   head_dim 64 or 128 (others: OS_ERR_UNSUPPORTED).  dtype an os_dtype.
+ *   batch <= 65535, max_pages * page_size <= 2^30.
+ * A page number outside 0 .. num_pages - 1 is never followed: that row is left
+ * out (not written; masked as a key) and the device error word is set
+ * (os_check_device_error then returns OS_ERR_BAD_INDEX).
+ * Alignment: the pools 16-byte aligned, their strides multiples of 8.
+ */
+typedef struct os_paged_cache {
+  void* k_pages;
+  void* v_pages;
+  int64_t ld_page, ld_head, ld_slot;
+  const int32_t* page_table;
+  int64_t ld_table;
+  const int32_t* kv_len;
+  int32_t num_pages, heads, page_size, head_dim, dtype;
+  int32_t batch, max_pages;
+} os_paged_cache;
+
+/*
+ * os_kv_cache_append -- copy the keys and values of new tokens into their
+ * pages. kv_len holds the lengths with the new tokens: of the n_b new tokens
+ * of sequence b, token i goes to position kv_len[b] - n_b + i.
+ *
+ *   k, v        [tokens, heads, D] of the cache's type, device: element
+ *               (token, head, d) at token * ld_token + head * ld_head + d.
+ *   cu_seqlens  [batch + 1] int32, DEVICE: the new tokens of sequence b are
+ *               rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (none is fine), in
+ *               ascending order; rows behind the last sequence are not
+ *               read. NULL: one new token for each sequence, tokens == batch.
+ * Two rows that name the same slot (a page shared by two sequences) leave one
+ * of the two there; which one is not determined.
+ * Positions below 0 or without a page are left out and set the error word.
+ * Alignment: k and v 16-byte aligned, ld_token and ld_head multiples of 8.
+ * Errors: OS_ERR_INVALID_ARGUMENT, OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED,
+ * OS_ERR_CUDA. tokens == 0 is OS_OK and launches nothing.
+ */
+OSS_API os_status os_kv_cache_append(const void* k, const void* v, int64_t ld_token, int64_t ld_head,
+                                     int64_t tokens, const int32_t* cu_seqlens,
+                                     const os_paged_cache* cache, void* stream);
+
+/*
+ * os_attention_decode_paged -- attention of one query token per sequence over
+ * its paged cache, H / heads query heads sharing each key head (query head h
+ * reads key head h / (H / heads)):
+ *     s_t = scale * q . k_t;  lse = ln sum_t exp(s_t);  o = sum_t exp(s_t - lse) v_t
+ * over the sequence's kv_len tokens (the new token's key and value among
+ * them: append first). The cached tokens are cut into equal shares for the
+ * GPU's SMs whatever the lengths are, and the partial states (m, l, O) of a
+ * sequence cut between SMs are joined with the merge identity in a fixed
+ * order, so every run gives the same bits. P is rounded to the cache's type for
+ * the P V product, l sums the fp32 P. kv_len 0 gives o = 0, lse = -inf.
+ *
+ *   q     [batch, H, D], device: element (b, h, d) at b * ld_q_batch +
+ *         h * ld_q_head + d; the cache's type.
+ *   o     [batch, H, D] dense, the cache's type (round to nearest even).
+ *   lse   [batch, H] fp32, or NULL to skip.
+ *   weights  NULL, or fp32 sums of the weights that each cached token has
+ *         received, updated in place:
+ *             weights[b, g, t] += sum over the query heads h of key head g of
+ *                                 exp(s_t - lse)
+ *         element (b, g, t) at b * ld_w_batch + g * ld_w_head + t, for t <
+ *         kv_len[b]; others are left as they are. os_kv_cache_evict takes them.
+ *   workspace  device memory of at least
+ *         os_attention_decode_paged_workspace_bytes bytes, 16-byte aligned;
+ *         it needs no initialising and keeps nothing between calls. Calls
+ *         that may run at the same time need workspaces of their own.
+ *   H a multiple of cache->heads.  scale finite and > 0.
+ * Alignment: q and o 16-byte aligned, q's strides multiples of 8.
+ * Errors: OS_ERR_INVALID_ARGUMENT (also a workspace that is too small),
+ * OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED, OS_ERR_CUDA.
+ */
+OSS_API os_status os_attention_decode_paged(const void* q, int64_t ld_q_batch, int64_t ld_q_head,
+                                            int32_t H, const os_paged_cache* cache, float scale,
+                                            void* o, float* lse, float* weights,
+                                            int64_t ld_w_batch, int64_t ld_w_head, void* workspace,
+                                            int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that os_attention_decode_paged uses for H query heads
+ * over this cache on the current device, with or without weights; -1 when the
+ * device cannot be queried, 0 for arguments that the call refuses. Reads only
+ * heads, head_dim, batch, max_pages and page_size of the cache. */
+OSS_API int64_t os_attention_decode_paged_workspace_bytes(int32_t H, const os_paged_cache* cache,
+                                                          int weights);
+
+/*
+ * os_attention_fwd_packed -- attention forward over sequences of different
+ * lengths packed one behind the other, Hq / Hkv query heads sharing each key
+ * head (query head h reads key head h / (Hq / Hkv)). For sequence b with Lq =
+ * cu_seqlens_q[b + 1] - cu_seqlens_q[b] queries and Lk keys (likewise),
+ * query i of it:
+ *     S_ij = scale * q_i . k_j;  lse_i = ln sum_j exp(S_ij);
+ *     o_i  = sum_j exp(S_ij - lse_i) v_j
+ * over all its keys, or, causal, over keys j <= i + Lk - Lq: the queries are
+ * the last Lq of the Lk positions, so a prompt may be continued piece by
+ * piece. A query that sees no key (Lk == 0, or Lk < Lq) gives o = 0, lse = -inf.
+ * S = Q K^T and O += P V run on the tcgen05 tensor cores with fp32
+ * accumulation; P is rounded to the inputs' type for P V, l sums the fp32 P.
+ *
+ *   q    [tokens_q, Hq, D], k, v [tokens_k, Hkv, D], device: element (t, h, d)
+ *        at t * ld_token + h * ld_head + d, k and v with the same strides.
+ *        q, k, v of the sequences are finite; rows outside every sequence
+ *        and the other sequences' values do not reach a sequence's results,
+ *        whatever they hold.
+ *   o    [tokens_q, Hq, D] dense, the inputs' type (round to nearest even);
+ *        lse [tokens_q, Hq] fp32, or NULL. Rows outside every sequence are
+ *        left as they were.
+ *   cu_seqlens_q, cu_seqlens_k  [batch + 1] int32, DEVICE, ascending, within
+ *        0 .. tokens. Offsets that are not are clamped on the device and set
+ *        the error word (OS_ERR_BAD_INDEX); results are then undefined.
+ *   D 64 or 128, dtype an os_dtype (others: OS_ERR_UNSUPPORTED / INVALID).
+ *   tokens_q, tokens_k < 2^31; Hq a multiple of Hkv; batch <= 65535.
+ *   workspace  at least os_attention_fwd_packed_workspace_bytes bytes,
+ *        16-byte aligned; no initialising, nothing kept between calls, one for
+ *        each call that may run at the same time.
+ * Alignment: q, k, v, o 16-byte aligned, strides multiples of 8.
+ * Errors: OS_ERR_INVALID_ARGUMENT, OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED,
+ * OS_ERR_CUDA; a timed-out internal wait is reported by os_check_device_error.
+ * tokens_q == 0 is OS_OK and launches nothing.
+ */
+OSS_API os_status os_attention_fwd_packed(const void* q, int64_t ld_q_token, int64_t ld_q_head,
+                                          const void* k, const void* v, int64_t ld_kv_token,
+                                          int64_t ld_kv_head, void* o, float* lse,
+                                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                          int32_t batch, int64_t tokens_q, int64_t tokens_k,
+                                          int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
+                                          float scale, int causal, void* workspace,
+                                          int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that os_attention_fwd_packed uses; 0 for arguments that
+ * the call refuses. */
+OSS_API int64_t os_attention_fwd_packed_workspace_bytes(int32_t batch, int64_t tokens_q, int32_t Hq,
+                                                        int32_t Hkv);
+
+/*
+ * os_kv_cache_evict -- keep the cached tokens that have received the most
+ * attention weight. Of the kv_len tokens of sequence b, each key head keeps
+ * n = min(kv_len, budget): the last min(recent, n), and of the older ones the
+ * n - min(recent, n) of the largest weight (the lower position first among
+ * equal weights; -0 equals 0, NaN counts as the largest). Their rows of K and V
+ * are copied, in the order of their positions, to positions 0 .. n - 1 of the
+ * pages that new_table names; the old pages are only read, so they may be shared
+ * with other sequences, and can be freed once the call has run. The key heads
+ * of a sequence keep different tokens but the same number.
+ *
+ *   weights    fp32 [batch, heads, ...] as os_attention_decode_paged sums them:
+ *              element (b, g, t) at b * ld_w_batch + g * ld_w_head + t.
+ *   new_table  [batch, new_max_pages] int32, DEVICE, row stride ld_new_table:
+ *              pages of the same pool that no sequence in use names; the
+ *              first ceil(n / page_size) of each row are written.
+ *   kept       [batch, heads, budget] int32: the kept positions in ascending
+ *              order, -1 behind them.
+ *   new_len    [batch] int32: n.
+ *   new_weights  fp32 [batch, heads, new_max_pages * page_size] dense: the kept
+ *              tokens' weights, 0 behind them.
+ *   1 <= budget <= new_max_pages * page_size; 0 <= recent <= budget.
+ * Alignment: as the cache.
+ * Errors: OS_ERR_INVALID_ARGUMENT, OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED,
+ * OS_ERR_CUDA.
+ */
+OSS_API os_status os_kv_cache_evict(const os_paged_cache* cache, const float* weights,
+                                    int64_t ld_w_batch, int64_t ld_w_head, const int32_t* new_table,
+                                    int64_t ld_new_table, int32_t new_max_pages, int32_t budget,
+                                    int32_t recent, int32_t* kept, int32_t* new_len,
+                                    float* new_weights, void* stream);
+
+/*
  * os_check_device_error -- synchronise `stream`, then read and clear the
  * current device's error word. *code receives 0 when no kernel gave up on a
  * wait since the last check, otherwise an OS_ERR_TIMEOUT detail code
@@ -475,9 +660,12 @@ OSS_API os_status os_merge_partials(const float* part_m, const float* part_l, co
  * forward (see os_debug_inject_fault); 2 | (1 << 8) is a row softmax whose
  * wait for its row's bulk copies into shared memory gave up, 2 | (2 << 8) one
  * whose wait for the (max, sum) states of the other CTAs of its cluster gave
- * up. Returns
- * OS_ERR_TIMEOUT when the word was set, OS_ERR_CUDA when a CUDA call failed,
- * OS_OK otherwise.
+ * up; kernel 4 is os_attention_fwd_packed (sites as kernel 1). Kernel 3 is
+ * not a wait: a call on a paged cache met an index outside the cache and left
+ * that row out (site 1: a page number; site 2: a position without a page;
+ * site 3: sequence offsets that run backwards or past the tokens). Returns
+ * OS_ERR_TIMEOUT when the word was set by a wait, OS_ERR_BAD_INDEX when it was
+ * set by kernel 3, OS_ERR_CUDA when a CUDA call failed, OS_OK otherwise.
  * `code` may be NULL.
  * The word keeps the FIRST error written since it was last cleared. Call
  * this after any launch that may have failed, before the next launch: while

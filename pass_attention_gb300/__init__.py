@@ -1,5 +1,6 @@
 """liboss: online-softmax row softmax, fused attention forward, split-KV
-decode and the (m, l, O) merge on one GB300 (sm_103a).
+decode, the (m, l, O) merge, and a paged key-value cache with the attention
+that fills and reads it, on one GB300 (sm_103a).
 
 This module is the thin Python binding over the C ABI in ``include/oss.h``:
 it checks tensor dtypes and devices, allocates outputs with PyTorch, passes
@@ -34,6 +35,10 @@ __all__ = [
     "attention_decode_splitkv",
     "merge_partials",
     "decode_from_host",
+    "attention_fwd_packed",
+    "kv_cache_append",
+    "attention_decode_paged",
+    "kv_cache_evict",
     "check_device_error",
     "debug_inject_fault",
     "set_rescale_policy",
@@ -54,12 +59,25 @@ STATUS_NAMES = {
     3: "OS_ERR_UNSUPPORTED",
     4: "OS_ERR_CUDA",
     5: "OS_ERR_TIMEOUT",
+    6: "OS_ERR_BAD_INDEX",
 }
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _f32 = ctypes.c_float
+
+
+class _PagedCache(ctypes.Structure):
+    """os_paged_cache of include/oss.h."""
+
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("ld_page", _i64), ("ld_head", _i64),
+                ("ld_slot", _i64), ("page_table", _vp), ("ld_table", _i64), ("kv_len", _vp),
+                ("num_pages", _i32), ("heads", _i32), ("page_size", _i32), ("head_dim", _i32),
+                ("dtype", _i32), ("batch", _i32), ("max_pages", _i32)]
+
+
+_cache_p = ctypes.POINTER(_PagedCache)
 
 # name -> (restype, argtypes), the signatures of include/oss.h
 _SIGNATURES = {
@@ -85,6 +103,16 @@ _SIGNATURES = {
     "os_attention_decode_splitkv": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                            _f32, _vp, _vp, _vp, _vp]),
     "os_merge_partials": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, ctypes.c_int, _vp, _vp, _vp,
+                                 _vp, _vp]),
+    "os_attention_fwd_packed": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32,
+                                       _i64, _i64, _i32, _i32, _i32, _i32, _f32, ctypes.c_int, _vp,
+                                       _i64, _vp]),
+    "os_attention_fwd_packed_workspace_bytes": (_i64, [_i32, _i64, _i32, _i32]),
+    "os_kv_cache_append": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _cache_p, _vp]),
+    "os_attention_decode_paged": (_i32, [_vp, _i64, _i64, _i32, _cache_p, _f32, _vp, _vp, _vp, _i64,
+                                         _i64, _vp, _i64, _vp]),
+    "os_attention_decode_paged_workspace_bytes": (_i64, [_i32, _cache_p, ctypes.c_int]),
+    "os_kv_cache_evict": (_i32, [_cache_p, _vp, _i64, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
                                  _vp, _vp]),
     "os_check_device_error": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "os_attention_set_rescale_policy": (_i32, [_i32]),
@@ -560,6 +588,243 @@ def decode_from_host(q_host, k_host, v_host, kv_len_host, num_splits, scale=None
     out[1].copy_(lse, non_blocking=True)
     torch.cuda.current_stream().synchronize()
     return out
+
+
+# ---------------------------------------------------------------------------
+# the paged key-value cache and packed prompts
+# ---------------------------------------------------------------------------
+
+def _strides(t: torch.Tensor, name: str, ndim: int, dtype: torch.dtype, device: torch.device):
+    """Strides of an input that may be a view: a CUDA tensor of this dtype, unit
+    stride in its last dimension, the others multiples of 8 elements (16 bytes).
+    A dimension of size 1 has no stride that matters: 0."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (liboss has no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the inputs on {device}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return tuple(0 if n == 1 else x for n, x in zip(t.shape[:-1], st))
+
+
+def _ints(t: torch.Tensor, name: str, ndim: int, device: torch.device) -> None:
+    _need(t, name, torch.int32, ndim)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the inputs on {device}")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+
+
+def _cache(k_pages, v_pages, page_table, kv_len) -> _PagedCache:
+    """The os_paged_cache of these tensors (which the caller keeps alive until
+    the call has been enqueued)."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in _DTYPE_CODES:
+        raise TypeError("k_pages must be a bfloat16 or float16 torch.Tensor")
+    dev = k_pages.device
+    st = _strides(k_pages, "k_pages", 4, k_pages.dtype, dev)
+    if _strides(v_pages, "v_pages", 4, k_pages.dtype, dev) != st or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape and strides")
+    _ints(page_table, "page_table", 2, dev)
+    _ints(kv_len, "kv_len", 1, dev)
+    pages, heads, page_size, d = k_pages.shape
+    batch, max_pages = page_table.shape
+    if kv_len.shape[0] != batch:
+        raise ValueError("kv_len must have one entry for each row of page_table")
+    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
+                       page_table.data_ptr(), page_table.stride(0) if batch > 1 else 0,
+                       kv_len.data_ptr(), pages, heads, page_size, d, _DTYPE_CODES[k_pages.dtype],
+                       batch, max_pages)
+
+
+def _scratch(nbytes: int, device: torch.device, stream) -> torch.Tensor:
+    """A workspace for one call. It comes from PyTorch's allocator each time, so
+    calls on two streams or in two captured graphs never share one; on a
+    stream other than the current one its memory is held until that stream
+    has passed the call."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def attention_fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         cu_seqlens_q: torch.Tensor, cu_seqlens_k: Optional[torch.Tensor] = None,
+                         scale: Optional[float] = None, causal: bool = True,
+                         o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         stream=None):
+    """Attention forward over packed sequences: q [tokens_q, Hq, D], k and v
+    [tokens_k, Hkv, D] (bf16 or fp16, D 64 or 128, Hq a multiple of Hkv; views
+    such as slices of a fused projection are taken as they are, k and v with the
+    same strides), cu_seqlens_q and cu_seqlens_k [batch + 1] int32 on the device
+    (cu_seqlens_k None: the same). Causal: a sequence's queries are the last of
+    its keys' positions. Returns ``(o, lse)``, [tokens_q, Hq, D] and fp32
+    [tokens_q, Hq]; rows outside every sequence are left as they were. See
+    ``os_attention_fwd_packed``."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE_CODES:
+        raise TypeError("q must be a bfloat16 or float16 torch.Tensor")
+    dev = q.device
+    sq = _strides(q, "q", 3, q.dtype, dev)
+    sk = _strides(k, "k", 3, q.dtype, dev)
+    if _strides(v, "v", 3, q.dtype, dev) != sk or v.shape != k.shape:
+        raise ValueError("k and v must have the same shape and strides")
+    tokens_q, hq, d = q.shape
+    tokens_k, hkv, dk = k.shape
+    if dk != d:
+        raise ValueError("q, k and v must have the same head dimension")
+    if hkv < 1 or hq < 1 or hq % hkv:
+        raise ValueError(f"{hq} query heads cannot share {hkv} key heads")
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    _ints(cu_seqlens_q, "cu_seqlens_q", 1, dev)
+    _ints(cu_seqlens_k, "cu_seqlens_k", 1, dev)
+    batch = cu_seqlens_q.shape[0] - 1
+    if batch < 1 or cu_seqlens_k.shape[0] != batch + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have batch + 1 entries each")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = torch.empty((tokens_q, hq, d), dtype=q.dtype, device=dev) if o is None \
+        else _out(o, "o", q.dtype, (tokens_q, hq, d), dev)
+    lse = torch.empty((tokens_q, hq), dtype=torch.float32, device=dev) if lse is None \
+        else _out(lse, "lse", torch.float32, (tokens_q, hq), dev)
+    lib = load()
+    with torch.cuda.device(dev):
+        sp = _stream_ptr(stream, dev)
+        need = int(lib.os_attention_fwd_packed_workspace_bytes(batch, tokens_q, hq, hkv))
+        ws = _scratch(max(need, 16), dev, stream)
+        st = lib.os_attention_fwd_packed(
+            q.data_ptr(), sq[0], sq[1], k.data_ptr(), v.data_ptr(), sk[0], sk[1], o.data_ptr(),
+            lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), batch, tokens_q,
+            tokens_k, hq, hkv, d, _DTYPE_CODES[q.dtype], float(scale), int(bool(causal)),
+            ws.data_ptr(), ws.numel(), sp)
+    _check(st, "os_attention_fwd_packed")
+    return o, lse
+
+
+def kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                    page_table: torch.Tensor, kv_len: torch.Tensor,
+                    cu_seqlens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Copy new tokens' k and v [tokens, Hkv, D] into the pages of a cache:
+    k_pages and v_pages [pages, Hkv, page_size, D] (any strides, the same for
+    both), page_table [batch, max_pages] and kv_len [batch] int32 on the device.
+    kv_len counts the new tokens: those of sequence b, rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1, go to its last positions. cu_seqlens None: one token
+    for each sequence. See ``os_kv_cache_append``."""
+    cache = _cache(k_pages, v_pages, page_table, kv_len)
+    dev = k_pages.device
+    sk = _strides(k, "k", 3, k_pages.dtype, dev)
+    if _strides(v, "v", 3, k_pages.dtype, dev) != sk or v.shape != k.shape:
+        raise ValueError("k and v must have the same shape and strides")
+    if k.shape[1] != cache.heads or k.shape[2] != cache.head_dim:
+        raise ValueError(f"k and v must be [tokens, {cache.heads}, {cache.head_dim}] like the cache")
+    if cu_seqlens is not None:
+        _ints(cu_seqlens, "cu_seqlens", 1, dev)
+        if cu_seqlens.shape[0] != cache.batch + 1:
+            raise ValueError("cu_seqlens must have batch + 1 entries")
+    with torch.cuda.device(dev):
+        st = load().os_kv_cache_append(k.data_ptr(), v.data_ptr(), sk[0], sk[1], k.shape[0],
+                                       _ptr(cu_seqlens), ctypes.byref(cache),
+                                       _stream_ptr(stream, dev))
+    _check(st, "os_kv_cache_append")
+
+
+def _weights(weights: torch.Tensor, cache: _PagedCache, device: torch.device):
+    st = _strides(weights, "weights", 3, torch.float32, device)
+    if weights.shape[0] != cache.batch or weights.shape[1] != cache.heads \
+            or weights.shape[2] < cache.max_pages * cache.page_size:
+        raise ValueError("weights must be [batch, Hkv, n] with n >= max_pages * page_size")
+    return st
+
+
+def attention_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                           page_table: torch.Tensor, kv_len: torch.Tensor,
+                           scale: Optional[float] = None, weights: Optional[torch.Tensor] = None,
+                           o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           stream=None):
+    """Attention of one new token per sequence, q [batch, Hq, D], over a paged
+    cache (see ``kv_cache_append``; append the new token first), Hq a multiple of
+    Hkv. ``weights`` (fp32 [batch, Hkv, n], n at least what the page table's rows
+    hold) is updated in place: each cached token's attention weight, summed
+    over the query heads of its key head, is added to it. Returns ``(o, lse)``,
+    [batch, Hq, D] and fp32 [batch, Hq]. See ``os_attention_decode_paged``."""
+    cache = _cache(k_pages, v_pages, page_table, kv_len)
+    dev = k_pages.device
+    sq = _strides(q, "q", 3, k_pages.dtype, dev)
+    batch, hq, d = q.shape
+    if batch != cache.batch or d != cache.head_dim:
+        raise ValueError(f"q must be [{cache.batch}, Hq, {cache.head_dim}] like the cache")
+    if hq < 1 or hq % cache.heads:
+        raise ValueError(f"{hq} query heads cannot share {cache.heads} key heads")
+    sw = (0, 0) if weights is None else _weights(weights, cache, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = torch.empty((batch, hq, d), dtype=q.dtype, device=dev) if o is None \
+        else _out(o, "o", q.dtype, (batch, hq, d), dev)
+    lse = torch.empty((batch, hq), dtype=torch.float32, device=dev) if lse is None \
+        else _out(lse, "lse", torch.float32, (batch, hq), dev)
+    lib = load()
+    with torch.cuda.device(dev):
+        sp = _stream_ptr(stream, dev)
+        ref = ctypes.byref(cache)
+        need = int(lib.os_attention_decode_paged_workspace_bytes(hq, ref, int(weights is not None)))
+        if need < 0:
+            raise OssError(4, "os_attention_decode_paged_workspace_bytes")
+        ws = _scratch(max(need, 16), dev, stream)
+        st = lib.os_attention_decode_paged(q.data_ptr(), sq[0], sq[1], hq, ref, float(scale),
+                                           o.data_ptr(), lse.data_ptr(), _ptr(weights), sw[0], sw[1],
+                                           ws.data_ptr(), ws.numel(), sp)
+    _check(st, "os_attention_decode_paged")
+    return o, lse
+
+
+def kv_cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.Tensor,
+                   page_table: torch.Tensor, kv_len: torch.Tensor, new_page_table: torch.Tensor,
+                   budget: int, recent: int = 0, kept: Optional[torch.Tensor] = None,
+                   new_len: Optional[torch.Tensor] = None,
+                   new_weights: Optional[torch.Tensor] = None, stream=None):
+    """Keep at most ``budget`` cached tokens of each sequence and key head: the
+    last ``recent`` and, of the others, those of the largest ``weights`` (as
+    ``attention_decode_paged`` sums them). Their rows are copied, in the order
+    of their positions, to the pages that new_page_table [batch, new_max_pages]
+    names in the same pools, which nothing else may use; the old pages are only
+    read. Returns ``(kept, new_len, new_weights)``: the kept positions [batch,
+    Hkv, budget] (-1 behind the last), the new kv_len and the kept tokens'
+    weights [batch, Hkv, new_max_pages * page_size] (0 behind the last), ready
+    for the next decode. See ``os_kv_cache_evict``."""
+    cache = _cache(k_pages, v_pages, page_table, kv_len)
+    dev = k_pages.device
+    sw = _weights(weights, cache, dev)
+    _ints(new_page_table, "new_page_table", 2, dev)
+    batch, new_max = new_page_table.shape
+    if batch != cache.batch:
+        raise ValueError("new_page_table must have one row for each row of page_table")
+    budget, recent = int(budget), int(recent)
+    room = new_max * cache.page_size
+    if not 1 <= budget <= room:
+        raise ValueError(f"budget {budget} outside 1 .. {room}, what the new pages hold")
+    if not 0 <= recent <= budget:
+        raise ValueError(f"recent {recent} outside 0 .. budget")
+    kept = torch.empty((batch, cache.heads, budget), dtype=torch.int32, device=dev) if kept is None \
+        else _out(kept, "kept", torch.int32, (batch, cache.heads, budget), dev)
+    new_len = torch.empty(batch, dtype=torch.int32, device=dev) if new_len is None \
+        else _out(new_len, "new_len", torch.int32, (batch,), dev)
+    new_weights = torch.empty((batch, cache.heads, room), dtype=torch.float32, device=dev) \
+        if new_weights is None \
+        else _out(new_weights, "new_weights", torch.float32, (batch, cache.heads, room), dev)
+    with torch.cuda.device(dev):
+        st = load().os_kv_cache_evict(ctypes.byref(cache), weights.data_ptr(), sw[0], sw[1],
+                                      new_page_table.data_ptr(),
+                                      new_page_table.stride(0) if batch > 1 else 0, new_max, budget,
+                                      recent, kept.data_ptr(), new_len.data_ptr(),
+                                      new_weights.data_ptr(), _stream_ptr(stream, dev))
+    _check(st, "os_kv_cache_evict")
+    return kept, new_len, new_weights
 
 
 RESCALE_POLICIES = {"threshold": 0, "on_rise": 1, "always": 2}

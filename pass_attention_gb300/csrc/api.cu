@@ -55,6 +55,27 @@ thread_local oss::AttnFault t_fault;
 // Armed by os_debug_inject_fault (kind 2), consumed by the next
 // os_softmax_rows or os_softmax_rows_16bit on the same host thread.
 thread_local oss::RowsFault t_rows_fault;
+// What every call on a paged cache asks of it. The pools themselves are
+// checked by the calls that follow them.
+os_status check_cache(const os_paged_cache* c) {
+  if (!c || !c->page_table || !c->kv_len || !c->k_pages || !c->v_pages) return OS_ERR_INVALID_ARGUMENT;
+  if (c->num_pages <= 0 || c->heads <= 0 || c->page_size <= 0 || c->head_dim <= 0 || c->batch <= 0 ||
+      c->max_pages <= 0)
+    return OS_ERR_INVALID_ARGUMENT;
+  if (c->dtype != OS_DTYPE_BF16 && c->dtype != OS_DTYPE_F16) return OS_ERR_INVALID_ARGUMENT;
+  if (c->ld_page < 0 || c->ld_head < 0 || c->ld_slot < 0 || c->ld_table < 0) return OS_ERR_INVALID_ARGUMENT;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || ((c->ld_page | c->ld_head | c->ld_slot) & 7))
+    return OS_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(c->page_table) | reinterpret_cast<uintptr_t>(c->kv_len)) & 3u)
+    return OS_ERR_MISALIGNED;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return OS_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return OS_ERR_UNSUPPORTED;
+  if (c->batch > 65535 || c->heads > 65535 || static_cast<int64_t>(c->max_pages) * c->page_size > (int64_t(1) << 30))
+    return OS_ERR_UNSUPPORTED;
+  return OS_OK;
+}
+
 // Set by os_attention_set_rescale_policy; kept for the host thread's later
 // attention calls.
 thread_local int t_rescale_policy = OS_RESCALE_THRESHOLD;
@@ -137,6 +158,7 @@ const char* os_status_string(os_status status) {
     case OS_ERR_UNSUPPORTED: return "OS_ERR_UNSUPPORTED";
     case OS_ERR_CUDA: return "OS_ERR_CUDA";
     case OS_ERR_TIMEOUT: return "OS_ERR_TIMEOUT";
+    case OS_ERR_BAD_INDEX: return "OS_ERR_BAD_INDEX";
   }
   return "OS_ERR_UNKNOWN";
 }
@@ -347,6 +369,119 @@ os_status os_merge_partials(const float* part_m, const float* part_l, const floa
                                               static_cast<cudaStream_t>(stream)));
 }
 
+os_status os_kv_cache_append(const void* k, const void* v, int64_t ld_token, int64_t ld_head,
+                             int64_t tokens, const int32_t* cu_seqlens, const os_paged_cache* cache,
+                             void* stream) {
+  const os_status st = check_cache(cache);
+  if (st != OS_OK) return st;
+  if (tokens < 0 || ld_token < 0 || ld_head < 0 || (!cu_seqlens && tokens != cache->batch))
+    return OS_ERR_INVALID_ARGUMENT;
+  if (tokens == 0) return OS_OK;
+  if (!k || !v) return OS_ERR_INVALID_ARGUMENT;
+  if (tokens > 0x7fffffff) return OS_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || ((ld_token | ld_head) & 7)) return OS_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) return OS_ERR_MISALIGNED;
+  unsigned int* err = error_word();
+  if (!err) return OS_ERR_CUDA;
+  return from_cuda(oss::launch_kv_append(static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+                                         ld_token, ld_head, tokens, cu_seqlens, *cache, err,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int64_t os_attention_decode_paged_workspace_bytes(int32_t H, const os_paged_cache* cache, int weights) {
+  if (!cache || cache->heads <= 0 || H <= 0 || H % cache->heads) return 0;
+  if (cache->batch <= 0 || cache->batch > 65535 || cache->max_pages <= 0 || cache->page_size <= 0 ||
+      static_cast<int64_t>(cache->max_pages) * cache->page_size > (int64_t(1) << 30))
+    return 0;
+  if (cache->head_dim != 64 && cache->head_dim != 128) return 0;
+  return oss::decode_paged_workspace_bytes(H, *cache, weights != 0);
+}
+
+os_status os_attention_decode_paged(const void* q, int64_t ld_q_batch, int64_t ld_q_head, int32_t H,
+                                    const os_paged_cache* cache, float scale, void* o, float* lse,
+                                    float* weights, int64_t ld_w_batch, int64_t ld_w_head,
+                                    void* workspace, int64_t workspace_bytes, void* stream) {
+  const os_status st = check_cache(cache);
+  if (st != OS_OK) return st;
+  if (!q || !o || !workspace || H <= 0 || H % cache->heads || !valid_scale(scale)) return OS_ERR_INVALID_ARGUMENT;
+  if (ld_q_batch < 0 || ld_q_head < 0) return OS_ERR_INVALID_ARGUMENT;
+  if (weights && (ld_w_batch < 0 || ld_w_head < 0)) return OS_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || ((ld_q_batch | ld_q_head) & 7))
+    return OS_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(weights)) & 3u) return OS_ERR_MISALIGNED;
+  if (H > 65535) return OS_ERR_UNSUPPORTED;
+  const int64_t need = oss::decode_paged_workspace_bytes(H, *cache, weights != nullptr);
+  if (need < 0) return OS_ERR_CUDA;
+  if (workspace_bytes < need) return OS_ERR_INVALID_ARGUMENT;
+  unsigned int* err = error_word();
+  if (!err) return OS_ERR_CUDA;
+  return from_cuda(oss::launch_decode_paged(static_cast<const uint16_t*>(q), ld_q_batch, ld_q_head, H, *cache,
+                                            scale, static_cast<uint16_t*>(o), lse, weights, ld_w_batch,
+                                            ld_w_head, workspace, err, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t os_attention_fwd_packed_workspace_bytes(int32_t batch, int64_t tokens_q, int32_t Hq, int32_t Hkv) {
+  if (batch <= 0 || batch > 65535 || tokens_q < 0 || tokens_q > 0x7fffffff || Hq <= 0 || Hkv <= 0 || Hq % Hkv)
+    return 0;
+  return oss::attn_packed_workspace_bytes(batch, tokens_q, Hq, Hkv);
+}
+
+os_status os_attention_fwd_packed(const void* q, int64_t ld_q_token, int64_t ld_q_head, const void* k,
+                                  const void* v, int64_t ld_kv_token, int64_t ld_kv_head, void* o,
+                                  float* lse, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                  int32_t batch, int64_t tokens_q, int64_t tokens_k, int32_t Hq, int32_t Hkv,
+                                  int32_t D, int32_t dtype, float scale, int causal, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+  if (!cu_seqlens_q || !cu_seqlens_k || batch <= 0 || tokens_q < 0 || tokens_k < 0 || Hq <= 0 || Hkv <= 0 ||
+      Hq % Hkv || D <= 0 || !valid_scale(scale))
+    return OS_ERR_INVALID_ARGUMENT;
+  if (dtype != OS_DTYPE_BF16 && dtype != OS_DTYPE_F16) return OS_ERR_INVALID_ARGUMENT;
+  if (ld_q_token < 0 || ld_q_head < 0 || ld_kv_token < 0 || ld_kv_head < 0) return OS_ERR_INVALID_ARGUMENT;
+  if (D != 64 && D != 128) return OS_ERR_UNSUPPORTED;
+  if (batch > 65535 || Hq > 65535 || tokens_q > 0x7fffffff || tokens_k > 0x7fffffff) return OS_ERR_UNSUPPORTED;
+  if (tokens_q == 0) return OS_OK;
+  if (!q || !o || !workspace || (tokens_k > 0 && (!k || !v))) return OS_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(workspace) ||
+      ((ld_q_token | ld_q_head | ld_kv_token | ld_kv_head) & 7))
+    return OS_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_seqlens_q) |
+       reinterpret_cast<uintptr_t>(cu_seqlens_k)) & 3u)
+    return OS_ERR_MISALIGNED;
+  if (workspace_bytes < oss::attn_packed_workspace_bytes(batch, tokens_q, Hq, Hkv)) return OS_ERR_INVALID_ARGUMENT;
+  unsigned int* err = error_word();
+  if (!err) return OS_ERR_CUDA;
+  const oss::PackedArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                          static_cast<const uint16_t*>(v), ld_q_token, ld_q_head, ld_kv_token, ld_kv_head,
+                          static_cast<uint16_t*>(o), lse, cu_seqlens_q, cu_seqlens_k, batch, tokens_q,
+                          tokens_k, Hq, Hkv, D, dtype == OS_DTYPE_F16, scale, causal != 0};
+  const oss::AttnFault fault = t_fault;
+  t_fault = oss::AttnFault();
+  return from_cuda(oss::launch_attn_packed(a, workspace, err, fault, static_cast<cudaStream_t>(stream)));
+}
+
+os_status os_kv_cache_evict(const os_paged_cache* cache, const float* weights, int64_t ld_w_batch,
+                            int64_t ld_w_head, const int32_t* new_table, int64_t ld_new_table,
+                            int32_t new_max_pages, int32_t budget, int32_t recent, int32_t* kept,
+                            int32_t* new_len, float* new_weights, void* stream) {
+  const os_status st = check_cache(cache);
+  if (st != OS_OK) return st;
+  if (!weights || !new_table || !kept || !new_len || !new_weights) return OS_ERR_INVALID_ARGUMENT;
+  if (ld_w_batch < 0 || ld_w_head < 0 || ld_new_table < 0 || new_max_pages <= 0) return OS_ERR_INVALID_ARGUMENT;
+  if (budget <= 0 || recent < 0 || recent > budget) return OS_ERR_INVALID_ARGUMENT;
+  const int64_t room = static_cast<int64_t>(new_max_pages) * cache->page_size;
+  if (budget > room) return OS_ERR_INVALID_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(new_table) |
+       reinterpret_cast<uintptr_t>(kept) | reinterpret_cast<uintptr_t>(new_len) |
+       reinterpret_cast<uintptr_t>(new_weights)) & 3u)
+    return OS_ERR_MISALIGNED;
+  if (room > (int64_t(1) << 30)) return OS_ERR_UNSUPPORTED;
+  unsigned int* err = error_word();
+  if (!err) return OS_ERR_CUDA;
+  return from_cuda(oss::launch_kv_evict(*cache, weights, ld_w_batch, ld_w_head, new_table, ld_new_table,
+                                        new_max_pages, budget, recent, kept, new_len, new_weights, err,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
 os_status os_attention_set_rescale_policy(int32_t policy) {
   if (policy != OS_RESCALE_THRESHOLD && policy != OS_RESCALE_ON_RISE && policy != OS_RESCALE_ALWAYS)
     return OS_ERR_INVALID_ARGUMENT;
@@ -382,7 +517,8 @@ os_status os_check_device_error(void* stream, int32_t* code) {
   if (cudaMemsetAsync(err, 0, sizeof(word), s) != cudaSuccess) return OS_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return OS_ERR_CUDA;
   if (code) *code = static_cast<int32_t>(word);
-  return word ? OS_ERR_TIMEOUT : OS_OK;
+  if (!word) return OS_OK;
+  return (word & 0xffu) == oss::kKernelPaged ? OS_ERR_BAD_INDEX : OS_ERR_TIMEOUT;
 }
 
 }  // extern "C"

@@ -5,10 +5,15 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "../../include/oss.h"
+#include "paged.h"
+
 namespace oss {
 
 // Kernel ids stored in bits 0..7 of the device error word.
-enum KernelId : unsigned int { kKernelAttnFwd = 1, kKernelSoftmaxRows = 2 };
+enum KernelId : unsigned int {
+  kKernelAttnFwd = 1, kKernelSoftmaxRows = 2, kKernelPaged = 3, kKernelAttnPacked = 4
+};
 
 // Test hook for the bounded wait of the cluster-resident row kernel (see
 // os_debug_inject_fault): extra_tx > 0 makes each CTA expect that many bytes
@@ -94,6 +99,48 @@ int64_t attention_workspace_bytes(int B, int H, int Sq, int Sk, bool causal);
 // Bytes of per-tile counters at the end of that workspace (*bytes; 0 when it
 // uses none). Returns -1 when the device could not be queried, else 0.
 int64_t attention_workspace_counters(int B, int H, int Sq, int Sk, bool causal, int64_t* bytes);
+
+// The pools and tables of a validated os_paged_cache, for kernels.
+PagedCache paged_cache(const os_paged_cache& c);
+
+cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t ld_token, int64_t ld_head,
+                             int64_t tokens, const int32_t* cu, const os_paged_cache& cache,
+                             unsigned int* err, cudaStream_t stream);
+
+cudaError_t launch_kv_evict(const os_paged_cache& cache, const float* weights, int64_t ld_w_batch,
+                            int64_t ld_w_head, const int32_t* new_table, int64_t ld_new_table,
+                            int32_t new_max_pages, int32_t budget, int32_t recent, int32_t* kept,
+                            int32_t* new_len, float* new_weights, unsigned int* err,
+                            cudaStream_t stream);
+
+// Workspace of the paged decode on the current device (-1: it could not be
+// queried).
+int64_t decode_paged_workspace_bytes(int H, const os_paged_cache& cache, bool weights);
+
+cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
+                                const os_paged_cache& cache, float scale, uint16_t* o, float* lse,
+                                float* weights, int64_t ld_w_batch, int64_t ld_w_head,
+                                void* workspace, unsigned int* err, cudaStream_t stream);
+
+// Arguments of the packed attention forward, as os_attention_fwd_packed's.
+struct PackedArgs {
+  const uint16_t *q, *k, *v;
+  int64_t ld_q_token, ld_q_head, ld_kv_token, ld_kv_head;
+  uint16_t* o;
+  float* lse;
+  const int32_t *cu_q, *cu_k;
+  int32_t batch;
+  int64_t tokens_q, tokens_k;
+  int32_t Hq, Hkv, D;
+  bool f16;
+  float scale;
+  bool causal;
+};
+
+int64_t attn_packed_workspace_bytes(int batch, int64_t tokens_q, int Hq, int Hkv);
+
+cudaError_t launch_attn_packed(const PackedArgs& args, void* workspace, unsigned int* err,
+                               const AttnFault& fault, cudaStream_t stream);
 
 // log2(e) split into a float and the float nearest to the remainder, so that
 // hi + lo carries about 48 bits of it.
