@@ -601,7 +601,8 @@ OSS_API int64_t os_attention_decode_paged_workspace_bytes(int32_t H, const os_pa
  *   workspace  at least os_attention_fwd_packed_workspace_bytes bytes,
  *        16-byte aligned; no initialising, nothing kept between calls, one for
  *        each call that may run at the same time.
- * Alignment: q, k, v, o 16-byte aligned, strides multiples of 8.
+ * Alignment: q, k, v, o 16-byte aligned, strides multiples of 8, and positive
+ * where the dimension is longer than 1.
  * Errors: OS_ERR_INVALID_ARGUMENT, OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED,
  * OS_ERR_CUDA; a timed-out internal wait is reported by os_check_device_error.
  * tokens_q == 0 is OS_OK and launches nothing.
@@ -615,10 +616,11 @@ OSS_API os_status os_attention_fwd_packed(const void* q, int64_t ld_q_token, int
                                           float scale, int causal, void* workspace,
                                           int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that os_attention_fwd_packed uses; 0 for arguments that
- * the call refuses. */
-OSS_API int64_t os_attention_fwd_packed_workspace_bytes(int32_t batch, int64_t tokens_q, int32_t Hq,
-                                                        int32_t Hkv);
+/* Bytes of workspace that os_attention_fwd_packed uses on the current device
+ * (about 21 MB for D 128, times the rounds in which a launch takes its work: 1 up
+ * to 64 MB of K and V, at most 8); -1 when the device cannot be queried, 0 for
+ * arguments that the call refuses. */
+OSS_API int64_t os_attention_fwd_packed_workspace_bytes(int64_t tokens_k, int32_t Hkv, int32_t D);
 
 /*
  * os_kv_cache_evict -- keep the cached tokens that have received the most

@@ -107,7 +107,7 @@ _SIGNATURES = {
     "os_attention_fwd_packed": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32,
                                        _i64, _i64, _i32, _i32, _i32, _i32, _f32, ctypes.c_int, _vp,
                                        _i64, _vp]),
-    "os_attention_fwd_packed_workspace_bytes": (_i64, [_i32, _i64, _i32, _i32]),
+    "os_attention_fwd_packed_workspace_bytes": (_i64, [_i64, _i32, _i32]),
     "os_kv_cache_append": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _cache_p, _vp]),
     "os_attention_decode_paged": (_i32, [_vp, _i64, _i64, _i32, _cache_p, _f32, _vp, _vp, _vp, _i64,
                                          _i64, _vp, _i64, _vp]),
@@ -696,7 +696,9 @@ def attention_fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     lib = load()
     with torch.cuda.device(dev):
         sp = _stream_ptr(stream, dev)
-        need = int(lib.os_attention_fwd_packed_workspace_bytes(batch, tokens_q, hq, hkv))
+        need = int(lib.os_attention_fwd_packed_workspace_bytes(tokens_k, hkv, d))
+        if need < 0:
+            raise OssError(4, "os_attention_fwd_packed_workspace_bytes")
         ws = _scratch(max(need, 16), dev, stream)
         st = lib.os_attention_fwd_packed(
             q.data_ptr(), sq[0], sq[1], k.data_ptr(), v.data_ptr(), sk[0], sk[1], o.data_ptr(),

@@ -420,10 +420,9 @@ os_status os_attention_decode_paged(const void* q, int64_t ld_q_batch, int64_t l
                                             ld_w_head, workspace, err, static_cast<cudaStream_t>(stream)));
 }
 
-int64_t os_attention_fwd_packed_workspace_bytes(int32_t batch, int64_t tokens_q, int32_t Hq, int32_t Hkv) {
-  if (batch <= 0 || batch > 65535 || tokens_q < 0 || tokens_q > 0x7fffffff || Hq <= 0 || Hkv <= 0 || Hq % Hkv)
-    return 0;
-  return oss::attn_packed_workspace_bytes(batch, tokens_q, Hq, Hkv);
+int64_t os_attention_fwd_packed_workspace_bytes(int64_t tokens_k, int32_t Hkv, int32_t D) {
+  if (tokens_k < 0 || tokens_k > 0x7fffffff || Hkv <= 0 || Hkv > 65535 || (D != 64 && D != 128)) return 0;
+  return oss::attn_packed_workspace_bytes(tokens_k, Hkv, D);
 }
 
 os_status os_attention_fwd_packed(const void* q, int64_t ld_q_token, int64_t ld_q_head, const void* k,
@@ -436,7 +435,9 @@ os_status os_attention_fwd_packed(const void* q, int64_t ld_q_token, int64_t ld_
       Hq % Hkv || D <= 0 || !valid_scale(scale))
     return OS_ERR_INVALID_ARGUMENT;
   if (dtype != OS_DTYPE_BF16 && dtype != OS_DTYPE_F16) return OS_ERR_INVALID_ARGUMENT;
-  if (ld_q_token < 0 || ld_q_head < 0 || ld_kv_token < 0 || ld_kv_head < 0) return OS_ERR_INVALID_ARGUMENT;
+  // a tensor map wants a positive stride for a dimension that is walked
+  if (ld_q_token < (tokens_q > 1) || ld_q_head < (Hq > 1) || ld_kv_token < (tokens_k > 1) || ld_kv_head < (Hkv > 1))
+    return OS_ERR_INVALID_ARGUMENT;
   if (D != 64 && D != 128) return OS_ERR_UNSUPPORTED;
   if (batch > 65535 || Hq > 65535 || tokens_q > 0x7fffffff || tokens_k > 0x7fffffff) return OS_ERR_UNSUPPORTED;
   if (tokens_q == 0) return OS_OK;
@@ -447,7 +448,9 @@ os_status os_attention_fwd_packed(const void* q, int64_t ld_q_token, int64_t ld_
   if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_seqlens_q) |
        reinterpret_cast<uintptr_t>(cu_seqlens_k)) & 3u)
     return OS_ERR_MISALIGNED;
-  if (workspace_bytes < oss::attn_packed_workspace_bytes(batch, tokens_q, Hq, Hkv)) return OS_ERR_INVALID_ARGUMENT;
+  const int64_t need = oss::attn_packed_workspace_bytes(tokens_k, Hkv, D);
+  if (need < 0) return OS_ERR_CUDA;
+  if (workspace_bytes < need) return OS_ERR_INVALID_ARGUMENT;
   unsigned int* err = error_word();
   if (!err) return OS_ERR_CUDA;
   const oss::PackedArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),

@@ -137,7 +137,9 @@ struct PackedArgs {
   bool causal;
 };
 
-int64_t attn_packed_workspace_bytes(int batch, int64_t tokens_q, int Hq, int Hkv);
+// Workspace of the packed attention forward on the current device (-1: it
+// could not be queried).
+int64_t attn_packed_workspace_bytes(int64_t tokens_k, int Hkv, int D);
 
 cudaError_t launch_attn_packed(const PackedArgs& args, void* workspace, unsigned int* err,
                                const AttnFault& fault, cudaStream_t stream);

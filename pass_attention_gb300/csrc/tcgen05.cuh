@@ -1,0 +1,274 @@
+// PTX wrappers shared by the attention kernels that run on the tcgen05 tensor
+// cores: mbarriers and their bounded waits, TMA loads, MMAs, tensor-memory
+// access, and the operand descriptors.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "device_common.cuh"
+#include "oss_internal.h"
+
+namespace oss {
+
+constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
+constexpr uint64_t kDrainNs = 200000000ull;     // 0.2 s to drain own copies
+
+// wait sites (error word bits 8..15)
+enum Site : unsigned int {
+  kSiteQFull = 1, kSiteKFull, kSiteVFull, kSiteKEmpty, kSiteVEmpty,
+  kSiteSFull, kSitePReady, kSiteODone, kSiteDrain, kSiteQEmpty, kSiteOFree
+};
+
+// ---------------------------------------------------------------------------
+// PTX wrappers
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ uint64_t global_timer() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Non-blocking test of a phase.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait, slow path: polls until the phase completes, another thread
+// aborts, or the time limit passes (then it raises the abort flag and
+// records the site). Kept out of line; the fast path below is inlined
+// because every wait sits on the pipeline's critical path (measured: an
+// out-of-line call costs the caller a few hundred cycles).
+// A give-up is recorded in the device error word together with the launch's
+// tag (bits 16..31); the other CTAs of the same launch see the tag on their
+// next slow-path poll and give up too, so a failed launch ends after one
+// timeout instead of one per wave of CTAs.
+template <unsigned int kKernel>
+__device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           unsigned int* err, unsigned int site,
+                                           uint64_t timeout_ns, unsigned int tag) {
+  const uint64_t t0 = global_timer();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if ((n & 63u) == 0) {
+      const unsigned int e = *reinterpret_cast<volatile unsigned int*>(err);
+      if (e != 0 && (e >> 16) == tag) {
+        *abort_flag = 1;
+        return false;
+      }
+      if (global_timer() - t0 > timeout_ns) {
+        *abort_flag = 1;
+        report_error(err, kKernel | (site << 8) | (tag << 16));
+        return false;
+      }
+    }
+  }
+}
+
+// Bounded wait used while draining: ignores the abort flag.
+template <unsigned int kKernel>
+__device__ __noinline__ bool drain_bar(uint32_t bar, uint32_t parity, unsigned int* err) {
+  const uint64_t t0 = global_timer();
+  for (uint32_t n = 0;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63u) == 0 && global_timer() - t0 > kDrainNs) {
+      report_error(err, kKernel | (kSiteDrain << 8));
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#define OSS_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), \
+                  "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define OSS_W8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), \
+                  "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+#define OSS_RW8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), \
+                   "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+
+// Completes outstanding tcgen05.ld of this thread; the register operands tie
+// the loaded values to the wait so no use is scheduled before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("" : OSS_RW8(0), OSS_RW8(8), OSS_RW8(16), OSS_RW8(24));
+}
+
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 16 lanes x 64 columns (shape 16x256b, 8 repetitions). Thread t holds, for
+// repetition k, columns 8k + 2(t%4) and 8k + 2(t%4) + 1 of lane t/4 in
+// r[4k], r[4k+1] and of lane 8 + t/4 in r[4k+2], r[4k+3].
+__device__ __forceinline__ void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : OSS_R8(0), OSS_R8(8), OSS_R8(16), OSS_R8(24)
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st16x256_x8(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      OSS_W8(0), OSS_W8(8), OSS_W8(16), OSS_W8(24)
+      : "memory");
+}
+
+// 16 lanes x 32 columns (shape 16x128b, 8 repetitions). Thread t writes,
+// for repetition k, column 4k + t%4 of lane t/4 from r[2k] and of lane
+// 8 + t/4 from r[2k+1].
+__device__ __forceinline__ void tmem_st16x128_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      OSS_W8(0), OSS_W8(8)
+      : "memory");
+}
+
+// max(a, b, c) in one instruction (three-input max.f32, sm_100 and later)
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 4 x 4 transpose of 32-bit words among the four lanes 4q .. 4q + 3 of a
+// warp (j = lane % 4): lane j gives a[i] = element (j, i) and gets back
+// a[i] = element (i, j). Two exchange rounds, at lane distance 1 and 2.
+__device__ __forceinline__ void lane_transpose4(uint32_t (&a)[4], int j) {
+  const bool o1 = (j & 1) != 0;
+  uint32_t x = o1 ? a[0] : a[1];
+  uint32_t y = o1 ? a[2] : a[3];
+  x = __shfl_xor_sync(0xffffffffu, x, 1);
+  y = __shfl_xor_sync(0xffffffffu, y, 1);
+  if (o1) { a[0] = x; a[2] = y; } else { a[1] = x; a[3] = y; }
+  const bool o2 = (j & 2) != 0;
+  x = o2 ? a[0] : a[2];
+  y = o2 ? a[1] : a[3];
+  x = __shfl_xor_sync(0xffffffffu, x, 2);
+  y = __shfl_xor_sync(0xffffffffu, y, 2);
+  if (o2) { a[0] = x; a[1] = y; } else { a[2] = x; a[3] = y; }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
+// ---------------------------------------------------------------------------
+// Descriptors
+// ---------------------------------------------------------------------------
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start address, leading
+// and stride byte offsets (16-byte units), the fixed 0b001 field at bit 46,
+// swizzle mode 2 at bits 61..63.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) |
+         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// Instruction descriptor, kind::f16: fp32 accumulator (bits 4-5 = 1), A and B
+// bf16 (bits 7-9 = 1, 10-12 = 1) or both fp16 (0), A K-major, B K-major (bit
+// 16 = 0) or N-major (bit 16 = 1), N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+constexpr uint32_t make_idesc(uint32_t M, uint32_t N, bool b_mn_major, bool f16 = false) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+// A 16-element step along K of a K-major operand moves 32 bytes inside the
+// 128-byte swizzled row (the first four steps), then to the second half.
+__device__ __forceinline__ uint64_t kstep_kmajor(int kk, int half_bytes) {
+  return static_cast<uint64_t>((kk >> 2) * (half_bytes >> 4) + (kk & 3) * 2);
+}
+
+}  // namespace oss

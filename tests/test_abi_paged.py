@@ -101,7 +101,8 @@ def test_packed_rejects_bad_arguments(lib):
                                            dtype, scale, 1, ws, nbytes, None)
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(cq=None), dict(ck=None), dict(batch=0), dict(tq=-1),
                 dict(tk=-1), dict(Hq=0), dict(Hkv=0), dict(Hq=5), dict(D=0), dict(dtype=0), dict(dtype=3), dict(scale=0.0),
-                dict(scale=float("inf")), dict(ws=None), dict(nbytes=0), dict(ldq=(-8, 128)), dict(ldk=(256, -8))):
+                dict(scale=float("inf")), dict(ws=None), dict(ldq=(-8, 128)), dict(ldk=(256, -8)), dict(ldq=(0, 128)),
+                dict(ldq=(512, 0)), dict(ldk=(0, 128)), dict(ldk=(256, 0))):
         assert call(**bad) == INVALID, bad
     for bad in (dict(q=A + 8), dict(k=A + 2), dict(o=A + 4), dict(ws=A + 8), dict(ldq=(516, 128)), dict(ldk=(256, 4)),
                 dict(cq=A + 2), dict(lse=A + 1)):
@@ -109,8 +110,9 @@ def test_packed_rejects_bad_arguments(lib):
     for bad in (dict(D=32), dict(D=256), dict(batch=65536), dict(tq=2 ** 31), dict(tk=2 ** 31)):
         assert call(**bad) == UNSUPPORTED, bad
     assert call(tq=0, q=None, o=None) == 0
-    assert lib.os_attention_fwd_packed_workspace_bytes(2, 20, 5, 2) == 0
-    assert lib.os_attention_fwd_packed_workspace_bytes(2, 20, 4, 2) > 0
+    assert lib.os_attention_fwd_packed_workspace_bytes(20, 2, 96) == 0
+    assert lib.os_attention_fwd_packed_workspace_bytes(-1, 2, 128) == 0
+    assert lib.os_attention_fwd_packed_workspace_bytes(20, 0, 128) == 0
 
 
 def test_evict_rejects_bad_arguments(lib):
@@ -228,3 +230,96 @@ def test_weight_order(probe):
     assert key == sorted(key, reverse=True) and len(set(key)) == len(key)
     zero, minus, nan = probe([f"w {0}", f"w {0x80000000}", f"w {0xffc00000}"])
     assert zero == minus and int(nan) == key[0]
+
+
+PLAN = r"""
+#include <cassert>
+#include <cstdio>
+#include <cstdlib>
+#include <utility>
+#include <vector>
+#include "packed_plan.h"
+using namespace oss;
+// Random sequences: the closed forms against sums tile by tile, and the shares
+// against a walk over all items.
+int main() {
+  srand(1);
+  for (int it = 0; it < 3000; ++it) {
+    const int ps = rand() % 8, B = 1 + rand() % 12, packs = 1 + rand() % 6, ctas = rand() % 2 ? 152 : 1 + rand() % 40;
+    const int rounds = 1 + rand() % 4;
+    const bool causal = rand() % 4 != 0;
+    std::vector<PackedSeq> seqs;
+    int64_t total = 0, items = 0;
+    for (int b = 0; b < B; ++b) {
+      const int ql = rand() % 4 == 0 ? 0 : rand() % (1 << (rand() % 11 + 1));
+      const int kl = rand() % 3 == 0 ? rand() % 2000 : ql + (rand() % 2 ? rand() % 3000 : 0);
+      const PackedSeq s = packed_seq(row_range(0, ql, 1 << 30), row_range(0, kl, 1 << 30), ps);
+      int64_t sum = 0;
+      for (int t = 0; t < s.tiles; ++t) {
+        int last = ((t + 1) << ps) - 1;
+        if (last >= ql) last = ql - 1;
+        int vis = causal ? last + 1 + kl - ql : kl;
+        if (vis > kl) vis = kl;
+        const int want = vis > 0 ? (vis + 127) / 128 : 1;
+        assert(kv_tiles(s, t, ps, causal) == want);
+        assert(length_before(s, t, ps, causal) == sum);
+        assert(tile_at(s, sum, ps, causal) == t && tile_at(s, sum + want + kTileWeight - 1, ps, causal) == t);
+        sum += want + kTileWeight;
+      }
+      assert(length_before(s, s.tiles, ps, causal) == sum);
+      seqs.push_back(s);
+      total += sum * packs;
+      items += static_cast<int64_t>(s.tiles) * packs;
+    }
+    if (!items) continue;
+    const int n = share_count(total, items, ctas, rounds);
+    assert(n >= 1 && n <= ctas * rounds && n <= total && (n <= ctas || n % ctas == 0));
+    struct Item { int64_t w; int steps; };
+    std::vector<Item> all;
+    int64_t w = 0;
+    for (auto& s : seqs)
+      for (int p = 0; p < packs; ++p)
+        for (int t = 0; t < s.tiles; ++t) {
+          all.push_back({w, kv_tiles(s, t, ps, causal)});
+          w += all.back().steps + kTileWeight;
+        }
+    // every share's beginning as (item, step); the last one is the end
+    std::vector<std::pair<int, int>> at;
+    size_t i = 0;
+    for (int c = 0; c < n; ++c) {
+      const int64_t x = share_begin(c, total, n);
+      while (i + 1 < all.size() && all[i + 1].w <= x) ++i;
+      const int st = cut_step(x - all[i].w, all[i].steps);
+      at.push_back(st == all[i].steps ? std::make_pair(static_cast<int>(i) + 1, 0) : std::make_pair(static_cast<int>(i), st));
+    }
+    at.push_back({static_cast<int>(all.size()), 0});
+    assert(share_begin(n, total, n) == total);
+    assert(at[0].first == 0 && at[0].second == 0);
+    for (int c = 0; c < n; ++c) {
+      assert(at[c] <= at[c + 1]);
+      const auto e = at[c + 1];
+      if (e.second == 0) continue;
+      assert(e.second >= kMinSteps && all[e.first].steps - e.second >= kMinSteps);
+      if (at[c].first == e.first && at[c].second > 0) continue;
+      // the item begins in share c and is cut at its end: its parts
+      const int64_t last = last_boundary(all[e.first].w + kTileWeight + all[e.first].steps - kMinSteps, total, n);
+      int parts = 1;
+      for (int d = c + 1; d < n; ++d) parts += at[d].first == e.first && at[d].second > 0;
+      assert(parts == last - c + 1);
+      for (int d = c + 1; d <= last; ++d) assert(at[d].first == e.first && at[d].second > 0 && at[d] < at[d + 1]);
+    }
+  }
+  std::puts("ok");
+}
+"""
+
+
+def test_packed_plan(tmp_path):
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not installed")
+    (tmp_path / "plan.cpp").write_text(PLAN)
+    exe = str(tmp_path / "plan")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", CSRC,
+                    str(tmp_path / "plan.cpp"), "-o", exe], check=True, capture_output=True, text=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout == "ok\n", r.stdout + r.stderr

@@ -117,11 +117,10 @@ def test_views_of_a_fused_projection():
     q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
     o, lse = oss.attention_fwd_packed(q, k, v, offsets(lens), scale=0.05)
     check_packed(o, lse, q, k, v, lens, lens, 0.05, True)
-    # head-major storage, and heads that share storage
-    t = rand(2, 4, 233, 128).transpose(0, 1)
-    one = rand(3, 233, 1, 128).expand(233, 2, 128)
-    o, lse = oss.attention_fwd_packed(t, one, one, offsets(lens))
-    check_packed(o, lse, t, one, one, lens, lens, 1 / math.sqrt(128), True)
+    # head-major storage
+    t, kv = rand(2, 4, 233, 128).transpose(0, 1), rand(3, 2, 233, 128).transpose(0, 1)
+    o, lse = oss.attention_fwd_packed(t, kv, kv, offsets(lens))
+    check_packed(o, lse, t, kv, kv, lens, lens, 1 / math.sqrt(128), True)
 
 
 def test_same_bits_every_time_and_beside_other_calls():
@@ -193,6 +192,35 @@ def test_refusals():
         call(q=q[..., :32], k=k[..., :32], v=k[..., :32])
     with pytest.raises(oss.OssError, match="INVALID"):
         call(scale=-1.0)
+    with pytest.raises(oss.OssError, match="INVALID"):
+        call(k=k[:, :1].expand(20, 2, 128), v=k[:, :1].expand(20, 2, 128))
     with pytest.raises(oss.OssError, match="MISALIGNED"):
         call(q=torch.zeros(20, 4, 132, dtype=q.dtype, device="cuda")[..., :128])
     assert oss.check_device_error() == 0
+
+
+def test_a_wait_that_runs_out_is_reported():
+    q, k, v = rand(1, 300, 4, 128), rand(2, 300, 1, 128), rand(3, 300, 1, 128)
+    cu = offsets([300])
+    oss.debug_inject_fault(1, step=1, timeout_ns=2_000_000)
+    oss.attention_fwd_packed(q, k, v, cu)
+    with pytest.raises(oss.OssError, match="OS_ERR_TIMEOUT"):
+        oss.check_device_error()
+    o, lse = oss.attention_fwd_packed(q, k, v, cu)
+    assert oss.check_device_error() == 0
+    check_packed(o, lse, q, k, v, [300], [300], 1 / math.sqrt(128), True)
+
+
+def test_many_rounds():
+    # more than 64 MB of K and V: shares in several rounds, a window of heads at a time
+    lens = [9000, 300]
+    q, k, v = (rand(s, sum(lens), 16, 128) for s in (1, 2, 3))
+    o, lse = oss.attention_fwd_packed(q, k, v, offsets(lens))
+    assert oss.check_device_error() == 0
+    heads = (0, 7, 15)
+    check_packed(o[9000:], lse[9000:], q[9000:], k[9000:], v[9000:], [300], [300], 1 / math.sqrt(128), True)
+    pick = torch.cat([torch.arange(40), torch.randint(40, 8900, (60,), generator=torch.Generator().manual_seed(1)),
+                      torch.arange(8940, 9000)]).cuda()
+    for i in pick.tolist():
+        check_packed(o[i:i + 1, heads], lse[i:i + 1, heads], q[i:i + 1, heads], k[:i + 1, heads], v[:i + 1, heads],
+                     [1], [i + 1], 1 / math.sqrt(128), True)
