@@ -12,9 +12,11 @@ error.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -68,16 +70,11 @@ _i64 = ctypes.c_int64
 _f32 = ctypes.c_float
 
 
-class _PagedCache(ctypes.Structure):
-    """os_paged_cache of include/oss.h."""
-
-    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("ld_page", _i64), ("ld_head", _i64),
-                ("ld_slot", _i64), ("page_table", _vp), ("ld_table", _i64), ("kv_len", _vp),
-                ("num_pages", _i32), ("heads", _i32), ("page_size", _i32), ("head_dim", _i32),
-                ("dtype", _i32), ("batch", _i32), ("max_pages", _i32)]
-
-
-_cache_p = ctypes.POINTER(_PagedCache)
+# os_paged_cache of include/oss.h, packed: k_pages, v_pages, ld_page, ld_head,
+# ld_slot, page_table, ld_table, kv_len, num_pages, heads, page_size, head_dim,
+# dtype, batch, max_pages (its bytes take the place of a pointer to it; a
+# ctypes.Structure costs a microsecond more per call)
+_PAGED_CACHE = struct.Struct("@PPqqqPqPiiiiiii")
 
 # name -> (restype, argtypes), the signatures of include/oss.h
 _SIGNATURES = {
@@ -108,11 +105,11 @@ _SIGNATURES = {
                                        _i64, _i64, _i32, _i32, _i32, _i32, _f32, ctypes.c_int, _vp,
                                        _i64, _vp]),
     "os_attention_fwd_packed_workspace_bytes": (_i64, [_i64, _i32, _i32]),
-    "os_kv_cache_append": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _cache_p, _vp]),
-    "os_attention_decode_paged": (_i32, [_vp, _i64, _i64, _i32, _cache_p, _f32, _vp, _vp, _vp, _i64,
+    "os_kv_cache_append": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "os_attention_decode_paged": (_i32, [_vp, _i64, _i64, _i32, _vp, _f32, _vp, _vp, _vp, _i64,
                                          _i64, _vp, _i64, _vp]),
-    "os_attention_decode_paged_workspace_bytes": (_i64, [_i32, _cache_p, ctypes.c_int]),
-    "os_kv_cache_evict": (_i32, [_cache_p, _vp, _i64, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
+    "os_attention_decode_paged_workspace_bytes": (_i64, [_i32, _vp, ctypes.c_int]),
+    "os_kv_cache_evict": (_i32, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
                                  _vp, _vp]),
     "os_check_device_error": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "os_attention_set_rescale_policy": (_i32, [_i32]),
@@ -594,64 +591,98 @@ def decode_from_host(q_host, k_host, v_host, kv_len_host, num_splits, scale=None
 # the paged key-value cache and packed prompts
 # ---------------------------------------------------------------------------
 
-def _strides(t: torch.Tensor, name: str, ndim: int, dtype: torch.dtype, device: torch.device):
-    """Strides of an input that may be a view: a CUDA tensor of this dtype, unit
-    stride in its last dimension, the others multiples of 8 elements (16 bytes).
-    A dimension of size 1 has no stride that matters: 0."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (liboss has no CPU path)")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+# These calls are made once per layer and token, where the host's time counts:
+# each tensor is checked in one expression, and what is wrong with it is found
+# out only when that fails.
+
+def _refuse(t, name: str, ndim: int, dtype: torch.dtype, device: torch.device) -> None:
+    """Raises what is wrong with a tensor that a quick check refused."""
+    _need(t, name, dtype, ndim)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the inputs on {device}")
+    raise ValueError(f"{name} must have unit stride in its last dimension")
+
+
+def _strides(t: torch.Tensor, name: str, ndim: int, dtype: torch.dtype, device: torch.device):
+    """Strides of an input that may be a view: a CUDA tensor of this dtype on
+    the CUDA device ``device``, with unit stride in its last dimension."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name} must have unit stride in its last dimension")
-    return tuple(0 if n == 1 else x for n, x in zip(t.shape[:-1], st))
+    if t.dtype is not dtype or len(st) != ndim or t.device != device or st[-1] != 1:
+        _refuse(t, name, ndim, dtype, device)
+    for x in st[:-1]:
+        if x & 7:
+            # a stride off the 16-byte grid matters only where it is walked
+            return tuple(0 if n == 1 else x for n, x in zip(t.shape, st))
+    return st
+
+
+def _pair(k: torch.Tensor, v: torch.Tensor, names, ndim: int, dtype: torch.dtype, device: torch.device):
+    """The strides that k and v share."""
+    sk = _strides(k, names[0], ndim, dtype, device)
+    sv = _strides(v, names[1], ndim, dtype, device)
+    if v.shape != k.shape or (sv != sk and any(n > 1 and a != b for n, a, b in zip(k.shape, sk, sv))):
+        raise ValueError(f"{names[0]} and {names[1]} must have the same shape and strides")
+    return sk
 
 
 def _ints(t: torch.Tensor, name: str, ndim: int, device: torch.device) -> None:
-    _need(t, name, torch.int32, ndim)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the inputs on {device}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have unit stride in its last dimension")
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != ndim or t.device != device \
+            or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        _refuse(t, name, ndim, torch.int32, device)
 
 
-def _cache(k_pages, v_pages, page_table, kv_len) -> _PagedCache:
-    """The os_paged_cache of these tensors (which the caller keeps alive until
-    the call has been enqueued)."""
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in _DTYPE_CODES:
-        raise TypeError("k_pages must be a bfloat16 or float16 torch.Tensor")
-    dev = k_pages.device
-    st = _strides(k_pages, "k_pages", 4, k_pages.dtype, dev)
-    if _strides(v_pages, "v_pages", 4, k_pages.dtype, dev) != st or v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must have the same shape and strides")
+def _cuda_device(t: torch.Tensor, name: str) -> torch.device:
+    """The device of a call's 16-bit tensors."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE_CODES:
+        raise TypeError(f"{name} must be a bfloat16 or float16 torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (liboss has no CPU path)")
+    return t.device
+
+
+def _cache(k_pages, v_pages, page_table, kv_len):
+    """``(os_paged_cache, device, batch, heads, head_dim, capacity, page_size)`` of
+    these tensors; capacity: the tokens that a row of the page table holds."""
+    dev = _cuda_device(k_pages, "k_pages")
+    dtype = k_pages.dtype
+    st = _pair(k_pages, v_pages, ("k_pages", "v_pages"), 4, dtype, dev)
     _ints(page_table, "page_table", 2, dev)
     _ints(kv_len, "kv_len", 1, dev)
     pages, heads, page_size, d = k_pages.shape
     batch, max_pages = page_table.shape
     if kv_len.shape[0] != batch:
         raise ValueError("kv_len must have one entry for each row of page_table")
-    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
-                       page_table.data_ptr(), page_table.stride(0) if batch > 1 else 0,
-                       kv_len.data_ptr(), pages, heads, page_size, d, _DTYPE_CODES[k_pages.dtype],
-                       batch, max_pages)
+    if max(pages, max_pages, batch) > 0x7fffffff:
+        raise ValueError("more pages than 32 bits count")
+    return (_PAGED_CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
+                              page_table.data_ptr(), page_table.stride(0), kv_len.data_ptr(), pages, heads,
+                              page_size, d, _DTYPE_CODES[dtype], batch, max_pages),
+            dev, batch, heads, d, max_pages * page_size, page_size)
 
 
-def _scratch(nbytes: int, device: torch.device, stream) -> torch.Tensor:
-    """A workspace for one call. It comes from PyTorch's allocator each time, so
-    calls on two streams or in two captured graphs never share one; on a
-    stream other than the current one its memory is held until that stream
-    has passed the call."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _on(dev: torch.device, stream):
+    """The context in which a call for tensors on ``dev`` allocates and
+    launches: the caller's stream, or the current one of that device. Outputs
+    and workspaces come from PyTorch's allocator under it, call by call, so
+    their memory is ordered with the stream that uses it, and two streams or
+    two captured graphs never share a workspace."""
     if stream is not None:
-        ws.record_stream(stream)
-    return ws
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index == torch.cuda.current_device():
+        return _HERE_ALREADY
+    return torch.cuda.device(dev)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _raw_stream(dev: torch.device) -> int:
+    """The current stream of ``dev``, without making a Stream object for it."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def attention_fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -667,13 +698,9 @@ def attention_fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     its keys' positions. Returns ``(o, lse)``, [tokens_q, Hq, D] and fp32
     [tokens_q, Hq]; rows outside every sequence are left as they were. See
     ``os_attention_fwd_packed``."""
-    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE_CODES:
-        raise TypeError("q must be a bfloat16 or float16 torch.Tensor")
-    dev = q.device
+    dev = _cuda_device(q, "q")
     sq = _strides(q, "q", 3, q.dtype, dev)
-    sk = _strides(k, "k", 3, q.dtype, dev)
-    if _strides(v, "v", 3, q.dtype, dev) != sk or v.shape != k.shape:
-        raise ValueError("k and v must have the same shape and strides")
+    sk = _pair(k, v, ("k", "v"), 3, q.dtype, dev)
     tokens_q, hq, d = q.shape
     tokens_k, hkv, dk = k.shape
     if dk != d:
@@ -689,22 +716,25 @@ def attention_fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have batch + 1 entries each")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty((tokens_q, hq, d), dtype=q.dtype, device=dev) if o is None \
-        else _out(o, "o", q.dtype, (tokens_q, hq, d), dev)
-    lse = torch.empty((tokens_q, hq), dtype=torch.float32, device=dev) if lse is None \
-        else _out(lse, "lse", torch.float32, (tokens_q, hq), dev)
+    if o is not None:
+        _out(o, "o", q.dtype, (tokens_q, hq, d), dev)
+    if lse is not None:
+        _out(lse, "lse", torch.float32, (tokens_q, hq), dev)
     lib = load()
-    with torch.cuda.device(dev):
-        sp = _stream_ptr(stream, dev)
-        need = int(lib.os_attention_fwd_packed_workspace_bytes(tokens_k, hkv, d))
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty((tokens_q, hq, d), dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((tokens_q, hq), dtype=torch.float32, device=dev)
+        need = lib.os_attention_fwd_packed_workspace_bytes(tokens_k, hkv, d)
         if need < 0:
             raise OssError(4, "os_attention_fwd_packed_workspace_bytes")
-        ws = _scratch(max(need, 16), dev, stream)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
         st = lib.os_attention_fwd_packed(
             q.data_ptr(), sq[0], sq[1], k.data_ptr(), v.data_ptr(), sk[0], sk[1], o.data_ptr(),
             lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), batch, tokens_q,
-            tokens_k, hq, hkv, d, _DTYPE_CODES[q.dtype], float(scale), int(bool(causal)),
-            ws.data_ptr(), ws.numel(), sp)
+            tokens_k, hq, hkv, d, _DTYPE_CODES[q.dtype], scale, bool(causal), ws.data_ptr(), need,
+            _raw_stream(dev))
     _check(st, "os_attention_fwd_packed")
     return o, lse
 
@@ -718,30 +748,31 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_p
     kv_len counts the new tokens: those of sequence b, rows cu_seqlens[b] ..
     cu_seqlens[b + 1] - 1, go to its last positions. cu_seqlens None: one token
     for each sequence. See ``os_kv_cache_append``."""
-    cache = _cache(k_pages, v_pages, page_table, kv_len)
-    dev = k_pages.device
-    sk = _strides(k, "k", 3, k_pages.dtype, dev)
-    if _strides(v, "v", 3, k_pages.dtype, dev) != sk or v.shape != k.shape:
-        raise ValueError("k and v must have the same shape and strides")
-    if k.shape[1] != cache.heads or k.shape[2] != cache.head_dim:
-        raise ValueError(f"k and v must be [tokens, {cache.heads}, {cache.head_dim}] like the cache")
+    cache, dev, batch, heads, d, _, _ = _cache(k_pages, v_pages, page_table, kv_len)
+    sk = _pair(k, v, ("k", "v"), 3, k_pages.dtype, dev)
+    tokens, hk, dk = k.shape
+    if hk != heads or dk != d:
+        raise ValueError(f"k and v must be [tokens, {heads}, {d}] like the cache")
+    cu = None
     if cu_seqlens is not None:
         _ints(cu_seqlens, "cu_seqlens", 1, dev)
-        if cu_seqlens.shape[0] != cache.batch + 1:
+        if cu_seqlens.shape[0] != batch + 1:
             raise ValueError("cu_seqlens must have batch + 1 entries")
-    with torch.cuda.device(dev):
-        st = load().os_kv_cache_append(k.data_ptr(), v.data_ptr(), sk[0], sk[1], k.shape[0],
-                                       _ptr(cu_seqlens), ctypes.byref(cache),
-                                       _stream_ptr(stream, dev))
+        cu = cu_seqlens.data_ptr()
+    with _on(dev, stream):
+        st = load().os_kv_cache_append(k.data_ptr(), v.data_ptr(), sk[0], sk[1], tokens, cu, cache,
+                                       _raw_stream(dev))
     _check(st, "os_kv_cache_append")
 
 
-def _weights(weights: torch.Tensor, cache: _PagedCache, device: torch.device):
-    st = _strides(weights, "weights", 3, torch.float32, device)
-    if weights.shape[0] != cache.batch or weights.shape[1] != cache.heads \
-            or weights.shape[2] < cache.max_pages * cache.page_size:
-        raise ValueError("weights must be [batch, Hkv, n] with n >= max_pages * page_size")
-    return st
+def _weights(weights: torch.Tensor, batch: int, heads: int, capacity: int, device: torch.device):
+    if not isinstance(weights, torch.Tensor) or weights.dtype is not torch.float32 or weights.dim() != 3 \
+            or weights.device != device or (weights.stride(-1) != 1 and weights.shape[-1] > 1):
+        _refuse(weights, "weights", 3, torch.float32, device)
+    b, h, n = weights.shape
+    if b != batch or h != heads or n < capacity:
+        raise ValueError(f"weights must be [{batch}, {heads}, n] with n >= max_pages * page_size")
+    return weights.stride()
 
 
 def attention_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -755,32 +786,37 @@ def attention_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     hold) is updated in place: each cached token's attention weight, summed
     over the query heads of its key head, is added to it. Returns ``(o, lse)``,
     [batch, Hq, D] and fp32 [batch, Hq]. See ``os_attention_decode_paged``."""
-    cache = _cache(k_pages, v_pages, page_table, kv_len)
-    dev = k_pages.device
-    sq = _strides(q, "q", 3, k_pages.dtype, dev)
-    batch, hq, d = q.shape
-    if batch != cache.batch or d != cache.head_dim:
-        raise ValueError(f"q must be [{cache.batch}, Hq, {cache.head_dim}] like the cache")
-    if hq < 1 or hq % cache.heads:
-        raise ValueError(f"{hq} query heads cannot share {cache.heads} key heads")
-    sw = (0, 0) if weights is None else _weights(weights, cache, dev)
+    cache, dev, batch, heads, d, capacity, _ = _cache(k_pages, v_pages, page_table, kv_len)
+    dtype = k_pages.dtype
+    sq = _strides(q, "q", 3, dtype, dev)
+    bq, hq, dq = q.shape
+    if bq != batch or dq != d:
+        raise ValueError(f"q must be [{batch}, Hq, {d}] like the cache")
+    if heads < 1 or hq < 1 or hq % heads:
+        raise ValueError(f"{hq} query heads cannot share {heads} key heads")
+    w, sw = None, (0, 0)
+    if weights is not None:
+        sw = _weights(weights, batch, heads, capacity, dev)
+        w = weights.data_ptr()
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty((batch, hq, d), dtype=q.dtype, device=dev) if o is None \
-        else _out(o, "o", q.dtype, (batch, hq, d), dev)
-    lse = torch.empty((batch, hq), dtype=torch.float32, device=dev) if lse is None \
-        else _out(lse, "lse", torch.float32, (batch, hq), dev)
+    if o is not None:
+        _out(o, "o", dtype, (batch, hq, d), dev)
+    if lse is not None:
+        _out(lse, "lse", torch.float32, (batch, hq), dev)
     lib = load()
-    with torch.cuda.device(dev):
-        sp = _stream_ptr(stream, dev)
-        ref = ctypes.byref(cache)
-        need = int(lib.os_attention_decode_paged_workspace_bytes(hq, ref, int(weights is not None)))
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty((batch, hq, d), dtype=dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
+        need = lib.os_attention_decode_paged_workspace_bytes(hq, cache, w is not None)
         if need < 0:
             raise OssError(4, "os_attention_decode_paged_workspace_bytes")
-        ws = _scratch(max(need, 16), dev, stream)
-        st = lib.os_attention_decode_paged(q.data_ptr(), sq[0], sq[1], hq, ref, float(scale),
-                                           o.data_ptr(), lse.data_ptr(), _ptr(weights), sw[0], sw[1],
-                                           ws.data_ptr(), ws.numel(), sp)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        st = lib.os_attention_decode_paged(q.data_ptr(), sq[0], sq[1], hq, cache, scale, o.data_ptr(),
+                                           lse.data_ptr(), w, sw[0], sw[1], ws.data_ptr(), need,
+                                           _raw_stream(dev))
     _check(st, "os_attention_decode_paged")
     return o, lse
 
@@ -799,32 +835,34 @@ def kv_cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.
     Hkv, budget] (-1 behind the last), the new kv_len and the kept tokens'
     weights [batch, Hkv, new_max_pages * page_size] (0 behind the last), ready
     for the next decode. See ``os_kv_cache_evict``."""
-    cache = _cache(k_pages, v_pages, page_table, kv_len)
-    dev = k_pages.device
-    sw = _weights(weights, cache, dev)
+    cache, dev, batch, heads, _, capacity, page_size = _cache(k_pages, v_pages, page_table, kv_len)
+    sw = _weights(weights, batch, heads, capacity, dev)
     _ints(new_page_table, "new_page_table", 2, dev)
-    batch, new_max = new_page_table.shape
-    if batch != cache.batch:
+    rows, new_max = new_page_table.shape
+    if rows != batch:
         raise ValueError("new_page_table must have one row for each row of page_table")
     budget, recent = int(budget), int(recent)
-    room = new_max * cache.page_size
+    room = new_max * page_size
     if not 1 <= budget <= room:
         raise ValueError(f"budget {budget} outside 1 .. {room}, what the new pages hold")
     if not 0 <= recent <= budget:
         raise ValueError(f"recent {recent} outside 0 .. budget")
-    kept = torch.empty((batch, cache.heads, budget), dtype=torch.int32, device=dev) if kept is None \
-        else _out(kept, "kept", torch.int32, (batch, cache.heads, budget), dev)
-    new_len = torch.empty(batch, dtype=torch.int32, device=dev) if new_len is None \
-        else _out(new_len, "new_len", torch.int32, (batch,), dev)
-    new_weights = torch.empty((batch, cache.heads, room), dtype=torch.float32, device=dev) \
-        if new_weights is None \
-        else _out(new_weights, "new_weights", torch.float32, (batch, cache.heads, room), dev)
-    with torch.cuda.device(dev):
-        st = load().os_kv_cache_evict(ctypes.byref(cache), weights.data_ptr(), sw[0], sw[1],
-                                      new_page_table.data_ptr(),
-                                      new_page_table.stride(0) if batch > 1 else 0, new_max, budget,
-                                      recent, kept.data_ptr(), new_len.data_ptr(),
-                                      new_weights.data_ptr(), _stream_ptr(stream, dev))
+    if kept is not None:
+        _out(kept, "kept", torch.int32, (batch, heads, budget), dev)
+    if new_len is not None:
+        _out(new_len, "new_len", torch.int32, (batch,), dev)
+    if new_weights is not None:
+        _out(new_weights, "new_weights", torch.float32, (batch, heads, room), dev)
+    with _on(dev, stream):
+        if kept is None:
+            kept = torch.empty((batch, heads, budget), dtype=torch.int32, device=dev)
+        if new_len is None:
+            new_len = torch.empty(batch, dtype=torch.int32, device=dev)
+        if new_weights is None:
+            new_weights = torch.empty((batch, heads, room), dtype=torch.float32, device=dev)
+        st = load().os_kv_cache_evict(cache, weights.data_ptr(), sw[0], sw[1], new_page_table.data_ptr(),
+                                      new_page_table.stride(0), new_max, budget, recent, kept.data_ptr(),
+                                      new_len.data_ptr(), new_weights.data_ptr(), _raw_stream(dev))
     _check(st, "os_kv_cache_evict")
     return kept, new_len, new_weights
 

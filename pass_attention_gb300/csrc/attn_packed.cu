@@ -826,16 +826,6 @@ bool make_map(CUtensorMap* map, const uint16_t* base, bool f16, int rank, const 
 
 constexpr int kMaxDevices = 64;
 
-int sm_count() {
-  static std::atomic<int> cached[kMaxDevices];
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  if ((sms = cached[dev].load(std::memory_order_relaxed)) > 0) return sms;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  cached[dev].store(sms, std::memory_order_relaxed);
-  return sms;
-}
-
 // Heads of one key head that a tile packs: a power of two, at most 128.
 int pack_heads(int group) {
   int n = 1;
@@ -883,8 +873,18 @@ cudaError_t launch_shape(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
 
 }  // namespace
 
+int device_sms() {
+  static std::atomic<int> cached[kMaxDevices];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  if ((sms = cached[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  cached[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
 int64_t attn_packed_workspace_bytes(int64_t tokens_k, int Hkv, int D) {
-  const int sms = sm_count();
+  const int sms = device_sms();
   if (sms < 1) return -1;
   const int64_t shares = static_cast<int64_t>(sms) * round_count(tokens_k, Hkv, D);
   return round256(2 * shares * (D / 8) * kSoftThreads * 16) + round256(2 * shares * kSoftThreads * 16) +
@@ -893,7 +893,7 @@ int64_t attn_packed_workspace_bytes(int64_t tokens_k, int Hkv, int D) {
 
 cudaError_t launch_attn_packed(const PackedArgs& a, void* workspace, unsigned int* err, const AttnFault& fault,
                                cudaStream_t stream) {
-  const int sms = sm_count();
+  const int sms = device_sms();
   if (sms < 1) return cudaErrorInvalidDevice;
   const int group = a.Hq / a.Hkv, heads = pack_heads(group);
   int pos_shift = 7;

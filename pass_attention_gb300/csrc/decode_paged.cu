@@ -29,10 +29,8 @@
 // copies with a cursor that runs ahead across segments, so no CTA barrier
 // stands between the loads. A page holds whole tiles (page_size >= 16).
 
+#include <atomic>
 #include <cstdint>
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include "device_common.cuh"
 #include "oss_internal.h"
@@ -642,10 +640,8 @@ struct Plan {
 };
 
 bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return false;
+  const int sms = device_sms();
+  if (sms < 1) return false;
   const int group = H / c.heads;
   Plan pl;
   pl.shares = sms * kCtasPerSm;
@@ -688,8 +684,17 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cuda
 template <bool kF16, int D, int NT>
 cudaError_t launch_shape(const DecodeParams& p, int shares, cudaStream_t stream) {
   constexpr int smem = Shape<D>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(decode_paged_kernel<kF16, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the kernel's shared-memory limit, raised once per device
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> smem_set[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices || !smem_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(decode_paged_kernel<kF16, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) smem_set[dev].store(true, std::memory_order_release);
+  }
   decode_paged_kernel<kF16, D, NT><<<shares, kThreads, smem, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_after(decode_join_kernel<kF16, D>, dim3(shares, NT * 8), kJoinWarps * 32, stream, p);

@@ -4,19 +4,27 @@
 // for whole prompts and by latency for one token a sequence.
 //
 // Eviction keeps n = min(len, budget) tokens of each (sequence, key head): the
-// last `recent`, and of the older ones those of the largest summed weight. The
-// selection finds the smallest kept weight by radix: fp32 weights become
-// integer keys of the same order, and a histogram of the leading digits of
-// the keys that match the digits found so far gives the next digit. Only
-// integers are counted, so atomics leave no order in the result. One more
-// sweep writes the kept positions in ascending order; of the keys equal to the
-// last one kept, the lowest positions are taken.
+// last `recent`, and of the older ones those of the largest summed weight. Two
+// kernels, both bound by HBM:
+//
+// * select. The smallest kept weight is found by radix: fp32 weights become
+//   integer keys of the same order, and a histogram of a digit (11, 11, 10 bits)
+//   of the keys that agree with the digits found so far gives the next digit.
+//   A thread-block cluster takes a row: its CTAs hold the keys of a slice in shared
+//   memory (one read of the weights), and each adds up all CTAs' histograms
+//   through distributed shared memory, so every digit costs one cluster
+//   barrier. Only integers are counted, so the atomics leave no order in the
+//   result. One more sweep writes the kept positions in ascending order; of the
+//   keys equal to the last one kept, the lowest positions are taken.
+// * move. Kept rows are copied page to page, four rows of a thread in flight.
 
+#include <atomic>
 #include <cstdint>
 
 #include "device_common.cuh"
 #include "oss_internal.h"
 #include "paged.h"
+#include "softmax_common.cuh"
 
 namespace oss {
 namespace {
@@ -75,8 +83,10 @@ kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
 // ---------------------------------------------------------------------------
 
 constexpr int kSelectThreads = 1024;
-constexpr int kDigitBits = 8;
-constexpr int kBins = 1 << kDigitBits;
+constexpr int kDigits = 3;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxSliceKeys = 48 * 1024;  // 192 KB of keys in shared memory
 
 struct EvictParams {
   PagedCache c;
@@ -103,23 +113,37 @@ __device__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t* total)
   __syncthreads();  // the previous scan's sums have been read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  uint32_t before = 0, all = 0;
-  for (int w = 0; w < kSelectThreads / 32; ++w) {
-    const uint32_t s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
+  // every warp scans the warps' sums
+  uint32_t w = warp_sums[lane];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, w, off);
+    if (lane >= off) w += y;
   }
-  *total = all;
-  return x + before;
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return x + (warp > 0 ? before : 0u);
 }
 
-// One CTA per (key head, sequence).
-__global__ void __launch_bounds__(kSelectThreads)
-evict_select_kernel(EvictParams p) {
-  __shared__ uint32_t hist[kBins];
+__device__ __forceinline__ uint32_t ld_peer(const uint32_t* slot, uint32_t rank) {
+  uint32_t remote, x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(slot)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(remote) : "memory");
+  return x;
+}
+
+// One cluster per (key head, sequence). kCached: a CTA's slice of the keys lies in
+// shared memory; otherwise every sweep reads the weights again.
+template <bool kCached>
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ uint32_t hist[kDigits][kBins];
   __shared__ uint32_t warp_sums[kSelectThreads / 32];
-  __shared__ uint32_t found_digit, found_rank;
-  const int head = blockIdx.x, seq = blockIdx.y;
+  __shared__ uint32_t found_digit, found_rank, slice_counts[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t C = cluster_size(), rank = cluster_rank();
+  const int head = blockIdx.x / C, seq = blockIdx.y;
+  const int tid = threadIdx.x;
   const int len = paged_length(p.c.kv_len[seq], p.c.max_pages, p.c.page_shift);
   const int keep = min(len, p.budget);
   const int recent = min(p.recent, keep);
@@ -130,98 +154,178 @@ evict_select_kernel(EvictParams p) {
   int32_t* kept = p.kept + row * p.budget;
   const int room = p.new_max_pages << p.c.page_shift;
   float* nw = p.new_weights + row * room;
-  if (head == 0 && threadIdx.x == 0) p.new_len[seq] = keep;
+  const int in_cluster = static_cast<int>(rank) * kSelectThreads + tid, all_threads = static_cast<int>(C) * kSelectThreads;
+  if (head == 0 && in_cluster == 0) p.new_len[seq] = keep;
 
-  // the smallest kept key, and how many keys equal to it are kept
-  uint32_t last = 0, ties = 0xffffffffu;
-  if (choose < older) {
-    uint32_t rank = choose;  // keys still to place at or below the digits found
-    for (int shift = 32 - kDigitBits; shift >= 0 && choose > 0; shift -= kDigitBits) {
-      for (int i = threadIdx.x; i < kBins; i += kSelectThreads) hist[i] = 0;
-      __syncthreads();
-      const uint64_t mask = ~((uint64_t(1) << (shift + kDigitBits)) - 1);
-      for (int i = threadIdx.x; i < older; i += kSelectThreads) {
-        const uint32_t key = weight_key(w[i]);
-        if ((key & mask) == last) atomicAdd(&hist[(key >> shift) & (kBins - 1)], 1u);
-      }
-      __syncthreads();
-      // thread i < kBins: keys in the bins above kBins - 1 - i, that bin included
-      const uint32_t mine = threadIdx.x < kBins ? hist[kBins - 1 - threadIdx.x] : 0u;
-      uint32_t total;
-      const uint32_t upto = block_scan(mine, warp_sums, &total);
-      if (threadIdx.x < kBins && upto >= rank && upto - mine < rank) {
-        found_digit = kBins - 1 - threadIdx.x;
-        found_rank = rank - (upto - mine);
-      }
-      __syncthreads();
-      last |= found_digit << shift;
-      rank = found_rank;
-      __syncthreads();
-    }
-    ties = rank;
-    if (choose == 0) {
-      last = 0xffffffffu;
-      ties = 0;
-    }
-  }
-  // kept positions in ascending order
-  uint32_t above = 0, equal = 0;  // keys before this tile
-  for (int base = 0; base < older; base += kSelectThreads) {
-    const int i = base + threadIdx.x;
-    const uint32_t key = i < older ? weight_key(w[i]) : 0u;
-    const bool gt = i < older && (key > last || ties == 0xffffffffu);
-    const bool eq = i < older && key == last && !gt;
-    uint32_t total;
-    const uint32_t upto = block_scan((gt ? 1u : 0u) | (eq ? 0x10000u : 0u), warp_sums, &total);
-    const uint32_t gt_before = above + (upto & 0xffffu) - (gt ? 1u : 0u);
-    const uint32_t eq_before = equal + (upto >> 16) - (eq ? 1u : 0u);
-    if (gt || (eq && eq_before < ties)) {
-      const uint32_t at = gt_before + min(eq_before, ties);
-      kept[at] = i;
-      nw[at] = w[i];
-    }
-    above += total & 0xffffu;
-    equal += total >> 16;
-  }
-  for (int i = threadIdx.x; i < recent; i += kSelectThreads) {
+  for (int i = in_cluster; i < recent; i += all_threads) {
     kept[choose + i] = older + i;
     nw[choose + i] = w[older + i];
   }
-  for (int i = keep + threadIdx.x; i < p.budget; i += kSelectThreads) kept[i] = -1;
-  for (int i = keep + threadIdx.x; i < room; i += kSelectThreads) nw[i] = 0.f;
+  for (int i = keep + in_cluster; i < p.budget; i += all_threads) kept[i] = -1;
+  for (int i = keep + in_cluster; i < room; i += all_threads) nw[i] = 0.f;
+  if (choose == 0) return;  // the same for the whole cluster
+  if (choose == older) {
+    for (int i = in_cluster; i < older; i += all_threads) {
+      kept[i] = i;
+      nw[i] = w[i];
+    }
+    return;
+  }
+
+  const int slice = (older + static_cast<int>(C) - 1) / static_cast<int>(C);
+  const int first = min(older, static_cast<int>(rank) * slice);
+  const int n = min(older - first, slice);
+  auto key_at = [&](int i) -> uint32_t { return kCached ? keys[i] : weight_key(w[first + i]); };
+  for (int i = tid; i < kDigits * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
+  if constexpr (kCached) {
+#pragma unroll 8
+    for (int i = tid; i < n; i += kSelectThreads) keys[i] = weight_key(__ldg(w + first + i));
+  }
+  __syncthreads();
+
+  // the smallest kept key, and how many keys equal to it are kept
+  uint32_t last = 0, ties = choose;
+#pragma unroll
+  for (int d = 0; d < kDigits; ++d) {
+    const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
+    const int bits = d == 2 ? 10 : 11;
+    for (int i = tid; i < n; i += kSelectThreads) {
+      const uint32_t key = key_at(i);
+      if (d == 0 || (key >> (shift + bits)) == (last >> (shift + bits)))
+        atomicAdd(&hist[d][(key >> shift) & ((1u << bits) - 1)], 1u);
+    }
+    __syncwarp();
+    cluster_sync_all();
+    // thread t: bins kBins - 1 - 2 t and the one below, over all slices
+    uint32_t hi = 0, lo = 0;
+    for (uint32_t r = 0; r < C; ++r) {
+      hi += ld_peer(&hist[d][kBins - 1 - 2 * tid], r);
+      lo += ld_peer(&hist[d][kBins - 2 - 2 * tid], r);
+    }
+    uint32_t total;
+    const uint32_t upto = block_scan(hi + lo, warp_sums, &total);
+    const uint32_t above = upto - hi - lo;  // keys in higher bins
+    if (above < ties && upto >= ties) {
+      const bool in_hi = above + hi >= ties;
+      found_digit = kBins - 1 - 2 * tid - (in_hi ? 0 : 1);
+      found_rank = ties - above - (in_hi ? 0u : hi);
+    }
+    __syncthreads();
+    last |= found_digit << shift;
+    ties = found_rank;
+  }
+
+  // a thread's run of keys: contiguous, of odd length (no bank conflicts)
+  const int run = ((n + kSelectThreads - 1) / kSelectThreads) | 1;
+  const int r0 = min(n, tid * run), r1 = min(n, r0 + run);
+  uint32_t gt = 0, eq = 0;
+  for (int i = r0; i < r1; ++i) {
+    const uint32_t key = key_at(i);
+    gt += key > last;
+    eq += key == last;
+  }
+  uint32_t all_gt, all_eq;
+  uint32_t gt_at = block_scan(gt, warp_sums, &all_gt) - gt;
+  uint32_t eq_at = block_scan(eq, warp_sums, &all_eq) - eq;
+  if (tid == 0) {
+    slice_counts[0] = all_gt;
+    slice_counts[1] = all_eq;
+  }
+  __syncwarp();
+  cluster_sync_all();
+  for (uint32_t r = 0; r < rank; ++r) {
+    gt_at += ld_peer(&slice_counts[0], r);
+    eq_at += ld_peer(&slice_counts[1], r);
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  for (int i = r0; i < r1; ++i) {
+    const uint32_t key = key_at(i);
+    if (key > last || (key == last && eq_at < ties)) {
+      const uint32_t at = gt_at + min(eq_at, ties);
+      kept[at] = first + i;
+      nw[at] = w[first + i];
+    }
+    gt_at += key > last;
+    eq_at += key == last;
+  }
+  // a CTA's counts may be read until the others have passed here
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-constexpr int kMoveThreads = 128;
-constexpr int kMoveRows = 64;  // rows a CTA moves
+constexpr int kMoveThreads = 256;
+constexpr int kMoveBatch = 4;  // rows of a thread in flight
 
 // One CTA per (rows, key head, sequence); a group of D / 8 threads takes a row.
+template <int kChunks>
 __global__ void __launch_bounds__(kMoveThreads)
-evict_move_kernel(EvictParams p, uint16_t* k_pages, uint16_t* v_pages, int chunks_per_head,
-                  unsigned int* err) {
+evict_move_kernel(EvictParams p, uint16_t* k_pages, uint16_t* v_pages, unsigned int* err) {
+  constexpr int kGroups = kMoveThreads / kChunks;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int head = blockIdx.y, seq = blockIdx.z;
-  const int64_t row = static_cast<int64_t>(seq) * p.c.heads + head;
-  const int32_t* kept = p.kept + row * p.budget;
-  const int rows = min(p.budget, p.new_max_pages << p.c.page_shift);
-  const int per_pass = kMoveThreads / chunks_per_head;
-  const int chunk = threadIdx.x % chunks_per_head;
-  const int first = blockIdx.x * kMoveRows;
+  const int32_t* kept = p.kept + (static_cast<int64_t>(seq) * p.c.heads + head) * p.budget;
+  const int chunk = threadIdx.x % kChunks;
+  const int r0 = blockIdx.x * (kGroups * kMoveBatch) + threadIdx.x / kChunks;
   const int slot_mask = (1 << p.c.page_shift) - 1;
-  for (int r = first + threadIdx.x / chunks_per_head; r < min(first + kMoveRows, rows); r += per_pass) {
-    const int pos = kept[r];
-    if (pos < 0) break;
-    const int from = p.c.table[static_cast<int64_t>(seq) * p.c.ld_table + (pos >> p.c.page_shift)];
-    const int to = p.new_table[static_cast<int64_t>(seq) * p.ld_new_table + (r >> p.c.page_shift)];
-    if (!page_ok(from, p.c.num_pages) || !page_ok(to, p.c.num_pages)) {
+  const int32_t* table = p.c.table + static_cast<int64_t>(seq) * p.c.ld_table;
+  const int32_t* new_table = p.new_table + static_cast<int64_t>(seq) * p.ld_new_table;
+  int64_t from[kMoveBatch], to[kMoveBatch];
+  uint4 kk[kMoveBatch], vv[kMoveBatch];
+#pragma unroll
+  for (int u = 0; u < kMoveBatch; ++u) {
+    const int r = r0 + u * kGroups;
+    to[u] = -1;
+    const int pos = r < p.budget ? kept[r] : -1;
+    if (pos < 0) continue;
+    const int src = table[pos >> p.c.page_shift], dst = new_table[r >> p.c.page_shift];
+    if (!page_ok(src, p.c.num_pages) || !page_ok(dst, p.c.num_pages)) {
       bad_index(err, kSiteBadPage);
       continue;
     }
-    const int64_t a = pool_offset(from, head, pos & slot_mask, p.c.ld_page, p.c.ld_head, p.c.ld_slot) + chunk * 8;
-    const int64_t b = pool_offset(to, head, r & slot_mask, p.c.ld_page, p.c.ld_head, p.c.ld_slot) + chunk * 8;
-    const uint4 kk = *reinterpret_cast<const uint4*>(k_pages + a);
-    const uint4 vv = *reinterpret_cast<const uint4*>(v_pages + a);
-    *reinterpret_cast<uint4*>(k_pages + b) = kk;
-    *reinterpret_cast<uint4*>(v_pages + b) = vv;
+    from[u] = pool_offset(src, head, pos & slot_mask, p.c.ld_page, p.c.ld_head, p.c.ld_slot) + chunk * 8;
+    to[u] = pool_offset(dst, head, r & slot_mask, p.c.ld_page, p.c.ld_head, p.c.ld_slot) + chunk * 8;
   }
+#pragma unroll
+  for (int u = 0; u < kMoveBatch; ++u) {
+    if (to[u] < 0) continue;
+    kk[u] = *reinterpret_cast<const uint4*>(k_pages + from[u]);
+    vv[u] = *reinterpret_cast<const uint4*>(v_pages + from[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kMoveBatch; ++u) {
+    if (to[u] < 0) continue;
+    *reinterpret_cast<uint4*>(k_pages + to[u]) = kk[u];
+    *reinterpret_cast<uint4*>(v_pages + to[u]) = vv[u];
+  }
+}
+
+template <bool kCached>
+cudaError_t launch_select(const EvictParams& p, int C, int smem, cudaStream_t stream) {
+  // the kernel's shared-memory limit, raised once per device
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> smem_set[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices || !smem_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(evict_select_kernel<kCached>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSliceKeys * 4);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) smem_set[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.c.heads * C, p.c.batch);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<kCached>, p);
 }
 
 PagedCache device_cache(const os_paged_cache& c) {
@@ -256,14 +360,29 @@ cudaError_t launch_kv_evict(const os_paged_cache& cache, const float* weights, i
                             cudaStream_t stream) {
   const EvictParams p{device_cache(cache), weights, ld_w_batch, ld_w_head, new_table, ld_new_table,
                       new_max_pages, budget, recent, kept, new_len, new_weights};
-  evict_select_kernel<<<dim3(cache.heads, cache.batch), kSelectThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  // CTAs of a row: enough for the GPU to be filled while a slice keeps at least
+  // 4096 keys, and for a slice to fit shared memory where eight can do it
+  const int64_t capacity = static_cast<int64_t>(cache.max_pages) * cache.page_size;
+  const int64_t rows = static_cast<int64_t>(cache.heads) * cache.batch;
+  int C = 1;
+  while (C < kMaxCluster && (capacity / C > kMaxSliceKeys || (rows * C < 152 && capacity / C > 4096))) C *= 2;
+  const int64_t slice = (capacity + C - 1) / C;
+  cudaError_t e = slice <= kMaxSliceKeys ? launch_select<true>(p, C, static_cast<int>(slice) * 4, stream)
+                                         : launch_select<false>(p, C, 0, stream);
   if (e != cudaSuccess) return e;
-  const dim3 grid((budget + kMoveRows - 1) / kMoveRows, cache.heads, cache.batch);
-  evict_move_kernel<<<grid, kMoveThreads, 0, stream>>>(p, static_cast<uint16_t*>(cache.k_pages),
-                                                       static_cast<uint16_t*>(cache.v_pages),
-                                                       cache.head_dim / 8, err);
-  return cudaGetLastError();
+  const int chunks = cache.head_dim / 8, rows_per_cta = kMoveThreads / chunks * kMoveBatch;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((budget + rows_per_cta - 1) / rows_per_cta, cache.heads, cache.batch);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  uint16_t *k = static_cast<uint16_t*>(cache.k_pages), *v = static_cast<uint16_t*>(cache.v_pages);
+  return chunks == 16 ? cudaLaunchKernelEx(&cfg, evict_move_kernel<16>, p, k, v, err)
+                      : cudaLaunchKernelEx(&cfg, evict_move_kernel<8>, p, k, v, err);
 }
 
 }  // namespace oss

@@ -100,6 +100,9 @@ int64_t attention_workspace_bytes(int B, int H, int Sq, int Sk, bool causal);
 // uses none). Returns -1 when the device could not be queried, else 0.
 int64_t attention_workspace_counters(int B, int H, int Sq, int Sk, bool causal, int64_t* bytes);
 
+// SMs of the current device (0: it could not be queried).
+int device_sms();
+
 // The pools and tables of a validated os_paged_cache, for kernels.
 PagedCache paged_cache(const os_paged_cache& c);
 

@@ -25,10 +25,25 @@ def lib():
     return oss.load()
 
 
+class Cache(ctypes.Structure):
+    """os_paged_cache, declared on its own: the binding's packed form has to agree with it."""
+
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("ld_page", ctypes.c_int64),
+                ("ld_head", ctypes.c_int64), ("ld_slot", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("ld_table", ctypes.c_int64), ("kv_len", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+def test_packed_struct_agrees():
+    values = list(range(1, 16))
+    assert oss._PAGED_CACHE.pack(*values) == bytes(Cache(*values))[:oss._PAGED_CACHE.size]
+
+
 def cache(**change):
     fields = dict(k_pages=A, v_pages=A, ld_page=4096, ld_head=2048, ld_slot=128, page_table=A, ld_table=4, kv_len=A,
                   num_pages=10, heads=2, page_size=16, head_dim=128, dtype=1, batch=3, max_pages=4)
-    return oss._PagedCache(**{**fields, **change})
+    return Cache(**{**fields, **change})
 
 
 BAD_CACHES = [(dict(k_pages=None), INVALID), (dict(v_pages=None), INVALID), (dict(page_table=None), INVALID),

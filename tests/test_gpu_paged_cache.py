@@ -166,6 +166,25 @@ def test_decode_same_bits_every_time_and_beside_other_calls():
         assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
 
 
+def test_outputs_on_another_stream_take_no_memory_in_use():
+    # a block freed while the current stream still has to read it: an output
+    # allocated for another stream must not be put there
+    q, kp, vp, table, kv_len, _ = make([2000] * 4, 8, 2, page=64, seed=13)
+    ref, _ = oss.attention_decode_paged(q, kp, vp, table, kv_len)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        x = [torch.full_like(q, 3.0) for _ in range(8)]
+        torch.cuda._sleep(20_000_000)
+        y = [t + 0 for t in x]
+        del x
+        o, _ = oss.attention_decode_paged(q, kp, vp, table, kv_len, stream=side)
+        side.synchronize()
+        assert torch.equal(o.clone(), ref)
+        torch.cuda.synchronize()
+        assert all(torch.all(t == 3.0) for t in y)
+
+
 def test_decode_in_two_graphs_with_new_lengths():
     # captured once, replayed side by side with other lengths in the same tensors
     q, kp, vp, table, kv_len, _ = make([3000, 700], 8, 2, page=32, seed=11)
