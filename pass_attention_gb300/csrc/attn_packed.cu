@@ -1,11 +1,18 @@
 // Attention forward over packed sequences with grouped key heads, on the
 // tcgen05 tensor cores.
 //
-// The recurrence, the tensor-memory layout and the roles of the warps are those
+// The recurrence, the tensor-memory layout and most roles of the warps are those
 // of the dense attention forward (attn_fwd.cu): 8 softmax warps, a TMA producer,
 // one thread that issues S = Q K^T and one that issues O += P V, three score
 // buffers in tensor memory, the O rescale past a threshold of 2^8. What bounds
 // it is the same chain; what is different here:
+//
+// Hand-over. Packed sequences are often short, and then the step from one query
+// tile to the next counts. Four warps of their own read O out of tensor memory, scale and store
+// it, while the softmax warps are at the next tile's scores already; the
+// first P V of that tile waits for the read-out only. Registers move to where they
+// are needed: 168 a thread for the softmax, 120 for the epilogue, 56 for the others
+// (512 threads x 128 at launch).
 //
 // Rows. A tile's 128 rows are 128 / P' consecutive queries times P' query heads of
 // one key head, P' the largest power of two that divides G = Hq / Hkv (up to
@@ -44,14 +51,20 @@ namespace {
 
 constexpr int kBM = 128;          // rows per query tile (= tensor-memory lanes)
 constexpr int kBN = 128;          // keys per KV tile
-constexpr int kStages = 3;        // K ring, V ring, score buffers
-constexpr int kKLead = 2;         // K loads run this many steps ahead of V loads
+constexpr int kScores = 3;        // score buffers, and stages of the V ring
+constexpr int kKStages = 2;       // K ring, and Q buffers
 constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kProducerWarp = 8;
 constexpr int kQkWarp = 9;
 constexpr int kPvWarp = 10;
-constexpr int kThreads = (kPvWarp + 1) * 32;
+constexpr int kVWarp = 11;
+constexpr int kEpiWarp = 12;      // warps 12..15: epilogue, 32 rows each
+constexpr int kEpiThreads = 128;
+constexpr int kThreads = 512;
+// registers a thread after the split; the warpgroups' sum is what the launch holds
+constexpr int kSoftRegs = 184, kIssueRegs = 64, kEpiRegs = 80;
+static_assert(256 * kSoftRegs + 128 * kIssueRegs + 128 * kEpiRegs <= kThreads * 128, "register split");
 constexpr int kHalf = 128 * 128;  // 128 rows x 64 dims x 2 bytes
 constexpr int kMaxRounds = 8;
 constexpr uint32_t kTmemCols = 512;
@@ -65,9 +78,9 @@ template <int D>
 struct Smem {
   static constexpr int kTile = (D / 64) * kHalf;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kTile;
-  static constexpr int kOffV = kOffK + kStages * kTile;
-  static constexpr int kBytes = kOffV + kStages * kTile + 1024;  // + alignment slack
+  static constexpr int kOffK = kOffQ + kKStages * kTile;
+  static constexpr int kOffV = kOffK + kKStages * kTile;
+  static constexpr int kBytes = kOffV + kScores * kTile + 1024;  // + alignment slack
 };
 
 struct PackedParams {
@@ -78,18 +91,42 @@ struct PackedParams {
   float C;  // scale * log2(e)
   int causal;
   unsigned int* err;
-  uint64_t timeout_ns;
-  unsigned int tag;
+  uint32_t wait_cycles;  // limit of every wait
   int skip_v_step;  // test hook: the producer skips the V load of this step (-1: none)
-  // workspace: a part's rows in the softmax threads' layout
-  float4* part_o;   // [2 shares][D / 8][kSoftThreads]: unnormalised O
-  float4* part_ml;  // [2 shares][kSoftThreads]: base-2 m, l of rows a, b
+  // workspace
+  float4* part_o;   // [2 shares][D / 4][128 rows]: unnormalised O, 4 dims of a row
+  float2* part_ml;  // [2 shares][128 rows]: base-2 m, l
   int4* meta;       // [shares]: {parts, first query row, queries, pack} of the item cut at its end
 };
 
-#define wait_bar(bar, parity, abort_flag, err, site) \
-  (mbar_test_wait((bar), (parity)) ||                 \
-   wait_bar_slow<kKernelAttnPacked>((bar), (parity), (abort_flag), (err), (site), p.timeout_ns, p.tag))
+// Bounded wait, small: it is inlined some twenty times, the step and hand-over
+// code of all roles has to stay in the instruction cache (with polls that read the
+// error word inlined, warps waited for instructions most of the time), and a
+// kernel that moves registers between warps makes no calls. A wait that runs out
+// leaves its site in the abort flag, which ends the other waits of the CTA and is
+// reported when all roles have stopped.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site,
+                                           uint32_t limit /* cycles */) {
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+  OSS_ROLLED
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  } while (static_cast<uint32_t>(clock()) - t0 < limit);
+  *abort_flag = site;
+  return false;
+}
+#define wait_bar(bar, parity, site) wait_phase((bar), (parity), abort_flag, (site), p.wait_cycles)
+
+// Wait used while draining: ignores the abort flag.
+__device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+  OSS_ROLLED
+  do {
+    if (mbar_try_wait(bar, parity)) return;
+  } while (static_cast<uint32_t>(clock()) - t0 < static_cast<uint32_t>(kDrainNs * 2));
+  *abort_flag = kSiteDrain;
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
                                             int c1, int c2, int c3) {
@@ -100,14 +137,43 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+constexpr int kUnits = 4;  // ring of units ahead of the slowest role
+constexpr int kUnitReaders = 3 + kSoftWarps + kEpiThreads / 32;  // Q K^T, P V and V threads, warps: each lets a unit go once
+
+// Place of KV step g in a ring of kDepth: g % kDepth, and the parity of g / kDepth.
+template <int kDepth>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kDepth) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ void st_shared_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr));
+  return x;
+}
+
 struct Barriers {
-  uint64_t q_full;   // Q tile landed
-  uint64_t q_free;   // every QK^T of the item in the Q buffer is done
-  uint64_t k_full[kStages], v_full[kStages];
-  uint64_t s_full[kStages];
-  uint64_t p_ready[2][kStages];  // P of keys 0..63 / 64..127 written
-  uint64_t o_done[kStages];      // P V done, for the steps of each buffer
+  uint64_t q_full[kKStages];  // Q tile landed
+  uint64_t q_free[kKStages];  // every QK^T of the item in the Q buffer is done, and its O has left through it
+  uint64_t k_full[kKStages];
+  uint64_t v_full[kScores];
+  uint64_t s_full[kScores];
+  uint64_t p_ready[2][kScores];  // P of keys 0..63 / 64..127 written
+  uint64_t o_done[kScores];      // P V done, for the steps of each buffer
   uint64_t o_free;               // the epilogue has read O out of tensor memory
+  uint64_t ml_full, ml_free;     // m and l of an item's rows, for the epilogue
+  uint64_t unit_full[kUnits], unit_free[kUnits];
   uint64_t drain[2];
 };
 
@@ -124,8 +190,7 @@ struct ShareEnd {
 struct Shares {
   ShareStart start[kMaxRounds];
   ShareEnd end[kMaxRounds];
-  int64_t total;
-  int32_t count;
+  ShareCut cut;
 };
 
 __device__ __forceinline__ PackedSeq load_seq(const PackedParams& p, int b) {
@@ -133,86 +198,125 @@ __device__ __forceinline__ PackedSeq load_seq(const PackedParams& p, int b) {
                     row_range(p.cu_k[b], p.cu_k[b + 1], p.tokens_k), p.pos_shift);
 }
 
-// Finds this CTA's shares: every thread measures a run of sequences, a block
-// scan places the runs, and the thread whose run holds a boundary locates it.
-__device__ void find_shares(const PackedParams& p, Shares* sh) {
-  __shared__ int64_t warp_len[kThreads / 32], warp_items[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool causal = p.causal != 0;
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
-  int64_t mine = 0, items = 0;
+// Length of the items of sequences [b0, b1), in one pack, and their tiles.
+__device__ __forceinline__ int64_t run_length(const PackedParams& p, int b0, int b1, uint32_t* tiles) {
+  int64_t sum = 0;
+  uint32_t n = 0;
+  OSS_ROLLED
   for (int b = b0; b < b1; ++b) {
     const PackedSeq s = load_seq(p, b);
-    mine += length_before(s, s.tiles, p.pos_shift, causal);
-    items += s.tiles;
-    if (blockIdx.x == 0 && (row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q).clamped ||
-                            row_range(p.cu_k[b], p.cu_k[b + 1], p.tokens_k).clamped))
-      report_error(p.err, kKernelPaged | (kSiteBadOffsets << 8));
+    sum += length_before(s, s.tiles, p.pos_shift, p.causal != 0);
+    n += static_cast<uint32_t>(s.tiles);
   }
-  mine *= p.packs;
-  items *= p.packs;
-  int64_t upto = mine;
-#pragma unroll
+  *tiles = n;
+  return sum;
+}
+
+// Inclusive scan over a warp.
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+  const int lane = threadIdx.x & 31;
+  OSS_ROLLED
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += x;
-    items += __shfl_xor_sync(0xffffffffu, items, off);
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
   }
-  if (lane == 31) {
-    warp_len[warp] = upto;
-    warp_items[warp] = items;
-  }
-  if (tid < kMaxRounds) {
-    sh->start[tid] = ShareStart{0, 0, 0, 0, 0};
-    sh->end[tid] = ShareEnd{0, 0};
-  }
-  __syncthreads();
-  int64_t before = upto - mine, total = 0, n_items = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += warp_len[i];
-    total += warp_len[i];
-    n_items += warp_items[i];
-  }
-  const int ctas = gridDim.x;
-  const int n = total > 0 ? share_count(total, n_items, ctas, p.rounds) : 0;
-  if (tid == 0) {
-    sh->total = total;
-    sh->count = n;
-  }
-  if (mine > 0) {
-    for (int r = 0; r < p.rounds; ++r) {
-      const int64_t share = static_cast<int64_t>(r) * ctas + blockIdx.x;
-      if (share >= n) break;
-#pragma unroll 1
-      for (int e = 0; e < 2; ++e) {
-        const int64_t at = share_begin(share + e, total, n);
-        if (at < before || at >= before + mine) {
-          if (at == total && at == before + mine) sh->end[r] = ShareEnd{total, 0};
-          continue;
-        }
-        int64_t w = before;
-        for (int b = b0; b < b1; ++b) {
-          const PackedSeq s = load_seq(p, b);
-          const int64_t len = length_before(s, s.tiles, p.pos_shift, causal);
-          if (at >= w + len * p.packs) {
-            w += len * p.packs;
-            continue;
-          }
-          const int pack = static_cast<int>((at - w) / len);
-          w += pack * len;
-          const int tile = tile_at(s, at - w, p.pos_shift, causal);
-          w += length_before(s, tile, p.pos_shift, causal);
-          const int steps = kv_tiles(s, tile, p.pos_shift, causal);
-          const int step = cut_step(at - w, steps);
-          if (e == 0)
-            sh->start[r] = ShareStart{w, b, pack, tile, step};
-          else
-            sh->end[r] = step == steps ? ShareEnd{w + kTileWeight + steps, 0} : ShareEnd{w, step};
-          break;
-        }
+  return x;
+}
+
+// Finds this CTA's shares. The sequences are cut into a run per warp, and each of
+// those into a run per lane. All warps measure theirs; then warp 2 r + e looks
+// for the beginning (e = 0) or the end (e = 1) of the share of round r: the warp's
+// run that holds it, that run's lane, and so on down to a sequence, then the query
+// tile, 32 candidates at a time. (One thread that searched alone took 7 us of a
+// launch; rolled loops, because code that runs once is paid for in instruction
+// fetches.)
+static_assert(2 * kMaxRounds <= kThreads / 32, "a warp for every boundary");
+__device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, int64_t* scratch /* [kThreads / 32] */, uint32_t* tile_scratch) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr uint32_t kAll = 0xffffffffu;
+  int64_t* warp_len = scratch;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool causal = p.causal != 0;
+  const int per_warp = (p.batch + kWarps - 1) / kWarps;
+  int lo = min(p.batch, warp * per_warp), hi = min(p.batch, lo + per_warp);  // the run in hand
+  int64_t before = 0, at = 0, sum = 0;
+  uint32_t tiles = 0;
+  const int r = warp >> 1, e = warp & 1;
+  OSS_ROLLED
+  for (int level = 0;; ++level) {
+    // the lanes' runs of [lo, hi)
+    const int per = (hi - lo + 31) / 32;
+    const int b0 = min(hi, lo + lane * per), b1 = min(hi, b0 + per);
+    sum = run_length(p, b0, b1, &tiles);
+    const int64_t upto = warp_scan(sum);
+    if (level == 0) {
+      if (blockIdx.x == 0) {
+        OSS_ROLLED
+        for (int b = b0; b < b1; ++b)
+          if (row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q).clamped || row_range(p.cu_k[b], p.cu_k[b + 1], p.tokens_k).clamped)
+            report_error(p.err, kKernelPaged | (kSiteBadOffsets << 8));
       }
+      tiles = __reduce_add_sync(kAll, tiles);
+      if (lane == 31) {
+        warp_len[warp] = upto;
+        tile_scratch[warp] = tiles;
+      }
+      if (threadIdx.x < kMaxRounds) {
+        sh->start[threadIdx.x] = ShareStart{0, 0, 0, 0, 0};
+        sh->end[threadIdx.x] = ShareEnd{0, 0};
+      }
+      __syncthreads();
+      const int64_t len = warp_scan(lane < kWarps ? warp_len[lane] : 0);
+      const int64_t items = static_cast<int64_t>(__reduce_add_sync(kAll, lane < kWarps ? tile_scratch[lane] : 0u)) * p.packs;
+      const int64_t total = __shfl_sync(kAll, len, 31) * p.packs;
+      const ShareCut cut = share_cut(total, share_count(total, items, gridDim.x, p.rounds));
+      if (threadIdx.x == 0) sh->cut = cut;
+      const uint32_t share = r * gridDim.x + blockIdx.x;
+      if (r >= p.rounds || share >= cut.count) break;
+      at = share_begin(cut, share + e);
+      if (at == total) {
+        if (lane == 0) sh->end[r] = ShareEnd{total, 0};
+        break;
+      }
+      // the first warp's run that ends behind the boundary
+      const int w = __ffs(__ballot_sync(kAll, len * p.packs > at)) - 1;
+      lo = min(p.batch, w * per_warp);
+      hi = min(p.batch, lo + per_warp);
+      before = w > 0 ? __shfl_sync(kAll, len, w - 1) * p.packs : 0;
+      continue;
     }
+    const int k = __ffs(__ballot_sync(kAll, before + upto * p.packs > at)) - 1;
+    lo = __shfl_sync(kAll, b0, k);
+    hi = __shfl_sync(kAll, b1, k);
+    before += __shfl_sync(kAll, upto - sum, k) * p.packs;
+    if (hi - lo > 1) continue;
+    // the sequence: its pack, then its query tile among T0 + lane * stride
+    const int64_t len = __shfl_sync(kAll, sum, k);
+    const int pack = small_quotient(at - before, len);
+    before += pack * len;
+    const PackedSeq s = load_seq(p, lo);
+    int tile = 0;
+    int64_t stride = 1;
+    while (stride * 32 < s.tiles) stride *= 32;
+    int64_t place = 0;
+    OSS_ROLLED
+    for (; stride > 0; stride /= 32) {
+      const int64_t T = tile + static_cast<int64_t>(lane) * stride;
+      const int64_t x = T < s.tiles ? length_before(s, static_cast<int>(T), p.pos_shift, causal) : INT64_MAX;
+      const int last = 31 - __clz(__ballot_sync(kAll, x <= at - before));
+      tile += static_cast<int>(last * stride);
+      place = __shfl_sync(kAll, x, last);
+    }
+    if (lane == 0) {
+      const int64_t w = before + place;
+      const int steps = kv_tiles(s, tile, p.pos_shift, causal);
+      const int step = cut_step(at - w, steps);
+      if (e == 0)
+        sh->start[r] = ShareStart{w, lo, pack, tile, step};
+      else
+        sh->end[r] = step == steps ? ShareEnd{w + kTileWeight + steps, 0} : ShareEnd{w, step};
+    }
+    break;
   }
   __syncthreads();
 }
@@ -222,42 +326,42 @@ struct Unit {
   int q_row, n_pos;       // first query row, queries of the tile
   int k_row, k_len, vis;  // first key row, keys, keys that the tile's first query sees
   int n_kv, n_diag, s0, s1, pack, share;
-  int64_t w;              // the item's place
+  int parts;              // parts of the item, if it begins here and is cut
+  int end;                // no unit: the shares are done
 };
 
-// The walk of a CTA over its shares; every role makes the same one.
+// The walk of a CTA over its shares.
 struct Walk {
   PackedSeq s;
   int64_t w, end_w;
   int seq, pack, tile, s0, end_step, round;
   bool fetch;  // the next item belongs to a later sequence
 
-  __device__ __forceinline__ void begin_round(const PackedParams& p, const Shares& sh) {
-    const ShareStart a = sh.start[round];
-    w = a.w;
-    seq = a.seq;
-    pack = a.pack;
-    tile = a.tile;
-    s0 = a.step;
-    end_w = sh.end[round].w;
-    end_step = sh.end[round].step;
-    fetch = false;
-    if (w < end_w || (w == end_w && end_step > 0)) s = load_seq(p, seq);
-  }
-  __device__ __forceinline__ void begin(const PackedParams& p, const Shares& sh) {
-    round = 0;
-    begin_round(p, sh);
+  __device__ __forceinline__ void begin() {
+    round = -1;
+    w = end_w = 0;
+    end_step = 0;
   }
   __device__ __forceinline__ bool next(const PackedParams& p, const Shares& sh, Unit& u) {
     const bool causal = p.causal != 0;
+    OSS_ROLLED
     for (;;) {
-      if (!(w < end_w || (w == end_w && end_step > 0))) {
+      if (w > end_w || (w == end_w && end_step == 0)) {  // the share of the next round
         if (++round >= p.rounds) return false;
-        begin_round(p, sh);
+        const ShareStart a = sh.start[round];
+        w = a.w;
+        seq = a.seq - 1;
+        pack = a.pack;
+        tile = a.tile;
+        s0 = a.step;
+        end_w = sh.end[round].w;
+        end_step = sh.end[round].step;
+        fetch = true;
         continue;
       }
       if (fetch) {
         fetch = false;
+        OSS_ROLLED
         do {
           s = load_seq(p, ++seq);
         } while (s.tiles == 0 && seq + 1 < p.batch);
@@ -279,7 +383,10 @@ struct Walk {
         u.s1 = s1;
         u.pack = pack;
         u.share = round * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-        u.w = w;
+        u.parts = 0;
+        if (from == 0 && s1 < steps)
+          u.parts = static_cast<int>(last_boundary(sh.cut, w + kTileWeight + steps - kMinSteps)) - u.share + 1;
+        u.end = 0;
       }
       w += kTileWeight + steps;
       s0 = 0;
@@ -310,25 +417,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return w;
 }
 
-// Stores 32 dims (from chunk 4 mb of half h) of rows a and b. v[4 i + e]: the
-// thread's values of 8-dim chunk i, a's two dims then b's two; a 4 x 4 transpose
-// among a row's four threads hands each a whole chunk. A row without keys (inv
-// 0) is written as zeros whatever its accumulator holds.
-template <bool kF16>
-__device__ __forceinline__ void store_chunks(uint4* oa, uint4* ob, const float (&v)[16], float inv_a, float inv_b,
-                                             int chunk0, int jj, bool live_a, bool live_b) {
-  uint32_t wa[4], wb[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    wa[i] = inv_a > 0.f ? pack16<kF16>(v[4 * i] * inv_a, v[4 * i + 1] * inv_a) : 0u;
-    wb[i] = inv_b > 0.f ? pack16<kF16>(v[4 * i + 2] * inv_b, v[4 * i + 3] * inv_b) : 0u;
-  }
-  lane_transpose4(wa, jj);
-  lane_transpose4(wb, jj);
-  if (live_a) oa[chunk0 + jj] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-  if (live_b) ob[chunk0 + jj] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
-}
-
 // Row r of a tile, as a row of o and lse.
 __device__ __forceinline__ int64_t out_row(const PackedParams& p, int q_row, int pack, int r) {
   const int head_shift = 7 - p.pos_shift;
@@ -346,6 +434,8 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bars;
   __shared__ Shares shares;
+  __shared__ float2 row_ml[kBM];  // find_shares uses it first
+  __shared__ Unit units[kUnits];
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag_s;
   volatile int* abort_flag = &abort_flag_s;
@@ -356,17 +446,25 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_addr(&bars.q_full), 1);
-    mbar_init(smem_addr(&bars.q_free), 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_addr(&bars.k_full[s]), 1);
-      mbar_init(smem_addr(&bars.v_full[s]), 1);
-      mbar_init(smem_addr(&bars.s_full[s]), 1);
-      mbar_init(smem_addr(&bars.p_ready[0][s]), kSoftThreads);
-      mbar_init(smem_addr(&bars.p_ready[1][s]), kSoftThreads);
-      mbar_init(smem_addr(&bars.o_done[s]), 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(smem_addr(&bars.q_full[i]), 1);
+      mbar_init(smem_addr(&bars.q_free[i]), 1 + kEpiThreads / 32);
+      mbar_init(smem_addr(&bars.k_full[i]), 1);
     }
-    mbar_init(smem_addr(&bars.o_free), kSoftThreads);
+    for (int b = 0; b < kScores; ++b) {
+      mbar_init(smem_addr(&bars.v_full[b]), 1);
+      mbar_init(smem_addr(&bars.s_full[b]), 1);
+      mbar_init(smem_addr(&bars.p_ready[0][b]), kSoftThreads);
+      mbar_init(smem_addr(&bars.p_ready[1][b]), kSoftThreads);
+      mbar_init(smem_addr(&bars.o_done[b]), 1);
+    }
+    mbar_init(smem_addr(&bars.o_free), kEpiThreads);
+    mbar_init(smem_addr(&bars.ml_full), kSoftThreads);
+    mbar_init(smem_addr(&bars.ml_free), kEpiThreads);
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(smem_addr(&bars.unit_full[i]), 1);
+      mbar_init(smem_addr(&bars.unit_free[i]), kUnitReaders);
+    }
     mbar_init(smem_addr(&bars.drain[0]), 1);
     mbar_init(smem_addr(&bars.drain[1]), 1);
     abort_flag_s = 0;
@@ -382,147 +480,269 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     tc_fence_before();
   }
   if (threadIdx.x < p.rounds) p.meta[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
-  find_shares(p, &shares);  // its barriers publish the set-up above
+  find_shares(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
   tc_fence_after();
   const uint32_t tbase = tmem_base_slot;
 
-  // Every role walks the same units and counts KV steps g across them: step g
-  // uses ring stage and score buffer g % 3, in round g / 3.
-  Walk walk;
-  walk.begin(p, shares);
-  Unit u;
+  // Every role takes the same units in turn and counts KV steps g across them: step
+  // g uses score buffer and V stage g % 3 and K stage g % 2, unit kt Q buffer kt % 2.
+  //
+  // Unit kt, copied (the fields that the role uses) and let go at once. False:
+  // there is none, or a wait gave up.
+  auto take_unit = [&](int kt, Unit& u) -> bool {
+    const int slot = kt % kUnits;
+    if (!wait_bar(smem_addr(&bars.unit_full[slot]), (kt / kUnits) & 1, kSiteUnitFull)) return false;
+    u = units[slot];
+    mbar_arrive(smem_addr(&bars.unit_free[slot]));
+    return !u.end;
+  };
+  // The same for a whole warp.
+  auto take_unit_warp = [&](int kt, Unit& u) -> bool {
+    const int slot = kt % kUnits;
+    if (!__all_sync(0xffffffffu, wait_bar(smem_addr(&bars.unit_full[slot]), (kt / kUnits) & 1, kSiteUnitFull)))
+      return false;
+    u = units[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&bars.unit_free[slot]));
+    return !u.end;
+  };
+  if (warp >= kProducerWarp && warp < kEpiWarp)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
   if (warp == kProducerWarp) {
-    // ------------------------------------------------------------ producer
+    // ------------------------------------------- walk over the shares, Q and K
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
-      const uint32_t qbar = smem_addr(&bars.q_full);
-      int k_issued = 0, v_issued = 0, q_loads = 0, skipped_v = -1;
-      int key_row[kStages] = {0, 0, 0}, key_head[kStages] = {0, 0, 0};
-      int kt = 0, j = 0;
-      bool have = walk.next(p, shares, u);
-      if (have) j = u.s0;
-      for (int g = 0;; ++g) {
-        // V of step g - kKLead first: it is the load the P V thread waits on soonest
-        const int gv = g - kKLead;
-        if (gv >= 0 && gv < k_issued) {
-          if (gv == p.skip_v_step) {
-            skipped_v = gv;
-          } else {
-            const int s = gv % kStages;
-            const int round = gv / kStages;
-            if (round > 0 && !wait_bar(smem_addr(&bars.o_done[s]), (round - 1) & 1, abort_flag, p.err, kSiteVEmpty))
-              break;
-            const uint32_t vb = smem_addr(&bars.v_full[s]);
-            mbar_expect_tx(vb, L::kTile);
-            for (int h = 0; h < kHalves; ++h)
-              tma_load_3d(sbase + L::kOffV + s * L::kTile + h * kHalf, &tmap_v, vb, h * 64, key_head[s], key_row[s]);
-            v_issued = gv + 1;
-          }
-        }
-        if (!have) {
-          if (gv + 1 >= k_issued) break;
-          continue;
-        }
-        if (j == u.s0) {
-          if (kt > 0 && !wait_bar(smem_addr(&bars.q_free), (kt - 1) & 1, abort_flag, p.err, kSiteQEmpty)) break;
-          mbar_expect_tx(qbar, L::kTile);
-          for (int h = 0; h < kHalves; ++h)
-            tma_load_4d(sbase + L::kOffQ + h * kHalf, &tmap_q, qbar, h * 64, 0, u.pack, u.q_row);
-          ++q_loads;
-        }
-        const int s = g % kStages;
-        const int round = g / kStages;
-        if (round > 0 && !wait_bar(smem_addr(&bars.s_full[s]), (round - 1) & 1, abort_flag, p.err, kSiteKEmpty))
-          break;
-        const uint32_t kb = smem_addr(&bars.k_full[s]);
-        mbar_expect_tx(kb, L::kTile);
-        key_row[s] = u.k_row + kv_tile(u, j) * kBN;
-        key_head[s] = u.pack / p.packs_per_key_head;
+      // K_g goes to its stage when QK_{g-2} is done (s_full)
+      static_assert(kKStages == 2, "sk below lags by two steps");
+      Ring<kKStages> rk;
+      Ring<kScores> sk;
+      Walk walk;
+      walk.begin();
+      Unit u;
+      int kt = 0, g = 0;
+      bool ok = true;
+      OSS_ROLLED
+      for (;; ++kt) {
+        const int slot = kt % kUnits, buf = kt & 1;
+        if (kt >= kUnits && !wait_bar(smem_addr(&bars.unit_free[slot]), (kt / kUnits - 1) & 1, kSiteUnitFree)) break;
+        u.end = 1;
+        const bool have = walk.next(p, shares, u);
+        units[slot] = u;
+        mbar_arrive(smem_addr(&bars.unit_full[slot]));
+        if (!have) break;
+        const uint32_t qb = smem_addr(&bars.q_full[buf]);
+        if (kt >= kKStages && !wait_bar(smem_addr(&bars.q_free[buf]), ((kt >> 1) - 1) & 1, kSiteQEmpty)) break;
+        mbar_expect_tx(qb, L::kTile);
+#pragma unroll
         for (int h = 0; h < kHalves; ++h)
-          tma_load_3d(sbase + L::kOffK + s * L::kTile + h * kHalf, &tmap_k, kb, h * 64, key_head[s], key_row[s]);
-        k_issued = g + 1;
-        if (++j == u.s1) {
-          ++kt;
-          have = walk.next(p, shares, u);
-          if (have) j = u.s0;
+          tma_load_4d(sbase + L::kOffQ + buf * L::kTile + h * kHalf, &tmap_q, qb, h * 64, 0, u.pack, u.q_row);
+        const int head = u.pack / p.packs_per_key_head;
+        OSS_ROLLED
+        for (int j = u.s0; j < u.s1; ++j, ++g, rk.next()) {
+          if (g >= kKStages) {
+            if (!(ok = wait_bar(smem_addr(&bars.s_full[sk.at]), sk.phase, kSiteKEmpty))) break;
+            sk.next();
+          }
+          const uint32_t kb = smem_addr(&bars.k_full[rk.at]);
+          mbar_expect_tx(kb, L::kTile);
+          const int row = u.k_row + kv_tile(u, j) * kBN;
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_3d(sbase + L::kOffK + rk.at * L::kTile + h * kHalf, &tmap_k, kb, h * 64, head, row);
+        }
+        if (!ok) {
+          ++kt;  // its Q load has been issued
+          break;
         }
       }
       // drain: every issued copy must land before the CTA may exit
-      if (q_loads > 0) drain_bar<kKernelAttnPacked>(qbar, (q_loads - 1) & 1, p.err);
-      for (int i = k_issued - 1; i >= 0 && i >= k_issued - kStages; --i)
-        drain_bar<kKernelAttnPacked>(smem_addr(&bars.k_full[i % kStages]), (i / kStages) & 1, p.err);
-      for (int i = v_issued - 1; i >= 0 && i >= v_issued - kStages; --i)
-        if (i != skipped_v)
-          drain_bar<kKernelAttnPacked>(smem_addr(&bars.v_full[i % kStages]), (i / kStages) & 1, p.err);
+      OSS_ROLLED
+      for (int i = max(0, kt - kKStages); i < kt; ++i)
+        drain_phase(smem_addr(&bars.q_full[i & 1]), (i >> 1) & 1, abort_flag);
+      OSS_ROLLED
+      for (int i = max(0, g - kKStages); i < g; ++i)
+        drain_phase(smem_addr(&bars.k_full[i & 1]), (i >> 1) & 1, abort_flag);
+    }
+  } else if (warp == kVWarp) {
+    // ------------------------------------------------------------------- V
+    // V_g goes to its stage when P_{g-3} V is done (o_done). A thread of its own: behind
+    // K it would wait for score buffers and Q buffers that the step it serves
+    // does not need, which in items of a step or two is most of their time.
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
+      Ring<kScores> r;
+      Unit u;
+      int g = 0, skipped = -1;
+      bool ok = true;
+      OSS_ROLLED
+      for (int kt = 0; ok && take_unit(kt, u); ++kt) {
+        const int head = u.pack / p.packs_per_key_head;
+        OSS_ROLLED
+        for (int j = u.s0; j < u.s1; ++j, ++g, r.next()) {
+          if (g >= kScores && !(ok = wait_bar(smem_addr(&bars.o_done[r.at]), r.phase ^ 1, kSiteVEmpty))) break;
+          if (g == p.skip_v_step) {
+            skipped = g;  // test hook: this V tile never arrives
+            continue;
+          }
+          const uint32_t vb = smem_addr(&bars.v_full[r.at]);
+          mbar_expect_tx(vb, L::kTile);
+          const int row = u.k_row + kv_tile(u, j) * kBN;
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_3d(sbase + L::kOffV + r.at * L::kTile + h * kHalf, &tmap_v, vb, h * 64, head, row);
+        }
+      }
+      OSS_ROLLED
+      for (int i = max(0, g - kScores); i < g; ++i)
+        if (i != skipped) drain_phase(smem_addr(&bars.v_full[i % kScores]), (i / kScores) & 1, abort_flag);
     }
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ QK issuer
     if (lane == 0) {
       bool ok = true;
-      const uint64_t dq = smem_desc(sbase + L::kOffQ, 16, 1024);
+      Ring<kScores> r;
+      Ring<kKStages> rk;
       int g = 0;
-      for (int kt = 0; ok && walk.next(p, shares, u); ++kt) {
-        if (!(ok = wait_bar(smem_addr(&bars.q_full), kt & 1, abort_flag, p.err, kSiteQFull))) break;
-        // the previous item's last P V goes through the tensor pipe before this
-        // one's first QK^T: its epilogue waits on it
-        if (kt > 0 && !(ok = wait_bar(smem_addr(&bars.o_done[(g - 1) % kStages]), ((g - 1) / kStages) & 1, abort_flag,
-                                      p.err, kSiteODone)))
-          break;
-        for (int j = u.s0; j < u.s1; ++j, ++g) {
-          const int s = g % kStages;
-          if (!(ok = wait_bar(smem_addr(&bars.k_full[s]), (g / kStages) & 1, abort_flag, p.err, kSiteKFull))) break;
-          if (g >= kStages && !(ok = wait_bar(smem_addr(&bars.o_done[s]), (g / kStages - 1) & 1, abort_flag, p.err,
-                                              kSiteODone)))
-            break;
+      Unit u;
+      OSS_ROLLED
+      for (int kt = 0; ok && take_unit(kt, u); ++kt) {
+        const int buf = kt & 1;
+        if (!(ok = wait_bar(smem_addr(&bars.q_full[buf]), (kt >> 1) & 1, kSiteQFull))) break;
+        const uint64_t dq = smem_desc(sbase + L::kOffQ + buf * L::kTile, 16, 1024);
+        OSS_ROLLED
+        for (int j = u.s0; j < u.s1; ++j, ++g, r.next(), rk.next()) {
+          if (!(ok = wait_bar(smem_addr(&bars.k_full[rk.at]), rk.phase, kSiteKFull))) break;
+          if (g >= kScores && !(ok = wait_bar(smem_addr(&bars.o_done[r.at]), r.phase ^ 1, kSiteODone))) break;
           tc_fence_after();
-          const uint64_t dk = smem_desc(sbase + L::kOffK + s * L::kTile, 16, 1024);
-          const uint32_t d_s = tbase + col_s(s);
+          const uint64_t dk = smem_desc(sbase + L::kOffK + rk.at * L::kTile, 16, 1024);
+          const uint32_t d_s = tbase + col_s(r.at);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_ss(d_s, dq + kstep_kmajor(kk, kHalf), dk + kstep_kmajor(kk, kHalf), kIdescQK, kk > 0 ? 1u : 0u);
-          tc_commit(smem_addr(&bars.s_full[s]));
+          tc_commit(smem_addr(&bars.s_full[r.at]));
         }
-        if (ok) tc_commit(smem_addr(&bars.q_free));
+        if (ok) tc_commit(smem_addr(&bars.q_free[buf]));
       }
       tc_commit(smem_addr(&bars.drain[0]));
-      drain_bar<kKernelAttnPacked>(smem_addr(&bars.drain[0]), 0, p.err);
+      drain_phase(smem_addr(&bars.drain[0]), 0, abort_flag);
     }
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------ PV issuer
     if (lane == 0) {
       bool ok = true;
       const uint32_t d_o = tbase + kColO;
-      int g = 0;
-      for (int kt = 0; ok && walk.next(p, shares, u); ++kt) {
-        for (int j = u.s0; j < u.s1; ++j, ++g) {
-          const int s = g % kStages;
-          if (!(ok = wait_bar(smem_addr(&bars.v_full[s]), (g / kStages) & 1, abort_flag, p.err, kSiteVFull))) break;
-          if (j == u.s0 && kt > 0 &&
-              !(ok = wait_bar(smem_addr(&bars.o_free), (kt - 1) & 1, abort_flag, p.err, kSiteOFree)))
-            break;
-          const uint64_t dv = smem_desc(sbase + L::kOffV + s * L::kTile, kHalf, 1024);
-          const uint32_t a_p = tbase + col_s(s);
-#pragma unroll
-          for (int hp = 0; hp < 2; ++hp) {
-            if (!(ok = wait_bar(smem_addr(&bars.p_ready[hp][s]), (g / kStages) & 1, abort_flag, p.err, kSitePReady)))
-              break;
+      Ring<kScores> r;
+      Unit u;
+      OSS_ROLLED
+      for (int kt = 0; ok && take_unit(kt, u); ++kt) {
+        OSS_ROLLED
+        for (int j = u.s0; j < u.s1; ++j, r.next()) {
+          if (!(ok = wait_bar(smem_addr(&bars.v_full[r.at]), r.phase, kSiteVFull))) break;
+          if (j == u.s0 && kt > 0 && !(ok = wait_bar(smem_addr(&bars.o_free), (kt - 1) & 1, kSiteOFree))) break;
+          const uint64_t dv = smem_desc(sbase + L::kOffV + r.at * L::kTile, kHalf, 1024);
+          const uint32_t a_p = tbase + col_s(r.at);
+          OSS_ROLLED
+          for (int hp = 0; hp < 2; ++hp) {  // keys 0..63, 64..127 of the tile
+            if (!(ok = wait_bar(smem_addr(&bars.p_ready[hp][r.at]), r.phase, kSitePReady))) break;
             tc_fence_after();
 #pragma unroll
-            for (int kk = 4 * hp; kk < 4 * hp + 4; ++kk)
-              mma_ts(d_o, a_p + kk * 8, dv + static_cast<uint64_t>(kk * (2048 >> 4)), kIdescPV,
-                     (j > u.s0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(d_o, a_p + (4 * hp + kk) * 8, dv + static_cast<uint64_t>((4 * hp + kk) * (2048 >> 4)), kIdescPV,
+                     (j > u.s0 || hp > 0 || kk > 0) ? 1u : 0u);
           }
           if (!ok) break;
-          tc_commit(smem_addr(&bars.o_done[s]));
+          tc_commit(smem_addr(&bars.o_done[r.at]));
         }
       }
       tc_commit(smem_addr(&bars.drain[1]));
-      drain_bar<kKernelAttnPacked>(smem_addr(&bars.drain[1]), 0, p.err);
+      drain_phase(smem_addr(&bars.drain[1]), 0, abort_flag);
     }
-  } else {
+  } else if (warp >= kEpiWarp) {
+    // ------------------------------------------------------------ epilogue
+    // Thread: one row, 32 dims at a time. The scaled and rounded rows go to the
+    // item's Q buffer, which nothing reads any more (128-byte rows, chunks swizzled), and
+    // from there out in whole rows: stores of 16 bytes a row straight from here
+    // kept the load/store unit busy for as long as a KV step, and the softmax warps'
+    // barriers with it. Rolled loops: this code shares the instruction cache with
+    // the softmax's.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int row0 = (warp - kEpiWarp) * 32;
+    const uint32_t t_o = tbase + (static_cast<uint32_t>(row0) << 16) + kColO;
+    const int head_shift = 7 - p.pos_shift;
+    bool ok = true;
+    int g = 0;  // steps of the items so far
+    Unit u;
+    OSS_ROLLED
+    for (int kt = 0; ok && take_unit_warp(kt, u); ++kt) {
+      g += u.s1 - u.s0;
+      ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.ml_full), kt & 1, kSiteMlFull));
+      if (!ok) break;
+      const float2 ml = row_ml[row0 + lane];
+      mbar_arrive(smem_addr(&bars.ml_free));
+      ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.o_done[(g - 1) % kScores]), ((g - 1) / kScores) & 1, kSiteODone));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t stage = sbase + L::kOffQ + (kt & 1) * L::kTile + (warp - kEpiWarp) * (L::kTile / 4);  // [half][32 rows][128 bytes]
+      if (u.s0 == 0 && u.s1 == u.n_kv) {
+        // (a row without keys has O = 0: its weights are zeros and V is finite)
+        const float inv = ml.y > 0.f ? 1.0f / ml.y : 0.f;
+        OSS_ROLLED
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32x32_x32(t_o + 32 * c, v);
+          tmem_ld_wait(v);
+          const uint32_t dst = stage + (c >> 1) * (32 * 128) + lane * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack16<kF16>(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
+            st_shared_u4(dst + (((4 * (c & 1) + i) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(smem_addr(&bars.o_free));  // the next item's first P V may overwrite O
+        __syncwarp();
+        constexpr int kChunks = D / 8;
+#pragma unroll 4
+        for (int i = lane; i < 32 * kChunks; i += 32) {
+          const int row = i / kChunks, c = i % kChunks;
+          const uint4 x = ld_shared_u4(stage + (c >> 3) * (32 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+          if (((row0 + row) >> head_shift) < u.n_pos)
+            reinterpret_cast<uint4*>(p.o + out_row(p, u.q_row, u.pack, row0 + row) * D)[c] = x;
+        }
+        __syncwarp();
+        if (p.lse && ((row0 + lane) >> head_shift) < u.n_pos)
+          p.lse[out_row(p, u.q_row, u.pack, row0 + lane)] = ml.y > 0.f ? (ml.x + __log2f(ml.y)) * kLn2 : neg_inf();
+      } else {
+        const int64_t slot = 2 * static_cast<int64_t>(u.share) + (u.s0 == 0 ? 1 : 0);
+        float4* dst = p.part_o + slot * (D / 4) * kBM + row0 + lane;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32x32_x32(t_o + 32 * c, v);
+          tmem_ld_wait(v);
+          if (c == D / 32 - 1) {
+            tc_fence_before();
+            mbar_arrive(smem_addr(&bars.o_free));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[(8 * c + i) * kBM] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+        }
+        p.part_ml[slot * kBM + row0 + lane] = ml;
+        if (u.parts > 0 && threadIdx.x == kEpiWarp * 32) p.meta[u.share] = make_int4(u.parts, u.q_row, u.n_pos, u.pack);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next Q tile lands where O's rows were
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&bars.q_free[kt & 1]));
+    }
+  } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // Warp w owns rows 32 (w % 4) + 16 (w / 4) .. + 15; thread t holds rows
     // ra = t/4 and rb = 8 + t/4 of them, columns 8k + cq + {0, 1}.
     const int lane0 = (warp & 3) * 32 + (warp >> 2) * 16;
@@ -534,17 +754,19 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const uint32_t tl = tbase + (static_cast<uint32_t>(lane0) << 16);
     const float C = p.C;
     bool ok = true;
-    int g = 0;
-    while (ok && walk.next(p, shares, u)) {
+    Ring<kScores> r, before;  // of this step and of the one before
+    Unit u;
+    OSS_ROLLED
+    for (int kt = 0; ok && take_unit_warp(kt, u); ++kt) {
       float m_a = neg_inf(), m_b = neg_inf();  // reference maxima, base 2
       float l_a = 0.f, l_b = 0.f;              // this thread's share of the row sums
       const int vis_a = p.causal ? min(u.k_len, u.vis + pos_a) : u.k_len;  // keys the rows see
       const int vis_b = p.causal ? min(u.k_len, u.vis + pos_b) : u.k_len;
-      for (int j = u.s0; j < u.s1; ++j, ++g) {
-        const int b = g % kStages;
+      OSS_ROLLED
+      for (int j = u.s0; j < u.s1; ++j, before = r, r.next()) {
+        const int b = r.at;
         const uint32_t colS = col_s(b);
-        ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.s_full[b]), (g / kStages) & 1, abort_flag, p.err,
-                                              kSiteSFull));
+        ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.s_full[b]), r.phase, kSiteSFull));
         if (!ok) break;
         tc_fence_after();
         uint32_t r0[32], r1[32];
@@ -598,8 +820,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (rescale && j > u.s0) {
           // wait for P_{j-1} V (its completion implies every earlier one), then
           // rescale this warp's rows of O
-          ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.o_done[(g - 1) % kStages]), ((g - 1) / kStages) & 1,
-                                                abort_flag, p.err, kSiteODone));
+          ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.o_done[before.at]), before.phase, kSiteODone));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -624,8 +845,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (key0 + kBN > u.k_len) {
           // rows of V behind the sequence's keys: zeros (a 16-byte chunk's place
           // in its 128-byte row does not matter for them)
-          ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.v_full[b]), (g / kStages) & 1, abort_flag, p.err,
-                                                kSiteVFull));
+          ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.v_full[r.at]), r.phase, kSiteVFull));
           if (!ok) break;
           const int first = max(0, u.k_len - key0);
           uint8_t* vt = smem_raw + (sbase - smem_addr(smem_raw)) + L::kOffV + b * L::kTile;
@@ -666,122 +886,75 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
       l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
       l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-      if (ok)
-        ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.o_done[(g - 1) % kStages]), ((g - 1) / kStages) & 1,
-                                              abort_flag, p.err, kSiteODone));
-      if (ok) {
-        tc_fence_after();
-        if (u.s0 == 0 && u.s1 == u.n_kv) {
-          const bool live_a = pos_a < u.n_pos, live_b = pos_b < u.n_pos;
-          const float inv_a = (l_a > 0.f) ? 1.0f / l_a : 0.f;
-          const float inv_b = (l_b > 0.f) ? 1.0f / l_b : 0.f;
-          const int64_t row_a = out_row(p, u.q_row, u.pack, ra), row_b = out_row(p, u.q_row, u.pack, rb);
-          uint4* oa = reinterpret_cast<uint4*>(p.o + row_a * D);
-          uint4* ob = reinterpret_cast<uint4*>(p.o + row_b * D);
-#pragma unroll 1
-          for (int h = 0; h < kHalves; ++h) {
-            uint32_t ov[32];
-            tmem_ld16x256_x8(tl + kColO + 64 * h, ov);
-            tmem_ld_wait(ov);
-#pragma unroll
-            for (int mb = 0; mb < 2; ++mb) {
-              float v[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(ov[16 * mb + i]);
-              store_chunks<kF16>(oa, ob, v, inv_a, inv_b, 8 * h + 4 * mb, lane & 3, live_a, live_b);
-            }
-          }
-          if ((lane & 3) == 0 && p.lse) {
-            if (live_a) p.lse[row_a] = (l_a > 0.f) ? (m_a + log2f(l_a)) * kLn2 : neg_inf();
-            if (live_b) p.lse[row_b] = (l_b > 0.f) ? (m_b + log2f(l_b)) * kLn2 : neg_inf();
-          }
-        } else {
-          // a part of an item: unnormalised, every warp access 512 contiguous bytes
-          const int64_t slot = 2 * static_cast<int64_t>(u.share) + (u.s0 == 0 ? 1 : 0);
-          float4* wo = p.part_o + slot * (D / 8) * kSoftThreads + threadIdx.x;
-#pragma unroll 1
-          for (int h = 0; h < kHalves; ++h) {
-            uint32_t ov[32];
-            tmem_ld16x256_x8(tl + kColO + 64 * h, ov);
-            tmem_ld_wait(ov);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              wo[(8 * h + e) * kSoftThreads] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
-                                                           __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
-          }
-          p.part_ml[slot * kSoftThreads + threadIdx.x] = make_float4(m_a, l_a, m_b, l_b);
-          if (u.s0 == 0 && threadIdx.x == 0) {
-            const int64_t last = last_boundary(u.w + kTileWeight + u.n_kv - kMinSteps, shares.total, shares.count);
-            p.meta[u.share] = make_int4(static_cast<int>(last) - u.share + 1, u.q_row, u.n_pos, u.pack);
-          }
-        }
+      if (!ok) break;
+      if (kt > 0) {
+        ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.ml_free), (kt - 1) & 1, kSiteMlFree));
+        if (!ok) break;
       }
-      tc_fence_before();
-      mbar_arrive(smem_addr(&bars.o_free));
+      if ((lane & 3) == 0) {
+        row_ml[ra] = make_float2(m_a, l_a);
+        row_ml[rb] = make_float2(m_b, l_b);
+      }
+      mbar_arrive(smem_addr(&bars.ml_full));
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) report_error(p.err, kKernelAttnPacked | (static_cast<unsigned>(*abort_flag) << 8));
   if (warp == kQkWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTmemCols) : "memory");
   }
 }
 
-// The join: CTA (share, quarter) merges 32 dims of the item that is cut at the
-// share's end. Part 0 lies in slot 2 share + 1, part i in slot 2 (share + i).
+// The join: CTA (share, c) merges dims 32 c .. 32 c + 31 of the item that is
+// cut at the share's end. Part 0 lies in slot 2 share + 1, part i in slot 2 (share
+// + i). Thread: a row, 16 dims.
+constexpr int kJoinThreads = 2 * kBM;
+
 template <int D, bool kF16>
-__global__ void __launch_bounds__(kSoftThreads) attn_packed_join_kernel(const PackedParams p) {
+__global__ void __launch_bounds__(kJoinThreads) attn_packed_join_kernel(const PackedParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int share = blockIdx.x, mb = blockIdx.y;
+  const int share = blockIdx.x;
   const int4 meta = p.meta[share];
   const int parts = meta.x;
   if (parts == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lane0 = (warp & 3) * 32 + (warp >> 2) * 16;
-  const int ra = lane0 + (lane >> 2), rb = ra + 8;
+  const int row = threadIdx.x & (kBM - 1), q4 = 8 * blockIdx.y + 4 * (threadIdx.x >> 7);  // first vector of 4 dims
+  if ((row >> (7 - p.pos_shift)) >= meta.z) return;
   auto slot = [&](int i) -> int64_t { return 2 * (static_cast<int64_t>(share) + i) + (i == 0 ? 1 : 0); };
-  float M_a = neg_inf(), M_b = neg_inf();
-  for (int i = 0; i < parts; ++i) {
-    const float4 st = p.part_ml[slot(i) * kSoftThreads + threadIdx.x];
-    M_a = fmaxf(M_a, st.x);
-    M_b = fmaxf(M_b, st.z);
-  }
-  float L_a = 0.f, L_b = 0.f, acc[16];
+  float M = neg_inf();
+  for (int i = 0; i < parts; ++i) M = fmaxf(M, p.part_ml[slot(i) * kBM + row].x);
+  float L = 0.f, acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 0; i < parts; ++i) {
-    const int64_t s = slot(i);
-    const float4 st = p.part_ml[s * kSoftThreads + threadIdx.x];
-    const float4* src = p.part_o + (s * (D / 8) + 4 * mb) * kSoftThreads + threadIdx.x;
+    const float2 ml = p.part_ml[slot(i) * kBM + row];
+    const float4* src = p.part_o + (slot(i) * (D / 4) + q4) * kBM + row;
     float4 v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = src[e * kSoftThreads];
-    // a part whose rows see none of its keys has m = -inf and adds nothing
-    const float fa = st.x == neg_inf() ? 0.f : ex2(st.x - M_a);
-    const float fb = st.z == neg_inf() ? 0.f : ex2(st.z - M_b);
-    L_a = fmaf(st.y, fa, L_a);
-    L_b = fmaf(st.w, fb, L_b);
+    for (int e = 0; e < 4; ++e) v[e] = src[e * kBM];
+    // a part in which the row sees no key has m = -inf and adds nothing
+    if (ml.x == neg_inf()) continue;
+    const float f = ex2(ml.x - M);
+    L = fmaf(ml.y, f, L);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      acc[4 * e] = fmaf(v[e].x, fa, acc[4 * e]);
-      acc[4 * e + 1] = fmaf(v[e].y, fa, acc[4 * e + 1]);
-      acc[4 * e + 2] = fmaf(v[e].z, fb, acc[4 * e + 2]);
-      acc[4 * e + 3] = fmaf(v[e].w, fb, acc[4 * e + 3]);
+      acc[4 * e] = fmaf(v[e].x, f, acc[4 * e]);
+      acc[4 * e + 1] = fmaf(v[e].y, f, acc[4 * e + 1]);
+      acc[4 * e + 2] = fmaf(v[e].z, f, acc[4 * e + 2]);
+      acc[4 * e + 3] = fmaf(v[e].w, f, acc[4 * e + 3]);
     }
   }
-  const int head_shift = 7 - p.pos_shift;
-  const bool live_a = (ra >> head_shift) < meta.z, live_b = (rb >> head_shift) < meta.z;
-  const float inv_a = L_a > 0.f ? 1.f / L_a : 0.f, inv_b = L_b > 0.f ? 1.f / L_b : 0.f;
-  const int64_t row_a = out_row(p, meta.y, meta.w, ra), row_b = out_row(p, meta.y, meta.w, rb);
-  store_chunks<kF16>(reinterpret_cast<uint4*>(p.o + row_a * D), reinterpret_cast<uint4*>(p.o + row_b * D), acc, inv_a,
-                     inv_b, 4 * mb, lane & 3, live_a, live_b);
-  if (mb == 0 && (lane & 3) == 0 && p.lse) {
-    if (live_a) p.lse[row_a] = L_a > 0.f ? (M_a + log2f(L_a)) * kLn2 : neg_inf();
-    if (live_b) p.lse[row_b] = L_b > 0.f ? (M_b + log2f(L_b)) * kLn2 : neg_inf();
-  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int64_t at = out_row(p, meta.y, meta.w, row);
+  uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + 4 * q4);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    dst[i] = make_uint4(pack16<kF16>(acc[8 * i] * inv, acc[8 * i + 1] * inv), pack16<kF16>(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
+                        pack16<kF16>(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv), pack16<kF16>(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
+  if (q4 == 0 && p.lse) p.lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
 }
 
 // ---------------------------------------------------------------------------
@@ -861,7 +1034,7 @@ cudaError_t launch_shape(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas * p.rounds, D / 32);
-  cfg.blockDim = dim3(kSoftThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -887,8 +1060,7 @@ int64_t attn_packed_workspace_bytes(int64_t tokens_k, int Hkv, int D) {
   const int sms = device_sms();
   if (sms < 1) return -1;
   const int64_t shares = static_cast<int64_t>(sms) * round_count(tokens_k, Hkv, D);
-  return round256(2 * shares * (D / 8) * kSoftThreads * 16) + round256(2 * shares * kSoftThreads * 16) +
-         round256(shares * 16);
+  return round256(2 * shares * D * kBM * 4) + round256(2 * shares * kBM * 8) + round256(shares * 16);
 }
 
 cudaError_t launch_attn_packed(const PackedArgs& a, void* workspace, unsigned int* err, const AttnFault& fault,
@@ -929,16 +1101,15 @@ cudaError_t launch_attn_packed(const PackedArgs& a, void* workspace, unsigned in
   p.C = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634074);
   p.causal = a.causal ? 1 : 0;
   p.err = err;
-  p.timeout_ns = fault.timeout_ns > 0 ? static_cast<uint64_t>(fault.timeout_ns) : kTimeoutNs;
-  static std::atomic<unsigned int> launches{0};
-  p.tag = launches.fetch_add(1, std::memory_order_relaxed) % 65535u + 1u;
+  const uint64_t timeout_ns = fault.timeout_ns > 0 ? static_cast<uint64_t>(fault.timeout_ns) : kTimeoutNs;
+  p.wait_cycles = static_cast<uint32_t>(timeout_ns < kTimeoutNs ? timeout_ns * 2 : kTimeoutNs * 2);  // about 2 GHz
   p.skip_v_step = fault.skip_v_step;
   const int64_t shares = static_cast<int64_t>(sms) * p.rounds;
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float4*>(ws);
-  ws += round256(2 * shares * (a.D / 8) * kSoftThreads * 16);
-  p.part_ml = reinterpret_cast<float4*>(ws);
-  ws += round256(2 * shares * kSoftThreads * 16);
+  ws += round256(2 * shares * a.D * kBM * 4);
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  ws += round256(2 * shares * kBM * 8);
   p.meta = reinterpret_cast<int4*>(ws);
   if (a.D == 128)
     return a.f16 ? launch_shape<128, true>(mq, mk, mv, p, sms, stream) : launch_shape<128, false>(mq, mk, mv, p, sms, stream);

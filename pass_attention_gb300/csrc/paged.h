@@ -5,10 +5,14 @@
 
 #include <cstdint>
 
+// OSS_ROLLED: a loop that is not to be unrolled (what runs once per call should
+// not push a kernel's main loop out of the instruction cache).
 #if defined(__CUDACC__)
 #define OSS_HD __host__ __device__ __forceinline__
+#define OSS_ROLLED _Pragma("unroll 1")
 #else
 #define OSS_HD inline
+#define OSS_ROLLED
 #endif
 
 namespace oss {

@@ -19,7 +19,8 @@ constexpr uint64_t kDrainNs = 200000000ull;     // 0.2 s to drain own copies
 // wait sites (error word bits 8..15)
 enum Site : unsigned int {
   kSiteQFull = 1, kSiteKFull, kSiteVFull, kSiteKEmpty, kSiteVEmpty,
-  kSiteSFull, kSitePReady, kSiteODone, kSiteDrain, kSiteQEmpty, kSiteOFree
+  kSiteSFull, kSitePReady, kSiteODone, kSiteDrain, kSiteQEmpty, kSiteOFree, kSiteMlFull, kSiteMlFree,
+  kSiteUnitFull, kSiteUnitFree
 };
 
 // ---------------------------------------------------------------------------
@@ -187,6 +188,16 @@ __device__ __forceinline__ void tmem_st_wait() {
 __device__ __forceinline__ void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : OSS_R8(0), OSS_R8(8), OSS_R8(16), OSS_R8(24)
+      : "r"(taddr));
+}
+
+// 32 lanes x 32 columns: thread t holds columns 0 .. 31 of lane t.
+__device__ __forceinline__ void tmem_ld32x32_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : OSS_R8(0), OSS_R8(8), OSS_R8(16), OSS_R8(24)

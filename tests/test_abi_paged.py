@@ -289,6 +289,7 @@ int main() {
     if (!items) continue;
     const int n = share_count(total, items, ctas, rounds);
     assert(n >= 1 && n <= ctas * rounds && n <= total && (n <= ctas || n % ctas == 0));
+    const ShareCut cut = share_cut(total, n);
     struct Item { int64_t w; int steps; };
     std::vector<Item> all;
     int64_t w = 0;
@@ -302,13 +303,13 @@ int main() {
     std::vector<std::pair<int, int>> at;
     size_t i = 0;
     for (int c = 0; c < n; ++c) {
-      const int64_t x = share_begin(c, total, n);
+      const int64_t x = share_begin(cut, c);
       while (i + 1 < all.size() && all[i + 1].w <= x) ++i;
       const int st = cut_step(x - all[i].w, all[i].steps);
       at.push_back(st == all[i].steps ? std::make_pair(static_cast<int>(i) + 1, 0) : std::make_pair(static_cast<int>(i), st));
     }
     at.push_back({static_cast<int>(all.size()), 0});
-    assert(share_begin(n, total, n) == total);
+    assert(share_begin(cut, n) == total);
     assert(at[0].first == 0 && at[0].second == 0);
     for (int c = 0; c < n; ++c) {
       assert(at[c] <= at[c + 1]);
@@ -317,12 +318,26 @@ int main() {
       assert(e.second >= kMinSteps && all[e.first].steps - e.second >= kMinSteps);
       if (at[c].first == e.first && at[c].second > 0) continue;
       // the item begins in share c and is cut at its end: its parts
-      const int64_t last = last_boundary(all[e.first].w + kTileWeight + all[e.first].steps - kMinSteps, total, n);
+      const int64_t last = last_boundary(cut, all[e.first].w + kTileWeight + all[e.first].steps - kMinSteps);
       int parts = 1;
       for (int d = c + 1; d < n; ++d) parts += at[d].first == e.first && at[d].second > 0;
       assert(parts == last - c + 1);
       for (int d = c + 1; d <= last; ++d) assert(at[d].first == e.first && at[d].second > 0 && at[d] < at[d + 1]);
     }
+  }
+  // cuts of long rows, and small quotients
+  for (int it = 0; it < 20000; ++it) {
+    const int64_t total = (int64_t(rand()) << (rand() % 20)) + rand() % 1000 + 1300;
+    const int n = 1 + rand() % 1216;
+    const ShareCut cut = share_cut(total, n);
+    assert(share_begin(cut, 0) == 0 && share_begin(cut, n) == total);
+    const int c = rand() % n;
+    const int64_t x = share_begin(cut, c);
+    assert(x < share_begin(cut, c + 1));
+    assert(last_boundary(cut, x) == static_cast<uint32_t>(c));
+    assert(last_boundary(cut, share_begin(cut, c + 1) - 1) == static_cast<uint32_t>(c));
+    const int64_t y = 1 + (int64_t(rand()) << (rand() % 12)), q = rand() % 65536;
+    assert(small_quotient(q * y + rand() % y, y) == q);
   }
   std::puts("ok");
 }
