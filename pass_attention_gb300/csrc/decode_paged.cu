@@ -22,7 +22,12 @@
 // of the bytes whatever the lengths are, from lengths that only the device
 // knows. An item inside one share is finished there; one that crosses shares
 // leaves partial states (m, l, O), which a second kernel joins in share order.
-// No atomics: every run gives the same bits.
+// No atomics: every run gives the same bits. Short caches (kWholeKeys) are not cut:
+// an item is one unit then, and there is nothing to join.
+//
+// With weights, the first kernel leaves its scores in the workspace, and the second
+// one, beside the joins, adds 2^(s - lse) to the sums: 4 bytes a head against
+// the 2 D of reading the key again.
 //
 // Each of a CTA's four warps streams tiles of 16 keys (every fourth one of its
 // segment) through its own ring in shared memory, by 16-byte asynchronous
@@ -45,6 +50,10 @@ constexpr int kTileKeys = 16;
 constexpr int kUnitTiles = kWarps;  // a unit: one tile per warp
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxHeadBlock = 16;
+// A page table that holds this many tokens or fewer is not cut into shares: the
+// second launch costs more than one CTA takes for them (a decode step of one
+// sequence of 333 tokens, 32 heads over 8: WHOLE_FIGURES).
+constexpr int kWholeKeys = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 // The reference maximum moves only when a score exceeds it by more than
 // 2^kSlack: any reference gives the same quotient O / l, and weights up to 2^8 are
@@ -68,6 +77,7 @@ struct DecodeParams {
   const uint16_t* q;
   int64_t ld_q_batch, ld_q_head;
   int32_t H, group, head_blocks, block_heads;  // block_heads: 8 or 16
+  int32_t unit_tiles;                          // tiles of a unit: 4, or all of an item
   float scale2;                                // scale * log2(e)
   uint16_t* o;
   float* lse;
@@ -75,8 +85,10 @@ struct DecodeParams {
   float* part_o;    // [2 N][block_heads][D]
   float2* part_ml;  // [2 N][block_heads]
   int4* meta;       // [N]: {sequence, key head and head block, parts, first slot}
-  float* lse2;      // [batch][H], base 2 (only with scores)
-  float* scores;    // [batch][heads * head_blocks][capacity][block_heads], or null
+  float* lse2;      // [batch][H], base 2: of items that were not cut (only with scores)
+  int2* item_meta;  // [batch][heads * head_blocks]: {first share, parts} (only with scores)
+  float* scores;    // [batch][heads * head_blocks][capacity][score_heads], or null
+  int32_t score_heads;
   unsigned int* err;
 };
 
@@ -134,7 +146,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Units [r0, r1) of an item: 64-key units of sequence b for key head and head block j.
+// Units [r0, r1) of an item: sequence b, key head and head block j.
 struct Segment {
   int b, j, len, units, r0, r1;
 };
@@ -144,7 +156,9 @@ struct Walk {
   Segment s;
   int64_t u, end;
 
-  __device__ __forceinline__ static int units_of(int len) {  // an empty sequence has one, to be answered
+  // (an empty sequence has a unit, to be answered)
+  __device__ __forceinline__ static int units_of(const DecodeParams& p, int len) {
+    if (p.unit_tiles != kUnitTiles) return 1;
     const int n = (len + kTileKeys * kUnitTiles - 1) / (kTileKeys * kUnitTiles);
     return n > 0 ? n : 1;
   }
@@ -160,15 +174,15 @@ struct Walk {
       s.j = 0;
       ++s.b;
       s.len = paged_length(p.c.kv_len[s.b], p.c.max_pages, p.c.page_shift);
-      s.units = units_of(s.len);
+      s.units = units_of(p, s.len);
     }
     s.r0 = 0;
     clip();
     return true;
   }
   // One past the last tile of the segment that holds a key.
-  __device__ __forceinline__ int tile_end() const {
-    return min(s.r1 * kUnitTiles, (s.len + kTileKeys - 1) / kTileKeys);
+  __device__ __forceinline__ int tile_end(const DecodeParams& p) const {
+    return min(s.r1 * p.unit_tiles, (s.len + kTileKeys - 1) / kTileKeys);
   }
 };
 
@@ -183,7 +197,7 @@ __device__ bool find_share(const DecodeParams& p, Walk* w, int64_t* total_units,
   const int b0 = min(p.c.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.c.batch, b0 + per);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b)
-    mine += Walk::units_of(paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift));
+    mine += Walk::units_of(p, paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift));
   int64_t upto = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -209,7 +223,7 @@ __device__ bool find_share(const DecodeParams& p, Walk* w, int64_t* total_units,
     int64_t at = before * per_seq;
     for (int b = b0; b < b1; ++b) {
       const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
-      const int units = Walk::units_of(len);
+      const int units = Walk::units_of(p, len);
       if (first < at + static_cast<int64_t>(units) * per_seq) {
         Walk f;
         f.s.b = b;
@@ -258,13 +272,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
 
   // ---- the loads' cursor: the tile to be loaded next, and its page
   Walk lw = w;
-  int lt = lw.s.r0 * kUnitTiles + warp;
+  int lt = lw.s.r0 * p.unit_tiles + warp;
   bool more = true;
   int page = 0;
   auto settle = [&]() {  // move to the next tile that exists, fetch its page number
-    while (lt >= lw.tile_end()) {
+    while (lt >= lw.tile_end(p)) {
       if (!(more = lw.next(p))) return;
-      lt = lw.s.r0 * kUnitTiles + warp;
+      lt = lw.s.r0 * p.unit_tiles + warp;
     }
     page = p.c.table[static_cast<int64_t>(lw.s.b) * p.c.ld_table + ((lt * kTileKeys) >> p.c.page_shift)];
   };
@@ -330,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) od[nt][i][e] = 0.f;
     }
-    const int t_end = w.tile_end();
-    for (int t = s.r0 * kUnitTiles + warp; t < t_end; t += kUnitTiles) {
+    const int t_end = w.tile_end(p);
+    for (int t = s.r0 * p.unit_tiles + warp; t < t_end; t += kUnitTiles) {
       copy_wait<kStages - 1>();
       __syncwarp();
       const uint32_t kt = ring + stage * S::kStageBytes, vt = kt + S::kTileBytes;
@@ -363,12 +377,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
       }
       if (p.scores) {
         const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
-        float* out = p.scores + ((static_cast<int64_t>(s.b) * p.c.heads * p.head_blocks + s.j) * cap + key) * p.block_heads + 2 * quad;
+        float* out = p.scores + ((static_cast<int64_t>(s.b) * p.c.heads * p.head_blocks + s.j) * cap + key) * p.score_heads + 2 * quad;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          if (8 * nt + 2 * quad >= p.score_heads) continue;
           if (key < s.len) *reinterpret_cast<float2*>(out + nt * 8) = make_float2(sc[nt][0], sc[nt][1]);
           if (key + 8 < s.len)
-            *reinterpret_cast<float2*>(out + 8 * p.block_heads + nt * 8) = make_float2(sc[nt][2], sc[nt][3]);
+            *reinterpret_cast<float2*>(out + 8 * p.score_heads + nt * 8) = make_float2(sc[nt][2], sc[nt][3]);
         }
       }
 #pragma unroll
@@ -427,11 +442,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
     // ---- the four warps' states, 8 heads at a time
     const bool whole = s.r0 == 0 && s.r1 == s.units;
     const int slot = 2 * blockIdx.x + (s.r0 == 0 ? 1 : 0);
-    if (!whole && s.r0 == 0 && threadIdx.x == 0) {
-      // the item's last unit lies in the last of its shares
-      const int64_t x = w.u + s.units - 1;
-      const int last = static_cast<int>(((x + 1) * shares - 1) / W);
-      p.meta[blockIdx.x] = make_int4(s.b, s.j, last - static_cast<int>(blockIdx.x) + 1, slot);
+    if (s.r0 == 0 && threadIdx.x == 0) {
+      int parts = 1;
+      if (!whole) {
+        // the item's last unit lies in the last of its shares
+        const int64_t x = w.u + s.units - 1;
+        parts = static_cast<int>(((x + 1) * shares - 1) / W) - static_cast<int>(blockIdx.x) + 1;
+        p.meta[blockIdx.x] = make_int4(s.b, s.j, parts, slot);
+      }
+      if (p.scores)
+        p.item_meta[static_cast<int64_t>(s.b) * p.c.heads * p.head_blocks + s.j] = make_int2(blockIdx.x, parts);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -511,43 +531,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   copy_wait<0>();
 }
 
-// The join: CTA (c, hh) merges head hh of the item that begins in share c and
-// goes on into the next ones. Its warps take the parts in turn.
-constexpr int kJoinWarps = 8;
+// The second kernel. Its first CTAs join: CTA (c, hh) merges head hh of the item
+// that begins in share c and goes on into the next ones; its warps take the
+// parts in turn. The others, with weights, add up: kAddKeys keys of one key head.
+constexpr int kFinishThreads = 256;
+constexpr int kFinishWarps = kFinishThreads / 32;
+constexpr int kAddKeysPerThread = 4;
+constexpr int kAddKeys = kAddKeysPerThread * kFinishThreads;
+
+// Slot of part i of an item that begins in share c: part 0 in 2 c + 1, part i > 0 in 2 (c + i).
+__device__ __forceinline__ int64_t part_slot(int c, int i) {
+  return 2 * (static_cast<int64_t>(c) + i) + (i == 0 ? 1 : 0);
+}
 
 template <bool kF16, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeParams p) {
+__device__ __forceinline__ void join_head(const DecodeParams& p, int share, int hh) {
   constexpr int kDims = D / 32;
-  __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
-  let_next_kernel_start();
-  wait_for_previous_kernel();
-  const int4 meta = p.meta[blockIdx.x];
+  __shared__ float sm[kFinishWarps], sl[kFinishWarps], so[kFinishWarps][D];
+  const int4 meta = p.meta[share];
   const int parts = meta.z;
   if (parts == 0) return;
   const int g = meta.y / p.head_blocks, hb = meta.y - g * p.head_blocks;
-  const int hh = blockIdx.y;
   if (hh >= min(p.block_heads, p.group - hb * p.block_heads)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // part 0 in slot 2 c + 1, part i > 0 in slot 2 (c + i)
-  auto slot = [&](int i) -> int64_t {
-    const int64_t s = i == 0 ? meta.w : 2 * (static_cast<int>(blockIdx.x) + i);
-    return s * p.block_heads + hh;
-  };
   float M = neg_inf(), L = 0.f, acc[kDims];
 #pragma unroll
   for (int k = 0; k < kDims; ++k) acc[k] = 0.f;
   constexpr int kBatch = 4;
-  for (int i0 = warp; i0 < parts; i0 += kJoinWarps * kBatch) {
+  for (int i0 = warp; i0 < parts; i0 += kFinishWarps * kBatch) {
     float2 ml[kBatch];
     float x[kBatch][kDims];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u * kJoinWarps;
+      const int i = i0 + u * kFinishWarps;
       ml[u] = make_float2(neg_inf(), 0.f);
 #pragma unroll
       for (int k = 0; k < kDims; ++k) x[u][k] = 0.f;
       if (i < parts) {
-        const int64_t at = slot(i);
+        const int64_t at = part_slot(share, i) * p.block_heads + hh;
         ml[u] = p.part_ml[at];
 #pragma unroll
         for (int k = 0; k < kDims; ++k) x[u][k] = p.part_o[at * D + lane + 32 * k];
@@ -582,10 +603,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
   L = 0.f;
   float a = 0.f, b = 0.f;
 #pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) M = fmaxf(M, sm[i]);
+  for (int i = 0; i < kFinishWarps; ++i) M = fmaxf(M, sm[i]);
   if (M != neg_inf()) {
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
+    for (int i = 0; i < kFinishWarps; ++i) {
       const float f = ex2(sm[i] - M);
       L = fmaf(sl[i], f, L);
       a = fmaf(so[i][2 * threadIdx.x], f, a);
@@ -595,48 +616,82 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
   const int64_t row = static_cast<int64_t>(meta.x) * p.H + g * p.group + hb * p.block_heads + hh;
   const float inv = L > 0.f ? 1.f / L : 0.f;
   reinterpret_cast<uint32_t*>(p.o + row * D)[threadIdx.x] = pack2<kF16>(a * inv, b * inv);
-  if (threadIdx.x == 0) {
-    const float e2 = L > 0.f ? M + log2f(L) : neg_inf();
-    if (p.lse) p.lse[row] = L > 0.f ? e2 * kLn2 : neg_inf();
-    if (p.scores) p.lse2[row] = e2;
+  if (threadIdx.x == 0 && p.lse) p.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
+}
+
+// weights[b, g, t] += sum over the group's heads of 2^(s - lse). Each key's sum
+// has one thread and a fixed order. A cut item's lse is formed here from its
+// parts, so that this does not wait for the join.
+__device__ __forceinline__ void add_weights(const DecodeParams& p, int b, int g, int chunk, float* __restrict__ weights) {
+  __shared__ float lse2[kMaxHeadBlock];
+  const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
+  const int t0 = chunk * kAddKeys + threadIdx.x;
+  if (chunk * kAddKeys >= len) return;
+  const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
+  float sum[kAddKeysPerThread];
+#pragma unroll
+  for (int i = 0; i < kAddKeysPerThread; ++i) sum[i] = 0.f;
+  for (int hb = 0; hb < p.head_blocks; ++hb) {
+    const int64_t item = (static_cast<int64_t>(b) * p.c.heads + g) * p.head_blocks + hb;
+    const int heads = min(p.block_heads, p.group - hb * p.block_heads);
+    __syncthreads();
+    if (threadIdx.x < heads) {
+      const int2 meta = p.item_meta[item];
+      if (meta.y == 1) {
+        lse2[threadIdx.x] = p.lse2[static_cast<int64_t>(b) * p.H + g * p.group + hb * p.block_heads + threadIdx.x];
+      } else {
+        float M = neg_inf(), L = 0.f;
+        for (int i = 0; i < meta.y; ++i) M = fmaxf(M, p.part_ml[part_slot(meta.x, i) * p.block_heads + threadIdx.x].x);
+        if (M != neg_inf())
+          for (int i = 0; i < meta.y; ++i) {
+            const float2 ml = p.part_ml[part_slot(meta.x, i) * p.block_heads + threadIdx.x];
+            L = fmaf(ml.y, ex2(ml.x - M), L);
+          }
+        lse2[threadIdx.x] = L > 0.f ? M + log2f(L) : neg_inf();
+      }
+    }
+    __syncthreads();
+    const float* s = p.scores + item * cap * p.score_heads;
+    for (int h = 0; h < heads; h += 2) {
+      float2 x[kAddKeysPerThread];
+#pragma unroll
+      for (int i = 0; i < kAddKeysPerThread; ++i) {
+        const int64_t t = t0 + i * kFinishThreads;
+        x[i] = t < len ? *reinterpret_cast<const float2*>(s + t * p.score_heads + h) : make_float2(neg_inf(), neg_inf());
+      }
+#pragma unroll
+      for (int i = 0; i < kAddKeysPerThread; ++i) {
+        if (x[i].x != neg_inf()) sum[i] += ex2(x[i].x - lse2[h]);
+        if (h + 1 < heads && x[i].y != neg_inf()) sum[i] += ex2(x[i].y - lse2[h + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kAddKeysPerThread; ++i) {
+    const int t = t0 + i * kFinishThreads;
+    if (t < len) weights[t] += sum[i];
   }
 }
 
-// weights[b, g, t] += sum over the group's heads of 2^(s - lse), from the
-// scores that the first kernel left in the workspace (4 bytes a head against the
-// 2 D of reading the key again). Each key's sum has one thread and a fixed order.
-constexpr int kAddThreads = 256;
-constexpr int kAddKeys = 4 * kAddThreads;
-
-__global__ void __launch_bounds__(kAddThreads)
-decode_add_weights_kernel(const DecodeParams p, float* __restrict__ weights, int64_t ld_w_batch, int64_t ld_w_head) {
+template <bool kF16, int D>
+__global__ void __launch_bounds__(kFinishThreads)
+decode_finish_kernel(const DecodeParams p, int joins, int chunks, float* weights, int64_t ld_w_batch, int64_t ld_w_head) {
   wait_for_previous_kernel();
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
-  const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
-  const int end = min(len, static_cast<int>(blockIdx.x + 1) * kAddKeys);
-  for (int t = blockIdx.x * kAddKeys + threadIdx.x; t < end; t += kAddThreads) {
-    float sum = 0.f;
-    for (int hb = 0; hb < p.head_blocks; ++hb) {
-      const float* s = p.scores + ((static_cast<int64_t>(b) * p.c.heads * p.head_blocks + g * p.head_blocks + hb) * cap + t) * p.block_heads;
-      const int heads = min(p.block_heads, p.group - hb * p.block_heads);
-      const float* lse2 = p.lse2 + static_cast<int64_t>(b) * p.H + g * p.group + hb * p.block_heads;
-      for (int h = 0; h < heads; h += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(s + h);
-        const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (h + e < heads && v[e] != neg_inf()) sum += ex2(v[e] - lse2[h + e]);
-      }
-    }
-    weights[b * ld_w_batch + g * ld_w_head + t] += sum;
+  const int i = blockIdx.x;
+  if (i < joins) {
+    join_head<kF16, D>(p, i / p.block_heads, i % p.block_heads);
+    return;
   }
+  const int chunk = (i - joins) % chunks, row = (i - joins) / chunks;
+  const int g = row % p.c.heads, b = row / p.c.heads;
+  add_weights(p, b, g, chunk, weights + b * ld_w_batch + g * ld_w_head);
 }
 
 // Layout of the workspace, the same for its size and its use.
 struct Plan {
-  int shares, block_heads, head_blocks;
-  int64_t part_o, part_ml, meta, lse2, scores, bytes;  // offsets, then the size
+  int shares, block_heads, head_blocks, score_heads;
+  bool whole;  // items are not cut
+  int64_t part_o, part_ml, meta, lse2, item_meta, scores, bytes;  // offsets, then the size
 };
 
 bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
@@ -647,6 +702,8 @@ bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
   pl.shares = sms * kCtasPerSm;
   pl.block_heads = group <= 8 ? 8 : kMaxHeadBlock;
   pl.head_blocks = (group + pl.block_heads - 1) / pl.block_heads;
+  pl.score_heads = pl.head_blocks > 1 ? pl.block_heads : (group + 1) / 2 * 2;
+  pl.whole = static_cast<int64_t>(c.max_pages) * c.page_size <= kWholeKeys;
   int64_t at = 0;
   auto take = [&](int64_t n) {
     const int64_t here = at;
@@ -656,11 +713,12 @@ bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
   pl.part_o = take(static_cast<int64_t>(2) * pl.shares * pl.block_heads * c.head_dim * 4);
   pl.part_ml = take(static_cast<int64_t>(2) * pl.shares * pl.block_heads * 8);
   pl.meta = take(static_cast<int64_t>(pl.shares) * 16);
-  pl.lse2 = pl.scores = 0;
+  pl.lse2 = pl.item_meta = pl.scores = 0;
   if (weights) {
     pl.lse2 = take(static_cast<int64_t>(c.batch) * H * 4);
+    pl.item_meta = take(static_cast<int64_t>(c.batch) * c.heads * pl.head_blocks * 8);
     pl.scores = take(static_cast<int64_t>(c.batch) * c.heads * pl.head_blocks * c.max_pages * c.page_size *
-                     pl.block_heads * 4);
+                     pl.score_heads * 4);
   }
   pl.bytes = at;
   *out = pl;
@@ -682,7 +740,8 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cuda
 }
 
 template <bool kF16, int D, int NT>
-cudaError_t launch_shape(const DecodeParams& p, int shares, cudaStream_t stream) {
+cudaError_t launch_shape(const DecodeParams& p, int shares, float* weights, int64_t ld_w_batch, int64_t ld_w_head,
+                         cudaStream_t stream) {
   constexpr int smem = Shape<D>::kSmemBytes;
   // the kernel's shared-memory limit, raised once per device
   constexpr int kMaxDevices = 64;
@@ -697,12 +756,20 @@ cudaError_t launch_shape(const DecodeParams& p, int shares, cudaStream_t stream)
   }
   decode_paged_kernel<kF16, D, NT><<<shares, kThreads, smem, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_after(decode_join_kernel<kF16, D>, dim3(shares, NT * 8), kJoinWarps * 32, stream, p);
+  const int64_t joins = p.unit_tiles == kUnitTiles ? static_cast<int64_t>(shares) * p.block_heads : 0;
+  const int64_t chunks = weights ? ((static_cast<int64_t>(p.c.max_pages) << p.c.page_shift) + kAddKeys - 1) / kAddKeys : 0;
+  const int64_t ctas = joins + chunks * p.c.heads * p.c.batch;
+  if (ctas > 0x7fffffff) return cudaErrorNotSupported;
+  if (ctas == 0) return cudaSuccess;
+  return launch_after(decode_finish_kernel<kF16, D>, dim3(static_cast<unsigned>(ctas)), kFinishThreads, stream, p,
+                      static_cast<int>(joins), static_cast<int>(chunks), weights, ld_w_batch, ld_w_head);
 }
 
 template <bool kF16, int D>
-cudaError_t launch_heads(const DecodeParams& p, int shares, cudaStream_t stream) {
-  return p.block_heads == 8 ? launch_shape<kF16, D, 1>(p, shares, stream) : launch_shape<kF16, D, 2>(p, shares, stream);
+cudaError_t launch_heads(const DecodeParams& p, int shares, float* weights, int64_t ld_w_batch, int64_t ld_w_head,
+                         cudaStream_t stream) {
+  return p.block_heads == 8 ? launch_shape<kF16, D, 1>(p, shares, weights, ld_w_batch, ld_w_head, stream)
+                            : launch_shape<kF16, D, 2>(p, shares, weights, ld_w_batch, ld_w_head, stream);
 }
 
 }  // namespace
@@ -728,6 +795,8 @@ cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t l
   p.group = H / cache.heads;
   p.head_blocks = pl.head_blocks;
   p.block_heads = pl.block_heads;
+  p.unit_tiles = pl.whole ? kWholeKeys / kTileKeys : kUnitTiles;
+  p.score_heads = pl.score_heads;
   p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.o = o;
   p.lse = lse;
@@ -735,17 +804,15 @@ cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t l
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
   p.meta = reinterpret_cast<int4*>(ws + pl.meta);
   p.lse2 = reinterpret_cast<float*>(ws + pl.lse2);
+  p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
   p.scores = weights ? reinterpret_cast<float*>(ws + pl.scores) : nullptr;
   p.err = err;
-  cudaError_t e;
+  const bool f16 = cache.dtype == OS_DTYPE_F16;
   if (cache.head_dim == 128)
-    e = cache.dtype == OS_DTYPE_F16 ? launch_heads<true, 128>(p, pl.shares, stream) : launch_heads<false, 128>(p, pl.shares, stream);
-  else
-    e = cache.dtype == OS_DTYPE_F16 ? launch_heads<true, 64>(p, pl.shares, stream) : launch_heads<false, 64>(p, pl.shares, stream);
-  if (e != cudaSuccess || !weights) return e;
-  const int cap = cache.max_pages * cache.page_size;
-  const dim3 grid((cap + kAddKeys - 1) / kAddKeys, cache.heads, cache.batch);
-  return launch_after(decode_add_weights_kernel, grid, kAddThreads, stream, p, weights, ld_w_batch, ld_w_head);
+    return f16 ? launch_heads<true, 128>(p, pl.shares, weights, ld_w_batch, ld_w_head, stream)
+               : launch_heads<false, 128>(p, pl.shares, weights, ld_w_batch, ld_w_head, stream);
+  return f16 ? launch_heads<true, 64>(p, pl.shares, weights, ld_w_batch, ld_w_head, stream)
+             : launch_heads<false, 64>(p, pl.shares, weights, ld_w_batch, ld_w_head, stream);
 }
 
 }  // namespace oss

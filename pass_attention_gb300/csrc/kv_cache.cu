@@ -10,12 +10,13 @@
 // * select. The smallest kept weight is found by radix: fp32 weights become
 //   integer keys of the same order, and a histogram of a digit (11, 11, 10 bits)
 //   of the keys that agree with the digits found so far gives the next digit.
-//   A thread-block cluster takes a row: its CTAs hold the keys of a slice in shared
-//   memory (one read of the weights), and each adds up all CTAs' histograms
-//   through distributed shared memory, so every digit costs one cluster
-//   barrier. Only integers are counted, so the atomics leave no order in the
-//   result. One more sweep writes the kept positions in ascending order; of the
-//   keys equal to the last one kept, the lowest positions are taken.
+//   A thread-block cluster takes a row: its CTAs hold the weights of a slice in
+//   shared memory (one read), and each adds up all CTAs' histograms through
+//   distributed shared memory, so every digit costs one cluster barrier: first 64
+//   sums of 32 bins each, then the 32 bins that hold the digit (all 2048 bins from
+//   eight CTAs took 2 us a digit). Only integers are counted, so the atomics leave
+//   no order in the result. One more sweep writes the kept positions in ascending
+//   order; of the keys equal to the last one kept, the lowest positions are taken.
 // * move. Kept rows are copied page to page, four rows of a thread in flight.
 
 #include <atomic>
@@ -85,8 +86,10 @@ kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
 constexpr int kSelectThreads = 1024;
 constexpr int kDigits = 3;
 constexpr int kBins = 2048;
+constexpr int kCoarse = 64;  // sums of 32 bins
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSliceKeys = 48 * 1024;  // 192 KB of keys in shared memory
+constexpr int kMaxSliceKeys = 48 * 1024;  // 192 KB of weights in shared memory
+constexpr int kLeastSlice = 4096;
 
 struct EvictParams {
   PagedCache c;
@@ -100,29 +103,37 @@ struct EvictParams {
   float* new_weights;
 };
 
-__device__ __forceinline__ uint32_t weight_key(float w) { return weight_key_bits(__float_as_uint(w)); }
-
-// Inclusive scan over the block's threads; *total gets the block's sum.
-__device__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive scan over a warp.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
     if (lane >= off) x += y;
   }
+  return x;
+}
+
+// Inclusive scan over the block's threads; *total gets the block's sum.
+__device__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = warp_scan(x);
   __syncthreads();  // the previous scan's sums have been read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   // every warp scans the warps' sums
-  uint32_t w = warp_sums[lane];
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, w, off);
-    if (lane >= off) w += y;
-  }
+  const uint32_t w = warp_scan(warp_sums[lane]);
   *total = __shfl_sync(0xffffffffu, w, 31);
   const uint32_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
   return x + (warp > 0 ? before : 0u);
+}
+
+__device__ __forceinline__ uint2 ld_peer2(const uint32_t* slot, uint32_t rank) {
+  uint32_t remote;
+  uint2 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(slot)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(remote) : "memory");
+  return x;
 }
 
 __device__ __forceinline__ uint32_t ld_peer(const uint32_t* slot, uint32_t rank) {
@@ -136,14 +147,16 @@ __device__ __forceinline__ uint32_t ld_peer(const uint32_t* slot, uint32_t rank)
 // shared memory; otherwise every sweep reads the weights again.
 template <bool kCached>
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParams p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ uint32_t slice_bits[];  // the weights of this CTA's slice, as they are
   __shared__ uint32_t hist[kDigits][kBins];
+  __shared__ __align__(8) uint32_t coarse[kDigits][kCoarse];
   __shared__ uint32_t warp_sums[kSelectThreads / 32];
-  __shared__ uint32_t found_digit, found_rank, slice_counts[2];
+  __shared__ uint32_t found_digit, found_rank;
+  __shared__ __align__(8) uint32_t slice_counts[2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t C = cluster_size(), rank = cluster_rank();
   const int head = blockIdx.x / C, seq = blockIdx.y;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = paged_length(p.c.kv_len[seq], p.c.max_pages, p.c.page_shift);
   const int keep = min(len, p.budget);
   const int recent = min(p.recent, keep);
@@ -175,11 +188,11 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
   const int slice = (older + static_cast<int>(C) - 1) / static_cast<int>(C);
   const int first = min(older, static_cast<int>(rank) * slice);
   const int n = min(older - first, slice);
-  auto key_at = [&](int i) -> uint32_t { return kCached ? keys[i] : weight_key(w[first + i]); };
+  auto bits_at = [&](int i) -> uint32_t { return kCached ? slice_bits[i] : __float_as_uint(w[first + i]); };
   for (int i = tid; i < kDigits * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
   if constexpr (kCached) {
-#pragma unroll 8
-    for (int i = tid; i < n; i += kSelectThreads) keys[i] = weight_key(__ldg(w + first + i));
+#pragma unroll 16
+    for (int i = tid; i < n; i += kSelectThreads) slice_bits[i] = __float_as_uint(__ldg(w + first + i));
   }
   __syncthreads();
 
@@ -189,26 +202,54 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
   for (int d = 0; d < kDigits; ++d) {
     const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
     const int bits = d == 2 ? 10 : 11;
+#pragma unroll 4
     for (int i = tid; i < n; i += kSelectThreads) {
-      const uint32_t key = key_at(i);
+      const uint32_t key = weight_key_bits(bits_at(i));
       if (d == 0 || (key >> (shift + bits)) == (last >> (shift + bits)))
         atomicAdd(&hist[d][(key >> shift) & ((1u << bits) - 1)], 1u);
     }
-    __syncwarp();
-    cluster_sync_all();
-    // thread t: bins kBins - 1 - 2 t and the one below, over all slices
-    uint32_t hi = 0, lo = 0;
-    for (uint32_t r = 0; r < C; ++r) {
-      hi += ld_peer(&hist[d][kBins - 1 - 2 * tid], r);
-      lo += ld_peer(&hist[d][kBins - 2 - 2 * tid], r);
+    __syncthreads();
+    // a warp: two sums of 32 bins
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t c = __reduce_add_sync(0xffffffffu, hist[d][(2 * warp + i) * 32 + lane]);
+      if (lane == 0) coarse[d][2 * warp + i] = c;
     }
-    uint32_t total;
-    const uint32_t upto = block_scan(hi + lo, warp_sums, &total);
-    const uint32_t above = upto - hi - lo;  // keys in higher bins
-    if (above < ties && upto >= ties) {
-      const bool in_hi = above + hi >= ties;
-      found_digit = kBins - 1 - 2 * tid - (in_hi ? 0 : 1);
-      found_rank = ties - above - (in_hi ? 0u : hi);
+    cluster_sync_all();
+    if (warp == 0) {
+      // over all slices, from the top: lane l has sums 63 - 2 l and 62 - 2 l
+      uint2 peer[kMaxCluster];
+      uint32_t lo = 0, hi = 0;
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxCluster; ++r)
+        peer[r] = r < C ? ld_peer2(&coarse[d][kCoarse - 2 - 2 * lane], r) : make_uint2(0u, 0u);
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxCluster; ++r) {
+        lo += peer[r].x;
+        hi += peer[r].y;
+      }
+      const uint32_t upto = warp_scan(hi + lo);
+      const uint32_t at = __ffs(__ballot_sync(0xffffffffu, upto >= ties)) - 1;  // the lane whose sums reach it
+      uint32_t above = __shfl_sync(0xffffffffu, upto - hi - lo, at);           // keys in higher bins
+      const uint32_t first_sum = __shfl_sync(0xffffffffu, hi, at);
+      uint32_t sum_of = kCoarse - 1 - 2 * at;
+      if (above + first_sum < ties) {
+        above += first_sum;
+        --sum_of;
+      }
+      // its 32 bins, lane l: bin 31 - l
+      uint32_t bin[kMaxCluster], count = 0;
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxCluster; ++r)
+        bin[r] = r < C ? ld_peer(&hist[d][sum_of * 32 + 31 - lane], r) : 0u;
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxCluster; ++r) count += bin[r];
+      const uint32_t within = warp_scan(count);
+      const uint32_t l = __ffs(__ballot_sync(0xffffffffu, above + within >= ties)) - 1;
+      if (lane == l) {
+        found_digit = sum_of * 32 + 31 - lane;
+        found_rank = ties - above - (within - count);
+      }
     }
     __syncthreads();
     last |= found_digit << shift;
@@ -220,31 +261,47 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
   const int r0 = min(n, tid * run), r1 = min(n, r0 + run);
   uint32_t gt = 0, eq = 0;
   for (int i = r0; i < r1; ++i) {
-    const uint32_t key = key_at(i);
+    const uint32_t key = weight_key_bits(bits_at(i));
     gt += key > last;
     eq += key == last;
   }
-  uint32_t all_gt, all_eq;
-  uint32_t gt_at = block_scan(gt, warp_sums, &all_gt) - gt;
-  uint32_t eq_at = block_scan(eq, warp_sums, &all_eq) - eq;
+  // both counts in one scan: a cached slice has fewer than 2^16 keys
+  uint32_t all_gt, all_eq, gt_at, eq_at;
+  if constexpr (kCached) {
+    uint32_t all;
+    const uint32_t upto = block_scan(gt | (eq << 16), warp_sums, &all);
+    gt_at = (upto & 0xffffu) - gt;
+    eq_at = (upto >> 16) - eq;
+    all_gt = all & 0xffffu;
+    all_eq = all >> 16;
+  } else {
+    gt_at = block_scan(gt, warp_sums, &all_gt) - gt;
+    eq_at = block_scan(eq, warp_sums, &all_eq) - eq;
+  }
   if (tid == 0) {
     slice_counts[0] = all_gt;
     slice_counts[1] = all_eq;
   }
   __syncwarp();
   cluster_sync_all();
-  for (uint32_t r = 0; r < rank; ++r) {
-    gt_at += ld_peer(&slice_counts[0], r);
-    eq_at += ld_peer(&slice_counts[1], r);
+  {
+    uint2 peer[kMaxCluster];
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r) peer[r] = r < rank ? ld_peer2(slice_counts, r) : make_uint2(0u, 0u);
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r) {
+      gt_at += peer[r].x;
+      eq_at += peer[r].y;
+    }
   }
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   for (int i = r0; i < r1; ++i) {
-    const uint32_t key = key_at(i);
+    const uint32_t bits = bits_at(i), key = weight_key_bits(bits);
     if (key > last || (key == last && eq_at < ties)) {
       const uint32_t at = gt_at + min(eq_at, ties);
       kept[at] = first + i;
-      nw[at] = w[first + i];
+      nw[at] = __uint_as_float(bits);
     }
     gt_at += key > last;
     eq_at += key == last;
@@ -300,32 +357,50 @@ evict_move_kernel(EvictParams p, uint16_t* k_pages, uint16_t* v_pages, unsigned 
   }
 }
 
+constexpr int kMaxDevices = 64;
+
+// Launch of the selection by clusters of C CTAs with `smem` bytes each.
 template <bool kCached>
-cudaError_t launch_select(const EvictParams& p, int C, int smem, cudaStream_t stream) {
-  // the kernel's shared-memory limit, raised once per device
-  constexpr int kMaxDevices = 64;
-  static std::atomic<bool> smem_set[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices || !smem_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(evict_select_kernel<kCached>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSliceKeys * 4);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices) smem_set[dev].store(true, std::memory_order_release);
-  }
+cudaLaunchConfig_t select_config(const EvictParams& p, int C, int smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = C;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.c.heads * C, p.c.batch);
   cfg.blockDim = dim3(kSelectThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<kCached>, p);
+  return cfg;
+}
+
+// The kernel's shared-memory limit, raised once per device.
+cudaError_t raise_select_smem(int dev) {
+  static std::atomic<bool> done[kMaxDevices];
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kMaxSliceKeys * 4);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+// Clusters of C CTAs that the device holds at one time with a full slice each
+// (one CTA an SM); asked once per device and C.
+int resident_clusters(const EvictParams& p, int dev, int C) {
+  static std::atomic<int> known[kMaxDevices][kMaxCluster + 1];
+  if (dev < 0 || dev >= kMaxDevices) return 0;
+  int n = known[dev][C].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = select_config<true>(p, C, kMaxSliceKeys * 4, nullptr, attr);
+  if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel<true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev][C].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 PagedCache device_cache(const os_paged_cache& c) {
@@ -360,15 +435,29 @@ cudaError_t launch_kv_evict(const os_paged_cache& cache, const float* weights, i
                             cudaStream_t stream) {
   const EvictParams p{device_cache(cache), weights, ld_w_batch, ld_w_head, new_table, ld_new_table,
                       new_max_pages, budget, recent, kept, new_len, new_weights};
-  // CTAs of a row: enough for the GPU to be filled while a slice keeps at least
-  // 4096 keys, and for a slice to fit shared memory where eight can do it
+  // CTAs of a row: as many (up to eight) as fit on the GPU for all rows at once while a
+  // slice keeps at least kLeastSlice keys, and as many as it takes for a slice
+  // to fit shared memory where eight can do that. (16 rows of 131072 keys: clusters of
+  // eight do not all fit at once and took 92 us with the copy, clusters of seven 77 us.)
   const int64_t capacity = static_cast<int64_t>(cache.max_pages) * cache.page_size;
   const int64_t rows = static_cast<int64_t>(cache.heads) * cache.batch;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = raise_select_smem(dev)) != cudaSuccess) return e;
   int C = 1;
-  while (C < kMaxCluster && (capacity / C > kMaxSliceKeys || (rows * C < 152 && capacity / C > 4096))) C *= 2;
+  while (C < kMaxCluster && (capacity > static_cast<int64_t>(C) * kMaxSliceKeys ||
+                             (capacity >= static_cast<int64_t>(C + 1) * kLeastSlice && rows <= resident_clusters(p, dev, C + 1))))
+    ++C;
   const int64_t slice = (capacity + C - 1) / C;
-  cudaError_t e = slice <= kMaxSliceKeys ? launch_select<true>(p, C, static_cast<int>(slice) * 4, stream)
-                                         : launch_select<false>(p, C, 0, stream);
+  cudaLaunchAttribute cluster[1];
+  if (slice <= kMaxSliceKeys) {
+    const cudaLaunchConfig_t cfg = select_config<true>(p, C, static_cast<int>(slice) * 4, stream, cluster);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p);
+  } else {
+    const cudaLaunchConfig_t cfg = select_config<false>(p, C, 0, stream, cluster);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
+  }
   if (e != cudaSuccess) return e;
   const int chunks = cache.head_dim / 8, rows_per_cta = kMoveThreads / chunks * kMoveBatch;
   cudaLaunchConfig_t cfg = {};
