@@ -50,10 +50,12 @@ constexpr int kTileKeys = 16;
 constexpr int kUnitTiles = kWarps;  // a unit: one tile per warp
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxHeadBlock = 16;
-// A page table that holds this many tokens or fewer is not cut into shares: the
-// second launch costs more than one CTA takes for them (a decode step of one
-// sequence of 333 tokens, 32 heads over 8: WHOLE_FIGURES).
-constexpr int kWholeKeys = 512;
+// Items are not cut, and nothing is joined, when a row of the page table holds at
+// most kWholeKeys tokens, or at most twice that and there are as many items as
+// shares. Replayed from a graph, 32 heads over 8, whole against cut: 1 x 128 tokens 4.9
+// against 7.4 us, 1 x 256 6.4 / 7.5, 64 x 256 12.1 / 17.6, 64 x 512 27 / 33; but
+// 1 x 512 9.2 / 7.4.
+constexpr int kWholeKeys = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
 // The reference maximum moves only when a score exceeds it by more than
 // 2^kSlack: any reference gives the same quotient O / l, and weights up to 2^8 are
@@ -531,9 +533,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   copy_wait<0>();
 }
 
-// The second kernel. Its first CTAs join: CTA (c, hh) merges head hh of the item
-// that begins in share c and goes on into the next ones; its warps take the
-// parts in turn. The others, with weights, add up: kAddKeys keys of one key head.
+// The second kernel. With weights, its first CTAs add up: kAddKeys keys of one key
+// head each. The others join: CTA (c, hh) merges head hh of the item that begins
+// in share c and goes on into the next ones; its warps take the parts in turn.
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
 constexpr int kAddKeysPerThread = 4;
@@ -621,70 +623,85 @@ __device__ __forceinline__ void join_head(const DecodeParams& p, int share, int 
 
 // weights[b, g, t] += sum over the group's heads of 2^(s - lse). Each key's sum
 // has one thread and a fixed order. A cut item's lse is formed here from its
-// parts, so that this does not wait for the join.
+// parts, so that this does not wait for the join; the scores are on their way
+// meanwhile.
 __device__ __forceinline__ void add_weights(const DecodeParams& p, int b, int g, int chunk, float* __restrict__ weights) {
   __shared__ float lse2[kMaxHeadBlock];
   const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
   const int t0 = chunk * kAddKeys + threadIdx.x;
   if (chunk * kAddKeys >= len) return;
+  wait_for_previous_kernel();
   const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
-  float sum[kAddKeysPerThread];
+  float was[kAddKeysPerThread], sum[kAddKeysPerThread];
 #pragma unroll
-  for (int i = 0; i < kAddKeysPerThread; ++i) sum[i] = 0.f;
+  for (int i = 0; i < kAddKeysPerThread; ++i) {
+    const int t = t0 + i * kFinishThreads;
+    was[i] = t < len ? weights[t] : 0.f;
+    sum[i] = 0.f;
+  }
   for (int hb = 0; hb < p.head_blocks; ++hb) {
     const int64_t item = (static_cast<int64_t>(b) * p.c.heads + g) * p.head_blocks + hb;
     const int heads = min(p.block_heads, p.group - hb * p.block_heads);
-    __syncthreads();
-    if (threadIdx.x < heads) {
-      const int2 meta = p.item_meta[item];
-      if (meta.y == 1) {
-        lse2[threadIdx.x] = p.lse2[static_cast<int64_t>(b) * p.H + g * p.group + hb * p.block_heads + threadIdx.x];
-      } else {
-        float M = neg_inf(), L = 0.f;
-        for (int i = 0; i < meta.y; ++i) M = fmaxf(M, p.part_ml[part_slot(meta.x, i) * p.block_heads + threadIdx.x].x);
-        if (M != neg_inf())
-          for (int i = 0; i < meta.y; ++i) {
-            const float2 ml = p.part_ml[part_slot(meta.x, i) * p.block_heads + threadIdx.x];
-            L = fmaf(ml.y, ex2(ml.x - M), L);
-          }
-        lse2[threadIdx.x] = L > 0.f ? M + log2f(L) : neg_inf();
-      }
-    }
-    __syncthreads();
     const float* s = p.scores + item * cap * p.score_heads;
-    for (int h = 0; h < heads; h += 2) {
-      float2 x[kAddKeysPerThread];
+    if (hb > 0) __syncthreads();
+    for (int h = 0; h < heads; h += 4) {
+      float4 x[kAddKeysPerThread];
 #pragma unroll
       for (int i = 0; i < kAddKeysPerThread; ++i) {
         const int64_t t = t0 + i * kFinishThreads;
-        x[i] = t < len ? *reinterpret_cast<const float2*>(s + t * p.score_heads + h) : make_float2(neg_inf(), neg_inf());
+        x[i] = t < len ? *reinterpret_cast<const float4*>(s + t * p.score_heads + h)
+                       : make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
+      }
+      if (h == 0) {
+        if (threadIdx.x < heads) {
+          const int2 meta = p.item_meta[item];
+          float e2 = neg_inf();
+          if (meta.y == 1) {
+            e2 = p.lse2[static_cast<int64_t>(b) * p.H + g * p.group + hb * p.block_heads + threadIdx.x];
+          } else {
+            float M = neg_inf(), L = 0.f;
+            for (int i = 0; i < meta.y; ++i) {
+              const float2 ml = p.part_ml[part_slot(meta.x, i) * p.block_heads + threadIdx.x];
+              const float to = fmaxf(M, ml.x);
+              if (to == neg_inf()) continue;
+              L = fmaf(L, ex2(M - to), ml.y * ex2(ml.x - to));
+              M = to;
+            }
+            if (L > 0.f) e2 = M + log2f(L);
+          }
+          lse2[threadIdx.x] = e2;
+        }
+        __syncthreads();
       }
 #pragma unroll
       for (int i = 0; i < kAddKeysPerThread; ++i) {
-        if (x[i].x != neg_inf()) sum[i] += ex2(x[i].x - lse2[h]);
-        if (h + 1 < heads && x[i].y != neg_inf()) sum[i] += ex2(x[i].y - lse2[h + 1]);
+        const float v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (h + e < heads && v[e] != neg_inf()) sum[i] += ex2(v[e] - lse2[h + e]);
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < kAddKeysPerThread; ++i) {
     const int t = t0 + i * kFinishThreads;
-    if (t < len) weights[t] += sum[i];
+    if (t < len) weights[t] = was[i] + sum[i];
   }
 }
 
 template <bool kF16, int D>
 __global__ void __launch_bounds__(kFinishThreads)
-decode_finish_kernel(const DecodeParams p, int joins, int chunks, float* weights, int64_t ld_w_batch, int64_t ld_w_head) {
-  wait_for_previous_kernel();
-  const int i = blockIdx.x;
-  if (i < joins) {
-    join_head<kF16, D>(p, i / p.block_heads, i % p.block_heads);
+decode_finish_kernel(const DecodeParams p, int adds, int chunks, float* weights, int64_t ld_w_batch, int64_t ld_w_head) {
+  int i = blockIdx.x;
+  if (i < adds) {
+    const int chunk = i % chunks, row = i / chunks;
+    const int g = row % p.c.heads, b = row / p.c.heads;
+    add_weights(p, b, g, chunk, weights + b * ld_w_batch + g * ld_w_head);
     return;
   }
-  const int chunk = (i - joins) % chunks, row = (i - joins) / chunks;
-  const int g = row % p.c.heads, b = row / p.c.heads;
-  add_weights(p, b, g, chunk, weights + b * ld_w_batch + g * ld_w_head);
+  i -= adds;
+  wait_for_previous_kernel();
+  join_head<kF16, D>(p, i / p.block_heads, i % p.block_heads);
 }
 
 // Layout of the workspace, the same for its size and its use.
@@ -702,8 +719,10 @@ bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
   pl.shares = sms * kCtasPerSm;
   pl.block_heads = group <= 8 ? 8 : kMaxHeadBlock;
   pl.head_blocks = (group + pl.block_heads - 1) / pl.block_heads;
-  pl.score_heads = pl.head_blocks > 1 ? pl.block_heads : (group + 1) / 2 * 2;
-  pl.whole = static_cast<int64_t>(c.max_pages) * c.page_size <= kWholeKeys;
+  pl.score_heads = pl.head_blocks > 1 ? pl.block_heads : (group + 3) / 4 * 4;
+  const int64_t capacity = static_cast<int64_t>(c.max_pages) * c.page_size;
+  const int64_t items = static_cast<int64_t>(c.batch) * c.heads * pl.head_blocks;
+  pl.whole = capacity <= kWholeKeys || (capacity <= 2 * kWholeKeys && items >= pl.shares);
   int64_t at = 0;
   auto take = [&](int64_t n) {
     const int64_t here = at;
@@ -758,11 +777,11 @@ cudaError_t launch_shape(const DecodeParams& p, int shares, float* weights, int6
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t joins = p.unit_tiles == kUnitTiles ? static_cast<int64_t>(shares) * p.block_heads : 0;
   const int64_t chunks = weights ? ((static_cast<int64_t>(p.c.max_pages) << p.c.page_shift) + kAddKeys - 1) / kAddKeys : 0;
-  const int64_t ctas = joins + chunks * p.c.heads * p.c.batch;
+  const int64_t adds = chunks * p.c.heads * p.c.batch, ctas = adds + joins;
   if (ctas > 0x7fffffff) return cudaErrorNotSupported;
   if (ctas == 0) return cudaSuccess;
   return launch_after(decode_finish_kernel<kF16, D>, dim3(static_cast<unsigned>(ctas)), kFinishThreads, stream, p,
-                      static_cast<int>(joins), static_cast<int>(chunks), weights, ld_w_batch, ld_w_head);
+                      static_cast<int>(adds), static_cast<int>(chunks), weights, ld_w_batch, ld_w_head);
 }
 
 template <bool kF16, int D>
@@ -795,7 +814,7 @@ cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t l
   p.group = H / cache.heads;
   p.head_blocks = pl.head_blocks;
   p.block_heads = pl.block_heads;
-  p.unit_tiles = pl.whole ? kWholeKeys / kTileKeys : kUnitTiles;
+  p.unit_tiles = pl.whole ? 2 * kWholeKeys / kTileKeys : kUnitTiles;
   p.score_heads = pl.score_heads;
   p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.o = o;

@@ -18,8 +18,9 @@ one to fp32. The inputs are exact.
   A = sum p_j |v_j| / l; the sum over n keys, 2 n U32 A; the weights, 2 e_w A.
   An fp16 p_j below its smallest normal is off by 2^-25 of the largest weight:
   n 2^-25 max |v| more; and o likewise, 2^-25.
-* summed weights: sum over the group of p (e_w + the lse's bar) and the
-  additions' roundings, 4 U32 times the total.
+* summed weights: sum over the group of p (e_w + the lse's bar); G positive terms
+  added in fp32 in any order round G - 1 times to at most the total, (G - 1) U32
+  total; the addition to the old value rounds once more, U32 |new value|.
 """
 
 import numpy as np
@@ -125,7 +126,7 @@ def check_decode(o, lse, q, k_pages, v_pages, table, kv_len, scale, weights=None
                 was = f64(before[b, g])
                 ref = was[:n] + total
                 got = f64(weights[b, g])
-                check(got[:n], ref, bar + 4 * U32 * (np.abs(ref) + total) + 2.0 ** -126, f"sequence {b} key head {g} weights")
+                check(got[:n], ref, bar + U32 * (np.abs(ref) + group * total) + 2.0 ** -126, f"sequence {b} key head {g} weights")
                 assert np.array_equal(got[n:], was[n:], equal_nan=True), "weights behind the sequence"
 
 
