@@ -12,11 +12,11 @@ error.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
 import struct
+import threading
 from typing import Optional
 
 import torch
@@ -654,7 +654,7 @@ def _cache(k_pages, v_pages, page_table, kv_len):
     batch, max_pages = page_table.shape
     if kv_len.shape[0] != batch:
         raise ValueError("kv_len must have one entry for each row of page_table")
-    if max(pages, max_pages, batch) > 0x7fffffff:
+    if pages > 0x7fffffff or max_pages > 0x7fffffff or batch > 0x7fffffff:
         raise ValueError("more pages than 32 bits count")
     return (_PAGED_CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
                               page_table.data_ptr(), page_table.stride(0), kv_len.data_ptr(), pages, heads,
@@ -662,27 +662,45 @@ def _cache(k_pages, v_pages, page_table, kv_len):
             dev, batch, heads, d, max_pages * page_size, page_size)
 
 
+def _elsewhere(dev: torch.device, stream) -> bool:
+    """Whether a call for tensors on ``dev`` has to change the current stream
+    or device first (``_on``)."""
+    return stream is not None or dev.index != _current_device()
+
+
 def _on(dev: torch.device, stream):
-    """The context in which a call for tensors on ``dev`` allocates and
-    launches: the caller's stream, or the current one of that device. Outputs
-    and workspaces come from PyTorch's allocator under it, call by call, so
-    their memory is ordered with the stream that uses it, and two streams or
-    two captured graphs never share a workspace."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index == torch.cuda.current_device():
-        return _HERE_ALREADY
-    return torch.cuda.device(dev)
+    """The context in which such a call allocates and launches. Outputs and
+    workspaces come from PyTorch's allocator under it, so that their memory is
+    ordered with the stream that uses it."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
-_HERE_ALREADY = contextlib.nullcontext()
+# The current device, and the raw current stream of a device, without making a
+# Stream object.
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+# Workspaces of the calls that launch two kernels, kept per (device, stream) up
+# to this size. The lock is held from taking one to the end of the launches:
+# kernels of two threads' calls on one stream would otherwise alternate on it. A call
+# under capture gets its own from the graph's memory.
+_KEEP_BYTES = 64 << 20
+_LAUNCH_LOCK = threading.Lock()
 
 
-def _raw_stream(dev: torch.device) -> int:
-    """The current stream of ``dev``, without making a Stream object for it."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+def _scratch(dev: torch.device, sp: int, nbytes: int) -> torch.Tensor:
+    if nbytes > _KEEP_BYTES or torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    key = (dev.index, sp, "cache")
+    ws = _WORKSPACES.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _WORKSPACES[key] = ws
+    return ws
 
 
 def attention_fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -720,21 +738,24 @@ def attention_fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         _out(o, "o", q.dtype, (tokens_q, hq, d), dev)
     if lse is not None:
         _out(lse, "lse", torch.float32, (tokens_q, hq), dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attention_fwd_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, o, lse)
+    if o is None:
+        o = torch.empty((tokens_q, hq, d), dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((tokens_q, hq), dtype=torch.float32, device=dev)
     lib = load()
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty((tokens_q, hq, d), dtype=q.dtype, device=dev)
-        if lse is None:
-            lse = torch.empty((tokens_q, hq), dtype=torch.float32, device=dev)
-        need = lib.os_attention_fwd_packed_workspace_bytes(tokens_k, hkv, d)
-        if need < 0:
-            raise OssError(4, "os_attention_fwd_packed_workspace_bytes")
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    need = lib.os_attention_fwd_packed_workspace_bytes(tokens_k, hkv, d)
+    if need < 0:
+        raise OssError(4, "os_attention_fwd_packed_workspace_bytes")
+    sp = _raw_stream(dev.index)
+    with _LAUNCH_LOCK:
+        ws = _scratch(dev, sp, need)
         st = lib.os_attention_fwd_packed(
             q.data_ptr(), sq[0], sq[1], k.data_ptr(), v.data_ptr(), sk[0], sk[1], o.data_ptr(),
             lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), batch, tokens_q,
-            tokens_k, hq, hkv, d, _DTYPE_CODES[q.dtype], scale, bool(causal), ws.data_ptr(), need,
-            _raw_stream(dev))
+            tokens_k, hq, hkv, d, _DTYPE_CODES[q.dtype], scale, bool(causal), ws.data_ptr(), need, sp)
     _check(st, "os_attention_fwd_packed")
     return o, lse
 
@@ -759,9 +780,11 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_p
         if cu_seqlens.shape[0] != batch + 1:
             raise ValueError("cu_seqlens must have batch + 1 entries")
         cu = cu_seqlens.data_ptr()
-    with _on(dev, stream):
-        st = load().os_kv_cache_append(k.data_ptr(), v.data_ptr(), sk[0], sk[1], tokens, cu, cache,
-                                       _raw_stream(dev))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv_cache_append(k, v, k_pages, v_pages, page_table, kv_len, cu_seqlens)
+    st = load().os_kv_cache_append(k.data_ptr(), v.data_ptr(), sk[0], sk[1], tokens, cu, cache,
+                                   _raw_stream(dev.index))
     _check(st, "os_kv_cache_append")
 
 
@@ -804,19 +827,22 @@ def attention_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
         _out(o, "o", dtype, (batch, hq, d), dev)
     if lse is not None:
         _out(lse, "lse", torch.float32, (batch, hq), dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attention_decode_paged(q, k_pages, v_pages, page_table, kv_len, scale, weights, o, lse)
+    if o is None:
+        o = torch.empty((batch, hq, d), dtype=dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
     lib = load()
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty((batch, hq, d), dtype=dtype, device=dev)
-        if lse is None:
-            lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
-        need = lib.os_attention_decode_paged_workspace_bytes(hq, cache, w is not None)
-        if need < 0:
-            raise OssError(4, "os_attention_decode_paged_workspace_bytes")
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    need = lib.os_attention_decode_paged_workspace_bytes(hq, cache, w is not None)
+    if need < 0:
+        raise OssError(4, "os_attention_decode_paged_workspace_bytes")
+    sp = _raw_stream(dev.index)
+    with _LAUNCH_LOCK:
+        ws = _scratch(dev, sp, need)
         st = lib.os_attention_decode_paged(q.data_ptr(), sq[0], sq[1], hq, cache, scale, o.data_ptr(),
-                                           lse.data_ptr(), w, sw[0], sw[1], ws.data_ptr(), need,
-                                           _raw_stream(dev))
+                                           lse.data_ptr(), w, sw[0], sw[1], ws.data_ptr(), need, sp)
     _check(st, "os_attention_decode_paged")
     return o, lse
 
@@ -853,16 +879,19 @@ def kv_cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.
         _out(new_len, "new_len", torch.int32, (batch,), dev)
     if new_weights is not None:
         _out(new_weights, "new_weights", torch.float32, (batch, heads, room), dev)
-    with _on(dev, stream):
-        if kept is None:
-            kept = torch.empty((batch, heads, budget), dtype=torch.int32, device=dev)
-        if new_len is None:
-            new_len = torch.empty(batch, dtype=torch.int32, device=dev)
-        if new_weights is None:
-            new_weights = torch.empty((batch, heads, room), dtype=torch.float32, device=dev)
-        st = load().os_kv_cache_evict(cache, weights.data_ptr(), sw[0], sw[1], new_page_table.data_ptr(),
-                                      new_page_table.stride(0), new_max, budget, recent, kept.data_ptr(),
-                                      new_len.data_ptr(), new_weights.data_ptr(), _raw_stream(dev))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv_cache_evict(k_pages, v_pages, weights, page_table, kv_len, new_page_table, budget, recent, kept,
+                                  new_len, new_weights)
+    if kept is None:
+        kept = torch.empty((batch, heads, budget), dtype=torch.int32, device=dev)
+    if new_len is None:
+        new_len = torch.empty(batch, dtype=torch.int32, device=dev)
+    if new_weights is None:
+        new_weights = torch.empty((batch, heads, room), dtype=torch.float32, device=dev)
+    st = load().os_kv_cache_evict(cache, weights.data_ptr(), sw[0], sw[1], new_page_table.data_ptr(),
+                                  new_page_table.stride(0), new_max, budget, recent, kept.data_ptr(),
+                                  new_len.data_ptr(), new_weights.data_ptr(), _raw_stream(dev.index))
     _check(st, "os_kv_cache_evict")
     return kept, new_len, new_weights
 

@@ -705,13 +705,15 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         tc_fence_before();
         mbar_arrive(smem_addr(&bars.o_free));  // the next item's first P V may overwrite O
         __syncwarp();
-        constexpr int kChunks = D / 8;
+        constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // chunks of a row, rows of a pass
+        uint4* base = reinterpret_cast<uint4*>(p.o + out_row(p, u.q_row, u.pack, 0) * D);
+        const int c = lane % kChunks;
+        const uint32_t from = stage + (c >> 3) * (32 * 128);
 #pragma unroll 4
-        for (int i = lane; i < 32 * kChunks; i += 32) {
-          const int row = i / kChunks, c = i % kChunks;
-          const uint4 x = ld_shared_u4(stage + (c >> 3) * (32 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-          if (((row0 + row) >> head_shift) < u.n_pos)
-            reinterpret_cast<uint4*>(p.o + out_row(p, u.q_row, u.pack, row0 + row) * D)[c] = x;
+        for (int row = lane / kChunks; row < 32; row += kRows) {
+          const uint4 x = ld_shared_u4(from + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+          const int at = (row0 + row) >> head_shift, head = (row0 + row) & ((1 << head_shift) - 1);
+          if (at < u.n_pos) base[static_cast<int64_t>(at * p.Hq + head) * kChunks + c] = x;
         }
         __syncwarp();
         if (p.lse && ((row0 + lane) >> head_shift) < u.n_pos)

@@ -18,7 +18,7 @@
 //
 // Division of the work: a unit is 64 keys of an item, an item being one
 // sequence, key head and block of up to 16 query heads. The units of all items
-// stand in a row, and CTA c of N takes units [c W / N, (c + 1) W / N): equal shares
+// stand in a row, and every CTA takes an equal share of them (share_cut): equal shares
 // of the bytes whatever the lengths are, from lengths that only the device
 // knows. An item inside one share is finished there; one that crosses shares
 // leaves partial states (m, l, O), which a second kernel joins in share order.
@@ -39,6 +39,7 @@
 
 #include "device_common.cuh"
 #include "oss_internal.h"
+#include "packed_plan.h"
 #include "paged.h"
 
 namespace oss {
@@ -51,11 +52,12 @@ constexpr int kUnitTiles = kWarps;  // a unit: one tile per warp
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxHeadBlock = 16;
 // Items are not cut, and nothing is joined, when a row of the page table holds at
-// most kWholeKeys tokens, or at most twice that and there are as many items as
-// shares. Replayed from a graph, 32 heads over 8, whole against cut: 1 x 128 tokens 4.9
-// against 7.4 us, 1 x 256 6.4 / 7.5, 64 x 256 12.1 / 17.6, 64 x 512 27 / 33; but
-// 1 x 512 9.2 / 7.4.
-constexpr int kWholeKeys = 256;
+// most kWholeKeys tokens, or at most kWholeKeysMany and there are as many items
+// as shares. Replayed from a graph, 32 heads over 8, whole against cut: 1 x 128 tokens
+// 4.9 against 7.4 us, 1 x 333 7.8 / 7.6 (but 3 us of the host for the second launch),
+// 64 x 256 12 / 18, 64 x 512 26 / 33; and 1 x 512 9.2 / 7.5.
+constexpr int kWholeKeys = 384;
+constexpr int kWholeKeysMany = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 // The reference maximum moves only when a score exceeds it by more than
 // 2^kSlack: any reference gives the same quotient O / l, and weights up to 2^8 are
@@ -191,7 +193,7 @@ struct Walk {
 // This CTA's share, from the lengths: every thread sums a run of sequences, a
 // block scan places the runs, and the thread whose run holds the first unit
 // finds the sequence in it. False when the CTA has no share.
-__device__ bool find_share(const DecodeParams& p, Walk* w, int64_t* total_units, int* shares) {
+__device__ bool find_share(const DecodeParams& p, Walk* w, ShareCut* share) {
   __shared__ int64_t warp_sum[kWarps];
   __shared__ Walk found;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -216,11 +218,10 @@ __device__ bool find_share(const DecodeParams& p, Walk* w, int64_t* total_units,
   }
   const int per_seq = p.c.heads * p.head_blocks;
   const int64_t W = all * per_seq;
-  const int n = W < gridDim.x ? static_cast<int>(W) : static_cast<int>(gridDim.x);
-  *total_units = W;
-  *shares = n;
-  if (static_cast<int>(blockIdx.x) >= n) return false;
-  const int64_t first = blockIdx.x * W / n, last = (blockIdx.x + 1) * W / n;
+  const ShareCut cut = share_cut(W, W < gridDim.x ? static_cast<int>(W) : static_cast<int>(gridDim.x));
+  *share = cut;
+  if (blockIdx.x >= cut.count) return false;
+  const int64_t first = share_begin(cut, blockIdx.x), last = share_begin(cut, blockIdx.x + 1);
   if (first >= before * per_seq && first < (before + mine) * per_seq) {
     int64_t at = before * per_seq;
     for (int b = b0; b < b1; ++b) {
@@ -229,7 +230,7 @@ __device__ bool find_share(const DecodeParams& p, Walk* w, int64_t* total_units,
       if (first < at + static_cast<int64_t>(units) * per_seq) {
         Walk f;
         f.s.b = b;
-        f.s.j = static_cast<int>((first - at) / units);
+        f.s.j = small_quotient(first - at, units);
         f.s.len = len;
         f.s.units = units;
         f.s.r0 = static_cast<int>((first - at) - static_cast<int64_t>(f.s.j) * units);
@@ -262,9 +263,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   const int quad = lane & 3, row8 = lane >> 2;
 
   Walk w;
-  int64_t W;
-  int shares;
-  const bool has_share = find_share(p, &w, &W, &shares);
+  ShareCut share;
+  const bool has_share = find_share(p, &w, &share);
   if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (!has_share) return;
 
@@ -448,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
       int parts = 1;
       if (!whole) {
         // the item's last unit lies in the last of its shares
-        const int64_t x = w.u + s.units - 1;
-        parts = static_cast<int>(((x + 1) * shares - 1) / W) - static_cast<int>(blockIdx.x) + 1;
+        parts = static_cast<int>(last_boundary(share, w.u + s.units - 1) - blockIdx.x) + 1;
         p.meta[blockIdx.x] = make_int4(s.b, s.j, parts, slot);
       }
       if (p.scores)
@@ -722,7 +721,7 @@ bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
   pl.score_heads = pl.head_blocks > 1 ? pl.block_heads : (group + 3) / 4 * 4;
   const int64_t capacity = static_cast<int64_t>(c.max_pages) * c.page_size;
   const int64_t items = static_cast<int64_t>(c.batch) * c.heads * pl.head_blocks;
-  pl.whole = capacity <= kWholeKeys || (capacity <= 2 * kWholeKeys && items >= pl.shares);
+  pl.whole = capacity <= kWholeKeys || (capacity <= kWholeKeysMany && items >= pl.shares);
   int64_t at = 0;
   auto take = [&](int64_t n) {
     const int64_t here = at;
@@ -814,7 +813,7 @@ cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t l
   p.group = H / cache.heads;
   p.head_blocks = pl.head_blocks;
   p.block_heads = pl.block_heads;
-  p.unit_tiles = pl.whole ? 2 * kWholeKeys / kTileKeys : kUnitTiles;
+  p.unit_tiles = pl.whole ? kWholeKeysMany / kTileKeys : kUnitTiles;
   p.score_heads = pl.score_heads;
   p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.o = o;
