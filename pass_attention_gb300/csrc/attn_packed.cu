@@ -42,6 +42,7 @@
 #include <cstdint>
 
 #include "device_common.cuh"
+#include "launch.cuh"
 #include "oss_internal.h"
 #include "packed_plan.h"
 #include "tcgen05.cuh"
@@ -439,7 +440,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag_s;
   volatile int* abort_flag = &abort_flag_s;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_kernel_start();
 
   const uint32_t sbase = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5;
@@ -479,6 +480,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
+  wait_for_previous_kernel();
   if (threadIdx.x < p.rounds) p.meta[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
   find_shares(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
   tc_fence_after();
@@ -917,7 +919,8 @@ constexpr int kJoinThreads = 2 * kBM;
 
 template <int D, bool kF16>
 __global__ void __launch_bounds__(kJoinThreads) attn_packed_join_kernel(const PackedParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   const int share = blockIdx.x;
   const int4 meta = p.meta[share];
   const int parts = meta.x;
@@ -1032,18 +1035,9 @@ cudaError_t launch_shape(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) smem_set[dev].store(true, std::memory_order_release);
   }
-  attn_packed_kernel<D, kF16><<<ctas, kThreads, Smem<D>::kBytes, stream>>>(mq, mk, mv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas * p.rounds, D / 32);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_packed_join_kernel<D, kF16>, p);
+  e = launch_after(attn_packed_kernel<D, kF16>, dim3(ctas), kThreads, Smem<D>::kBytes, stream, mq, mk, mv, p);
+  if (e != cudaSuccess) return e;
+  return launch_after(attn_packed_join_kernel<D, kF16>, dim3(ctas * p.rounds, D / 32), kJoinThreads, 0, stream, p);
 }
 
 }  // namespace

@@ -38,6 +38,7 @@
 #include <cstdint>
 
 #include "device_common.cuh"
+#include "launch.cuh"
 #include "oss_internal.h"
 #include "packed_plan.h"
 #include "paged.h"
@@ -146,9 +147,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
 }
-
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Units [r0, r1) of an item: sequence b, key head and head block j.
 struct Segment {
@@ -259,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float merge_m[kWarps][8], merge_l[kWarps][8];
   let_next_kernel_start();
+  wait_for_previous_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane & 3, row8 = lane >> 2;
 
@@ -628,8 +627,8 @@ __device__ __forceinline__ void add_weights(const DecodeParams& p, int b, int g,
   __shared__ float lse2[kMaxHeadBlock];
   const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
   const int t0 = chunk * kAddKeys + threadIdx.x;
-  if (chunk * kAddKeys >= len) return;
   wait_for_previous_kernel();
+  if (chunk * kAddKeys >= len) return;
   const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
   float was[kAddKeysPerThread], sum[kAddKeysPerThread];
 #pragma unroll
@@ -691,6 +690,7 @@ __device__ __forceinline__ void add_weights(const DecodeParams& p, int b, int g,
 template <bool kF16, int D>
 __global__ void __launch_bounds__(kFinishThreads)
 decode_finish_kernel(const DecodeParams p, int adds, int chunks, float* weights, int64_t ld_w_batch, int64_t ld_w_head) {
+  let_next_kernel_start();
   int i = blockIdx.x;
   if (i < adds) {
     const int chunk = i % chunks, row = i / chunks;
@@ -743,20 +743,6 @@ bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
   return true;
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <bool kF16, int D, int NT>
 cudaError_t launch_shape(const DecodeParams& p, int shares, float* weights, int64_t ld_w_batch, int64_t ld_w_head,
                          cudaStream_t stream) {
@@ -772,14 +758,13 @@ cudaError_t launch_shape(const DecodeParams& p, int shares, float* weights, int6
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) smem_set[dev].store(true, std::memory_order_release);
   }
-  decode_paged_kernel<kF16, D, NT><<<shares, kThreads, smem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_after(decode_paged_kernel<kF16, D, NT>, dim3(shares), kThreads, smem, stream, p)) != cudaSuccess) return e;
   const int64_t joins = p.unit_tiles == kUnitTiles ? static_cast<int64_t>(shares) * p.block_heads : 0;
   const int64_t chunks = weights ? ((static_cast<int64_t>(p.c.max_pages) << p.c.page_shift) + kAddKeys - 1) / kAddKeys : 0;
   const int64_t adds = chunks * p.c.heads * p.c.batch, ctas = adds + joins;
   if (ctas > 0x7fffffff) return cudaErrorNotSupported;
   if (ctas == 0) return cudaSuccess;
-  return launch_after(decode_finish_kernel<kF16, D>, dim3(static_cast<unsigned>(ctas)), kFinishThreads, stream, p,
+  return launch_after(decode_finish_kernel<kF16, D>, dim3(static_cast<unsigned>(ctas)), kFinishThreads, 0, stream, p,
                       static_cast<int>(adds), static_cast<int>(chunks), weights, ld_w_batch, ld_w_head);
 }
 
