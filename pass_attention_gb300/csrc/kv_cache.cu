@@ -173,15 +173,18 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
   const int in_cluster = static_cast<int>(rank) * kSelectThreads + tid, all_threads = static_cast<int>(C) * kSelectThreads;
   if (head == 0 && in_cluster == 0) p.new_len[seq] = keep;
 
-  for (int i = in_cluster; i < recent; i += all_threads) {
-    kept[choose + i] = older + i;
-    nw[choose + i] = w[older + i];
-  }
-  for (int i = keep + in_cluster; i < p.budget; i += all_threads) kept[i] = -1;
-  for (int i = keep + in_cluster; i < room; i += all_threads) nw[i] = 0.f;
-  if (choose == 0) return;  // the same for the whole cluster
-  if (choose == older) {
-    for (int i = in_cluster; i < older; i += all_threads) {
+  // the rows' parts that need no selection
+  auto write_rest = [&]() {
+    for (int i = in_cluster; i < recent; i += all_threads) {
+      kept[choose + i] = older + i;
+      nw[choose + i] = w[older + i];
+    }
+    for (int i = keep + in_cluster; i < p.budget; i += all_threads) kept[i] = -1;
+    for (int i = keep + in_cluster; i < room; i += all_threads) nw[i] = 0.f;
+  };
+  if (choose == 0 || choose == older) {  // the same for the whole cluster
+    write_rest();
+    for (int i = in_cluster; i < choose; i += all_threads) {
       kept[i] = i;
       nw[i] = w[i];
     }
@@ -192,11 +195,11 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
   const int first = min(older, static_cast<int>(rank) * slice);
   const int n = min(older - first, slice);
   auto bits_at = [&](int i) -> uint32_t { return kCached ? slice_bits[i] : __float_as_uint(w[first + i]); };
-  for (int i = tid; i < kDigits * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
   if constexpr (kCached) {
-#pragma unroll 16
+#pragma unroll 8
     for (int i = tid; i < n; i += kSelectThreads) slice_bits[i] = __float_as_uint(__ldg(w + first + i));
   }
+  for (int i = tid; i < kDigits * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
 
   // the smallest kept key, and how many keys equal to it are kept
@@ -218,7 +221,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
       const uint32_t c = __reduce_add_sync(0xffffffffu, hist[d][(2 * warp + i) * 32 + lane]);
       if (lane == 0) coarse[d][2 * warp + i] = c;
     }
-    cluster_sync_all();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (d == 0) {
+      write_rest();
+      __syncwarp();
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == 0) {
       // over all slices, from the top: lane l has sums 63 - 2 l and 62 - 2 l
       uint2 peer[kMaxCluster];
@@ -251,12 +259,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
       const uint32_t l = __ffs(__ballot_sync(0xffffffffu, above + within >= ties)) - 1;
       if (lane == l) {
         found_digit = sum_of * 32 + 31 - lane;
-        found_rank = ties - above - (within - count);
+        const uint32_t rank_in = ties - above - (within - count);
+        found_rank = rank_in < count ? rank_in : 0;
       }
     }
     __syncthreads();
     last |= found_digit << shift;
     ties = found_rank;
+    if (ties == 0) {
+      // the whole bin is kept: every key from its first on (a digit is never 0 in
+      // front, -infinity's key being 0x007fffff)
+      --last;
+      break;
+    }
   }
 
   // a thread's run of keys: contiguous, of odd length (no bank conflicts)
