@@ -486,6 +486,7 @@ OSS_API os_status os_merge_partials(const float* part_m, const float* part_l, co
  *                     first pages are read.
  *   kv_len            [batch] int32, DEVICE; a value outside 0 .. max_pages *
  *                     page_size is clamped to it on the device.
+ *                     Positive where the dimension is longer than 1.
  *   page_size a power of two, 16 .. 1024 (others: OS_ERR_UNSUPPORTED).
  *   head_dim 64 or 128 (others: OS_ERR_UNSUPPORTED).  dtype an os_dtype.
  *   batch <= 65535, max_pages * page_size <= 2^30.
@@ -548,7 +549,8 @@ OSS_API os_status os_kv_cache_append(const void* k, const void* v, int64_t ld_to
  *             weights[b, g, t] += sum over the query heads h of key head g of
  *                                 exp(s_t - lse)
  *         element (b, g, t) at b * ld_w_batch + g * ld_w_head + t, for t <
- *         kv_len[b]; others are left as they are. os_kv_cache_evict takes them.
+ *         kv_len[b]; others are left as they are. The strides are positive
+ *         where the dimension is longer than 1. os_kv_cache_evict takes them.
  *   workspace  device memory of at least
  *         os_attention_decode_paged_workspace_bytes bytes, 16-byte aligned;
  *         it needs no initialising and keeps nothing between calls. Calls
@@ -682,7 +684,8 @@ OSS_API os_status os_check_device_error(void* stream, int32_t* code);
  * the next call of the kind's entry point made by the calling host thread
  * (that call disarms it):
  *   kind 0: disarm.
- *   kind 1: the kernel's load warp skips the V tile of KV step `step` (counted
+ *   kind 1: (os_attention_fwd, its variants and os_attention_fwd_packed) the
+ *           kernel's load warp skips the V tile of KV step `step` (counted
  *           in the order each CTA visits its KV tiles), so the thread that
  *           issues P V waits on a phase that never completes. After
  *           `timeout_ns` (0: the default of 2 s) it raises the CTA's abort
@@ -691,6 +694,8 @@ OSS_API os_status os_check_device_error(void* stream, int32_t* code);
  *           the recorded error and stop too). os_check_device_error then
  *           returns OS_ERR_TIMEOUT with code & 0xFFFF = 1 | (3 << 8) (kernel
  *           1, wait site 3: V tile full); bits 16..31 hold the launch's tag.
+ *           os_attention_fwd_packed reports 4 | (site << 8), the site of one
+ *           of the waits that ran out, and no tag.
  *           The CUDA context stays usable; the outputs of that call are
  *           undefined.
  *   kind 2: the next os_softmax_rows or os_softmax_rows_16bit call. If it

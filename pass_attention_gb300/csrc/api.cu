@@ -63,7 +63,9 @@ os_status check_cache(const os_paged_cache* c) {
       c->max_pages <= 0)
     return OS_ERR_INVALID_ARGUMENT;
   if (c->dtype != OS_DTYPE_BF16 && c->dtype != OS_DTYPE_F16) return OS_ERR_INVALID_ARGUMENT;
-  if (c->ld_page < 0 || c->ld_head < 0 || c->ld_slot < 0 || c->ld_table < 0) return OS_ERR_INVALID_ARGUMENT;
+  // a stride of 0 would put several rows of a pool in one place
+  if (c->ld_page < (c->num_pages > 1) || c->ld_head < (c->heads > 1) || c->ld_slot < 1 || c->ld_table < 0)
+    return OS_ERR_INVALID_ARGUMENT;
   if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || ((c->ld_page | c->ld_head | c->ld_slot) & 7))
     return OS_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(c->page_table) | reinterpret_cast<uintptr_t>(c->kv_len)) & 3u)
@@ -405,7 +407,7 @@ os_status os_attention_decode_paged(const void* q, int64_t ld_q_batch, int64_t l
   if (st != OS_OK) return st;
   if (!q || !o || !workspace || H <= 0 || H % cache->heads || !valid_scale(scale)) return OS_ERR_INVALID_ARGUMENT;
   if (ld_q_batch < 0 || ld_q_head < 0) return OS_ERR_INVALID_ARGUMENT;
-  if (weights && (ld_w_batch < 0 || ld_w_head < 0)) return OS_ERR_INVALID_ARGUMENT;
+  if (weights && (ld_w_batch < (cache->batch > 1) || ld_w_head < (cache->heads > 1))) return OS_ERR_INVALID_ARGUMENT;
   if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || ((ld_q_batch | ld_q_head) & 7))
     return OS_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(weights)) & 3u) return OS_ERR_MISALIGNED;

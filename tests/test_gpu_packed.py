@@ -67,7 +67,8 @@ def test_queries_and_keys_of_different_lengths(lens_q, lens_k, causal):
         assert torch.all(o == 3.0)
 
 
-@pytest.mark.parametrize("lens,hq,hkv", [([1500, 2, 999], 8, 2), ([2049], 2, 2), ([5] * 500, 4, 2), ([700] * 12, 4, 4)])
+@pytest.mark.parametrize("lens,hq,hkv", [([1500, 2, 999], 8, 2), ([2049], 2, 2), ([5] * 500, 4, 2), ([700] * 12, 4, 4),
+                                         ([1, 0, 2, 3] * 700, 2, 1)])
 def test_long_and_many(lens, hq, hkv):
     run(lens, lens, hq, hkv, seed=len(lens))
 

@@ -90,6 +90,7 @@ def test_decode_pages_and_layouts(page, layout):
     ([40001], 8, 1),                        # one sequence, one key head, over the whole GPU
     ([1, 20000, 3, 0, 777, 20001], 8, 2),   # long and short ones side by side
     ([130] * 300, 4, 2),                    # many sequences
+    ([1, 17, 0, 40] * 600, 2, 1),
 ])
 def test_decode_long_and_many(lens, hq, hkv):
     decode(lens, hq, hkv, weights=True, page=64, seed=len(lens))
@@ -450,6 +451,8 @@ def test_refusals():
             dec(**bad)
     with pytest.raises(oss.OssError, match="INVALID"):
         dec(scale=0.0)
+    with pytest.raises(oss.OssError, match="INVALID"):
+        dec(weights=w[:, :1].expand(2, 2, 32))  # the heads' sums in one place
     with pytest.raises(oss.OssError, match="MISALIGNED"):
         dec(q=torch.zeros(2, 4, 132, dtype=q.dtype, device="cuda")[..., :128])
     for bad in (dict(k=k[:, :1], v=k[:, :1]), dict(v=k[:1]), dict(cu_seqlens=kv_len), dict(k=k[..., :64], v=k[..., :64])):
