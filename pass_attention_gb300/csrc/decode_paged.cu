@@ -630,9 +630,11 @@ __device__ __forceinline__ void join_head(const DecodeParams& p, int share, int 
 // meanwhile.
 __device__ __forceinline__ void add_weights(const DecodeParams& p, int b, int g, int chunk, float* __restrict__ weights) {
   __shared__ float lse2[kMaxHeadBlock];
+  // (the lengths too may come from a kernel that still runs, one before the first
+  // kernel: an eviction writes them)
+  wait_for_previous_kernel();
   const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
   const int t0 = chunk * kAddKeys + threadIdx.x;
-  wait_for_previous_kernel();
   if (chunk * kAddKeys >= len) return;
   const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
   float was[kAddKeysPerThread], sum[kAddKeysPerThread];

@@ -116,6 +116,41 @@ def test_prompts_steps_and_evictions():
     assert oss.check_device_error() == 0
 
 
+@pytest.mark.parametrize("stale", [0, 1 << 20])
+def test_decode_directly_behind_an_eviction(stale):
+    # the lengths that eviction writes are the next call's kv_len, with no other
+    # kernel between the two: every kernel of the decode has to wait for them,
+    # whatever the buffer held before
+    batch, hkv, hq, page, n, budget = 4, 2, 8, 16, 8000, 1000
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(11)
+    columns, new_columns = n // page, -(-budget // page) + 1
+    pages = batch * (columns + new_columns)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    kp, vp = (r(pages, hkv, page, 128).to(torch.bfloat16) for _ in range(2))
+    order = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+    table = order[:batch * columns].view(batch, columns)
+    new_table = order[batch * columns:].view(batch, new_columns)
+    kv_len = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    w = r(batch, hkv, n).square_()
+    q = r(batch, hq, 128).to(torch.bfloat16)
+    new_len = torch.empty(batch, dtype=torch.int32, device="cuda")
+    new_w = torch.empty((batch, hkv, new_columns * page), device="cuda")
+    want = None
+    for i in range(10):
+        new_len.fill_(budget if i == 0 else stale)
+        oss.kv_cache_evict(kp, vp, w, table, kv_len, new_table, budget, 10, new_len=new_len, new_weights=new_w)
+        if i == 0:
+            torch.cuda.synchronize()
+        o, lse = oss.attention_decode_paged(q, kp, vp, new_table, new_len, weights=new_w)
+        got = o.view(torch.int16).clone(), lse.clone(), new_w.clone()
+        if i == 0:
+            want = got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.all(new_w[:, :, budget:] == 0)
+    assert oss.check_device_error() == 0
+
+
 def test_a_step_in_a_graph_follows_the_cache():
     # length, append, decode and weights in one captured step, replayed token by
     # token beside the same steps made one by one
