@@ -516,7 +516,9 @@ typedef struct os_paged_cache {
  *   cu_seqlens  [batch + 1] int32, DEVICE: the new tokens of sequence b are
  *               rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (none is fine), in
  *               ascending order; rows behind the last sequence are not
- *               read. NULL: one new token for each sequence, tokens == batch.
+ *               read. NULL: one new token for each sequence, tokens == batch; a
+ *               sequence whose kv_len is 0 (an empty place of a padded batch)
+ *               has none.
  * Two rows that name the same slot (a page shared by two sequences) leave one
  * of the two there; which one is not determined.
  * Positions below 0 or without a page are left out and set the error word.

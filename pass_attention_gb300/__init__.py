@@ -768,7 +768,7 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_p
     both), page_table [batch, max_pages] and kv_len [batch] int32 on the device.
     kv_len counts the new tokens: those of sequence b, rows cu_seqlens[b] ..
     cu_seqlens[b + 1] - 1, go to its last positions. cu_seqlens None: one token
-    for each sequence. See ``os_kv_cache_append``."""
+    for each sequence, none for those of kv_len 0. See ``os_kv_cache_append``."""
     cache, dev, batch, heads, d, _, _ = _cache(k_pages, v_pages, page_table, kv_len)
     sk = _pair(k, v, ("k", "v"), 3, k_pages.dtype, dev)
     tokens, hk, dk = k.shape

@@ -69,7 +69,9 @@ kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
       if (seq < 0) continue;  // a row of no sequence
       behind = cu[seq + 1] - token;
     }
-    const int64_t pos = c.kv_len[seq] - behind;
+    const int32_t len = c.kv_len[seq];
+    if (!cu && len == 0) continue;  // an empty place of the batch
+    const int64_t pos = len - behind;
     if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) {
       bad_index(err, kSiteBadPosition);
       continue;

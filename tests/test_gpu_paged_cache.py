@@ -282,6 +282,29 @@ def test_append_one_token_each():
     assert torch.equal(vp.view(torch.int16), wv.view(torch.int16))
 
 
+@pytest.mark.parametrize("cu", [False, True])
+def test_append_and_decode_of_a_padded_batch(cu):
+    # places of the batch without a sequence: kv_len 0, no page, a row that is
+    # not read; with offsets, a new token that has no position is reported
+    lens = [0, 17, 0, 40]
+    q, kp, vp, table, kv_len, _ = make(lens, 4, 2, seed=24)
+    k, v = (torch.randn((4, 2, 128), device="cuda").to(torch.bfloat16) for _ in range(2))
+    wk, wv = kp.clone(), vp.clone()
+    for b, n in ((1, 17), (3, 40)):
+        at = table[b, (n - 1) // 16].long()
+        wk[at, :, (n - 1) % 16], wv[at, :, (n - 1) % 16] = k[b], v[b]
+    oss.kv_cache_append(k, v, kp, vp, table, kv_len, ints([0, 1, 2, 3, 4]) if cu else None)
+    if cu:
+        with pytest.raises(oss.OssError, match="OS_ERR_BAD_INDEX"):
+            oss.check_device_error()
+    assert oss.check_device_error() == 0
+    assert torch.equal(kp.view(torch.int16), wk.view(torch.int16))
+    assert torch.equal(vp.view(torch.int16), wv.view(torch.int16))
+    o, lse = oss.attention_decode_paged(q, kp, vp, table, kv_len)
+    assert oss.check_device_error() == 0
+    check_decode(o, lse, q, kp, vp, table, kv_len, 1.0 / math.sqrt(128))
+
+
 def test_append_many_tokens():
     lens = [4000, 1, 2500]
     _, kp, vp, table, kv_len, _ = make(lens, 8, 8, page=64, seed=22)
@@ -295,7 +318,7 @@ def test_append_many_tokens():
         at += n
 
 
-@pytest.mark.parametrize("kv_len,entry", [([16, 40], -1), ([16, 40], 99999), ([0, 40], None), ([16, 65], None)])
+@pytest.mark.parametrize("kv_len,entry", [([16, 40], -1), ([16, 40], 99999), ([-1, 40], None), ([16, 65], None)])
 def test_append_leaves_out_what_has_no_place(kv_len, entry):
     # a bad page, a position before the first, one behind the last page: the
     # other sequence's row is written, nothing else is, and it is reported
