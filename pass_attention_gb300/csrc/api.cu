@@ -55,6 +55,12 @@ thread_local oss::AttnFault t_fault;
 // Armed by os_debug_inject_fault (kind 2), consumed by the next
 // os_softmax_rows or os_softmax_rows_16bit on the same host thread.
 thread_local oss::RowsFault t_rows_fault;
+// Whether two runs of 4-byte elements share one.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < static_cast<uintptr_t>(na) * 4 : x - y < static_cast<uintptr_t>(nb) * 4;
+}
+
 // What every call on a paged cache asks of it. The pools themselves are
 // checked by the calls that follow them.
 os_status check_cache(const os_paged_cache* c) {
@@ -480,6 +486,13 @@ os_status os_kv_cache_evict(const os_paged_cache* cache, const float* weights, i
        reinterpret_cast<uintptr_t>(new_weights)) & 3u)
     return OS_ERR_MISALIGNED;
   if (room > (int64_t(1) << 30)) return OS_ERR_UNSUPPORTED;
+  // what is read by one CTA while another writes
+  const int64_t rows = static_cast<int64_t>(cache->batch) * cache->heads;
+  const int64_t span = (cache->batch - 1) * ld_w_batch + (cache->heads - 1) * ld_w_head +
+                       static_cast<int64_t>(cache->max_pages) * cache->page_size;
+  if (new_table == cache->page_table || overlap(new_len, cache->batch, cache->kv_len, cache->batch) ||
+      overlap(new_weights, rows * room, weights, span))
+    return OS_ERR_INVALID_ARGUMENT;
   unsigned int* err = error_word();
   if (!err) return OS_ERR_CUDA;
   return from_cuda(oss::launch_kv_evict(*cache, weights, ld_w_batch, ld_w_head, new_table, ld_new_table,

@@ -8,6 +8,7 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
 import pass_attention_gb300 as oss
 from pass_attention_gb300 import build_lib
@@ -139,6 +140,25 @@ def test_evict_rejects_bad_arguments(lib):
         assert evict(lib, c, **bad) == INVALID, bad
     for bad in (dict(w=A + 1), dict(table=A + 2), dict(kept=A + 3), dict(n=A + 1), dict(nw=A + 2)):
         assert evict(lib, c, **bad) == MISALIGNED, bad
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls that are not refused would run on stand-in addresses")
+def test_evict_refuses_what_it_would_overwrite(lib):
+    # batch 2, 2 heads, 64 positions: weights and new_weights of 1024 bytes each
+    MB = 1 << 20
+    c = ctypes.byref(cache(page_table=MB, kv_len=2 * MB, batch=2, heads=2, page_size=16, max_pages=4))
+    free = dict(w=3 * MB, ldw=(128, 64), table=4 * MB, kept=5 * MB, n=6 * MB, nw=7 * MB)
+    no_device = evict(lib, c, **free)
+    assert no_device not in (0, INVALID, MISALIGNED, UNSUPPORTED)
+    for n in (-8, 8):
+        assert evict(lib, c, **{**free, "n": 2 * MB + n}) == no_device
+    for n in (-4, 0, 4):
+        assert evict(lib, c, **{**free, "n": 2 * MB + n}) == INVALID
+    for n in (-1024, 1024):
+        assert evict(lib, c, **{**free, "nw": 3 * MB + n}) == no_device
+    for n in (-1020, 0, 1020):
+        assert evict(lib, c, **{**free, "nw": 3 * MB + n}) == INVALID
+    assert evict(lib, c, **{**free, "table": MB}) == INVALID
 
 
 PROBE = r"""

@@ -487,4 +487,8 @@ def test_refusals():
                 dict(weights=w[..., :31]), dict(kept=w), dict(new_weights=w)):
         with pytest.raises((ValueError, TypeError)):
             evi(**bad)
+    for bad in (dict(new_page_table=table), dict(new_len=kv_len),
+                dict(new_page_table=free[:4].reshape(2, 2), new_weights=w)):
+        with pytest.raises(oss.OssError, match="INVALID"):
+            evi(**bad)
     assert oss.check_device_error() == 0
