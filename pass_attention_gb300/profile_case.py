@@ -6,11 +6,18 @@
     python -m pass_attention_gb300.profile_case attn [--B --H --S] [--causal] [--reps N]
     python -m pass_attention_gb300.profile_case decode [--B --H --Lmax --splits] [--reps N]
     python -m pass_attention_gb300.profile_case merge [--B --H --Lmax --splits] [--reps N]
+    python -m pass_attention_gb300.profile_case packed [--B --H --Hkv --S] [--reps N]
+    python -m pass_attention_gb300.profile_case paged [--B --H --Hkv --Lmax] [--weights] [--reps N]
+    python -m pass_attention_gb300.profile_case evict [--B --Hkv --Lmax] [--reps N]
 
 ``merge`` runs the split-KV decode once and then the merge ``--reps`` times on
 its partials: the merge's inputs are the decode's (B, H, splits) partial
 arrays, whose size does not depend on Lmax, so a short cache gives the same
 merge launch with little memory held.
+
+``packed``, ``paged`` and ``evict`` run ``attention_fwd_packed`` (causal),
+``attention_decode_paged`` and ``kv_cache_evict`` (to an eighth) on B sequences
+whose lengths spread evenly up to S or Lmax, head dimension 128, pages of 16.
 
 ``--no-ws`` calls ``os_softmax_rows`` / ``os_softmax_rows_16bit`` without a
 workspace, so rows over 1.6 MB take the kernels that stream them twice from
@@ -51,14 +58,48 @@ def _no_ws(x, y, kind):
         raise oss.OssError(st, "softmax without a workspace")
 
 
+def _cache_case(a):
+    B, H, page, d = a.B or 8, a.H or 32, 16, 128
+    most = a.S if a.case == "packed" else a.Lmax
+    lens = [max(1, most * (b + 1) // B) for b in range(B)]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    draw = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    if a.case == "packed":
+        cu = ints([sum(lens[:b]) for b in range(B + 1)])
+        q, k, v = draw(sum(lens), H, d), draw(sum(lens), a.Hkv, d), draw(sum(lens), a.Hkv, d)
+        call = lambda: oss.attention_fwd_packed(q, k, v, cu)  # noqa: E731
+    else:
+        columns, new_columns = -(-most // page), -(-most // 8 // page)
+        pages = B * (columns + new_columns)
+        kp, vp = draw(pages, a.Hkv, page, d), draw(pages, a.Hkv, page, d)
+        order = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+        table, new_table = order[:B * columns].view(B, columns), order[B * columns:].view(B, new_columns)
+        kv_len, q = ints(lens), draw(B, H, d)
+        weights = torch.rand((B, a.Hkv, columns * page), generator=gen, device="cuda")
+        if a.case == "paged":
+            call = lambda: oss.attention_decode_paged(q, kp, vp, table, kv_len,  # noqa: E731
+                                                      weights=weights if a.weights else None)
+        else:
+            call = lambda: oss.kv_cache_evict(kp, vp, weights, table, kv_len, new_table, most // 8, 16)  # noqa: E731
+    for _ in range(a.reps):
+        call()
+        torch.cuda.synchronize()
+    oss.check_device_error()
+    print("tokens", sum(lens))
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("case", choices=["softmax", "softmax16", "multipass", "attn", "decode", "merge"])
+    ap.add_argument("case", choices=["softmax", "softmax16", "multipass", "attn", "decode", "merge",
+                                     "packed", "paged", "evict"])
     ap.add_argument("--passes", type=int, default=3)
     ap.add_argument("--rows", type=int, default=32768)
     ap.add_argument("--cols", type=int, default=8192)
     ap.add_argument("--B", type=int, default=None)
     ap.add_argument("--H", type=int, default=None)
+    ap.add_argument("--Hkv", type=int, default=8)
     ap.add_argument("--S", type=int, default=4096)
     ap.add_argument("--Lmax", type=int, default=32768)
     ap.add_argument("--splits", type=int, default=16)
@@ -66,6 +107,7 @@ def main(argv=None):
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--dtype", choices=["bf16", "f16"], default="bf16")
     ap.add_argument("--no-ws", action="store_true")
+    ap.add_argument("--weights", action="store_true")
     a = ap.parse_args(argv)
     oss.load()
     if a.case == "softmax":
@@ -100,6 +142,8 @@ def main(argv=None):
             oss.attention_fwd(q, k, v, 1.0 / math.sqrt(128), a.causal)
             torch.cuda.synchronize()
         oss.check_device_error()
+    elif a.case in ("packed", "paged", "evict"):
+        _cache_case(a)
     elif a.case == "merge":
         B, H = a.B or 64, a.H or 32
         q, k, v, kv = workloads.decode_inputs(B, H, a.Lmax, 128, seed=4, device="cuda")
