@@ -20,9 +20,10 @@
 //   order; of the keys equal to the last one kept, the lowest positions are taken.
 // * move. Kept rows are copied page to page, four rows of a thread in flight.
 //
-// 2 x 8 rows of up to 131072 weights cut to 16384: 77 us, of them 42 the copy (at
-// the copy peak) and some 25 the selection, a chain of about ten meetings of a
-// cluster's CTAs; 8 x 8 rows of up to 8192 cut to 2048: 39 us, 23 and 11.
+// 2 x 8 rows of up to 131072 weights cut to 16384: 69 us, of them 42 the copy (at
+// the copy peak) and most of the rest the selection, a chain of about ten meetings
+// of a cluster's CTAs; 8 x 8 rows of up to 8192 cut to 2048: 37 us, 23 of them the
+// copy.
 
 #include <atomic>
 #include <cstdint>
@@ -203,10 +204,13 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
   const int n = min(older - first, slice);
   auto bits_at = [&](int i) -> uint32_t { return kCached ? slice_bits[i] : __float_as_uint(w[first + i]); };
   if constexpr (kCached) {
-#pragma unroll 8
-    for (int i = tid; i < n; i += kSelectThreads) slice_bits[i] = __float_as_uint(__ldg(w + first + i));
+    // (asynchronous: every key of a thread is on its way at once)
+#pragma unroll 4
+    for (int i = tid; i < n; i += kSelectThreads)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slice_bits + i)), "l"(w + first + i) : "memory");
   }
   for (int i = tid; i < kDigits * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
+  if constexpr (kCached) asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 
   // the smallest kept key, and how many keys equal to it are kept
@@ -229,10 +233,6 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
       if (lane == 0) coarse[d][2 * warp + i] = c;
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (d == 0) {
-      write_rest();
-      __syncwarp();
-    }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == 0) {
       // over all slices, from the top: lane l has sums 63 - 2 l and 62 - 2 l
@@ -321,6 +321,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
   }
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  // no store before this last barrier: its and the earlier ones' releases would wait
+  // for them (77 against 70 us for 2 x 8 rows of 131072)
+  write_rest();
   for (int i = r0; i < r1; ++i) {
     const uint32_t bits = bits_at(i), key = weight_key_bits(bits);
     if (key > last || (key == last && eq_at < ties)) {
