@@ -620,6 +620,12 @@ def _strides(t: torch.Tensor, name: str, ndim: int, dtype: torch.dtype, device: 
 
 def _pair(k: torch.Tensor, v: torch.Tensor, names, ndim: int, dtype: torch.dtype, device: torch.device):
     """The strides that k and v share."""
+    if isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor):
+        st = k.stride()
+        if len(st) == ndim and st[-1] == 1 and not (st[0] | st[1] | st[ndim - 2]) & 7 and v.stride() == st \
+                and k.dtype is dtype and v.dtype is dtype and k.device == device and v.device == device \
+                and v.shape == k.shape:
+            return st
     sk = _strides(k, names[0], ndim, dtype, device)
     sv = _strides(v, names[1], ndim, dtype, device)
     if v.shape != k.shape or (sv != sk and any(n > 1 and a != b for n, a, b in zip(k.shape, sk, sv))):
@@ -628,7 +634,7 @@ def _pair(k: torch.Tensor, v: torch.Tensor, names, ndim: int, dtype: torch.dtype
 
 
 def _ints(t: torch.Tensor, name: str, ndim: int, device: torch.device) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != ndim or t.device != device \
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.ndim != ndim or t.device != device \
             or (t.stride(-1) != 1 and t.shape[-1] > 1):
         _refuse(t, name, ndim, torch.int32, device)
 
@@ -654,12 +660,13 @@ def _cache(k_pages, v_pages, page_table, kv_len):
     batch, max_pages = page_table.shape
     if kv_len.shape[0] != batch:
         raise ValueError("kv_len must have one entry for each row of page_table")
-    if pages > 0x7fffffff or max_pages > 0x7fffffff or batch > 0x7fffffff:
-        raise ValueError("more pages than 32 bits count")
-    return (_PAGED_CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
-                              page_table.data_ptr(), page_table.stride(0), kv_len.data_ptr(), pages, heads,
-                              page_size, d, _DTYPE_CODES[dtype], batch, max_pages),
-            dev, batch, heads, d, max_pages * page_size, page_size)
+    try:
+        packed = _PAGED_CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
+                                   page_table.data_ptr(), page_table.stride(0), kv_len.data_ptr(), pages, heads,
+                                   page_size, d, _DTYPE_CODES[dtype], batch, max_pages)
+    except struct.error:
+        raise ValueError("more pages than 32 bits count") from None
+    return packed, dev, batch, heads, d, max_pages * page_size, page_size
 
 
 def _elsewhere(dev: torch.device, stream) -> bool:
@@ -681,8 +688,9 @@ def _on(dev: torch.device, stream):
 
 # The current device, and the raw current stream of a device, without making a
 # Stream object.
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 # Workspaces of the calls that launch two kernels, kept per (device, stream) up
 # to this size. The lock is held from taking one to the end of the launches:
@@ -693,7 +701,7 @@ _LAUNCH_LOCK = threading.Lock()
 
 
 def _scratch(dev: torch.device, sp: int, nbytes: int) -> torch.Tensor:
-    if nbytes > _KEEP_BYTES or torch.cuda.is_current_stream_capturing():
+    if nbytes > _KEEP_BYTES or _capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     key = (dev.index, sp, "cache")
     ws = _WORKSPACES.get(key)

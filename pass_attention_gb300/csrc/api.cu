@@ -55,6 +55,7 @@ thread_local oss::AttnFault t_fault;
 // Armed by os_debug_inject_fault (kind 2), consumed by the next
 // os_softmax_rows or os_softmax_rows_16bit on the same host thread.
 thread_local oss::RowsFault t_rows_fault;
+
 // Whether two runs of 4-byte elements share one.
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
