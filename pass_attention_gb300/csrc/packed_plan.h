@@ -5,7 +5,8 @@
 // sequence times a pack of 128 / positions query heads that share a key head.
 // It visits kv_tiles tiles of 128 keys. The items of a launch stand in a row,
 // (sequence, pack, tile)-major, each kTileWeight + kv_tiles long (a hand-over
-// costs about as much as two KV steps, by a fit over the CTAs' times of a ragged batch), and the
+// costs about as much as two KV steps, by a fit over the CTAs' times of a ragged batch: 8
+// sequences of 77 to 2500 tokens take 160 us with 2, 187 with 1, 164 with 3), and the
 // row is cut into equal shares, one or a few per CTA. A share's boundary that
 // falls inside an item cuts it along the keys, unless one side would get fewer
 // than kMinSteps KV steps: then the boundary moves to the item's edge.
