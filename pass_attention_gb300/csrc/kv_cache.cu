@@ -390,7 +390,7 @@ constexpr int kMaxDevices = 64;
 
 // Launch of the selection by clusters of C CTAs with `smem` bytes each. (Not
 // overlapped with the kernel before it: clusters that were placed between that
-// one's last CTAs took longer, 84 against 78 us for 2 x 8 rows of 131072.)
+// one's last CTAs took 6 us longer for 2 x 8 rows of 131072.)
 template <bool kCached>
 cudaLaunchConfig_t select_config(const EvictParams& p, int C, int smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[1]) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -468,7 +468,7 @@ cudaError_t launch_kv_evict(const os_paged_cache& cache, const float* weights, i
   // CTAs of a row: as many (up to eight) as fit on the GPU for all rows at once while a
   // slice keeps at least kLeastSlice keys, and as many as it takes for a slice
   // to fit shared memory where eight can do that. (16 rows of 131072 keys: clusters of
-  // eight do not all fit at once and took 92 us with the copy, clusters of seven 77 us.)
+  // eight do not all fit at once and took 15 us longer than clusters of seven.)
   const int64_t capacity = static_cast<int64_t>(cache.max_pages) * cache.page_size;
   const int64_t rows = static_cast<int64_t>(cache.heads) * cache.batch;
   int dev = 0;
