@@ -774,6 +774,11 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       float l_a = 0.f, l_b = 0.f;              // this thread's share of the row sums
       const int vis_a = p.causal ? min(u.k_len, u.vis + pos_a) : u.k_len;  // keys the rows see
       const int vis_b = p.causal ? min(u.k_len, u.vis + pos_b) : u.k_len;
+      // Rows behind the tile's queries hold another sequence's, or none: they have no
+      // vote on the rescale, which would change how the warp's own rows are rounded
+      // (-inf + inf is NaN, and no maximum exceeds either).
+      const float slack_a = pos_a < u.n_pos ? kRescaleSlack : -neg_inf();
+      const float slack_b = pos_b < u.n_pos ? kRescaleSlack : -neg_inf();
       OSS_ROLLED
       for (int j = u.s0; j < u.s1; ++j, before = r, r.next()) {
         const int b = r.at;
@@ -821,7 +826,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
         xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
         const float mnew_a = fmaxf(m_a, xa * C), mnew_b = fmaxf(m_b, xb * C);
-        const bool rescale = __any_sync(0xffffffffu, (mnew_a > m_a + kRescaleSlack) || (mnew_b > m_b + kRescaleSlack));
+        const bool rescale = __any_sync(0xffffffffu, (mnew_a > m_a + slack_a) || (mnew_b > m_b + slack_b));
         float corr_a = 1.f, corr_b = 1.f;
         if (rescale) {
           corr_a = ex2(m_a - ((mnew_a == neg_inf()) ? 0.f : mnew_a));  // 0 while m = -inf
