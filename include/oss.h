@@ -540,7 +540,8 @@ OSS_API os_status os_kv_cache_append(const void* k, const void* v, int64_t ld_to
  * GPU's SMs whatever the lengths are, and the partial states (m, l, O) of a
  * sequence cut between SMs are joined with the merge identity in a fixed
  * order, so every run gives the same bits. P is rounded to the cache's type for
- * the P V product, l sums the fp32 P. kv_len 0 gives o = 0, lse = -inf.
+ * the P V product, l sums the fp32 P. kv_len 0 gives o = 0, lse = -inf; a head
+ * whose scores hold NaN gives NaN in both, and in the weights of its key head.
  *
  *   q     [batch, H, D], device: element (b, h, d) at b * ld_q_batch +
  *         h * ld_q_head + d; the cache's type.

@@ -153,6 +153,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return w;
 }
 
+// What exponents are taken relative to where the maximum is m: 0 in place of -inf.
+// A part without a key then adds zeros, and one whose scores are NaN (which no
+// maximum shows) adds NaN instead of nothing.
+__device__ __forceinline__ float reference(float m) { return m == neg_inf() ? 0.f : m; }
+
 // Units [r0, r1) of an item: sequence b, key head and head block j.
 struct Segment {
   int b, j, len, units, r0, r1;
@@ -425,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
         float pe[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float ref = m[nt][e & 1] == neg_inf() ? 0.f : m[nt][e & 1];
-          pe[e] = ex2(sc[nt][e] - ref);
+          pe[e] = ex2(sc[nt][e] - reference(m[nt][e & 1]));
         }
         l[nt][0] += pe[0] + pe[2];
         l[nt][1] += pe[1] + pe[3];
@@ -487,26 +491,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
         for (int i = 0; i < kWarps; ++i) M = fmaxf(M, merge_m[i][hh]);
 #pragma unroll
         for (int k = 0; k < kDims; ++k) acc[k] = 0.f;
-        if (M != neg_inf()) {
 #pragma unroll
-          for (int i = 0; i < kWarps; ++i) {
-            const float f = ex2(merge_m[i][hh] - M);
-            L = fmaf(merge_l[i][hh], f, L);
-            const float4* src = reinterpret_cast<const float4*>(merge + (i * 8 + hh) * S::kMergeLd + d0);
+        for (int i = 0; i < kWarps; ++i) {
+          const float f = ex2(merge_m[i][hh] - reference(M));
+          L = fmaf(merge_l[i][hh], f, L);
+          const float4* src = reinterpret_cast<const float4*>(merge + (i * 8 + hh) * S::kMergeLd + d0);
 #pragma unroll
-            for (int k = 0; k < kDims / 4; ++k) {
-              const float4 x = src[k];
-              acc[4 * k] = fmaf(x.x, f, acc[4 * k]);
-              acc[4 * k + 1] = fmaf(x.y, f, acc[4 * k + 1]);
-              acc[4 * k + 2] = fmaf(x.z, f, acc[4 * k + 2]);
-              acc[4 * k + 3] = fmaf(x.w, f, acc[4 * k + 3]);
-            }
+          for (int k = 0; k < kDims / 4; ++k) {
+            const float4 x = src[k];
+            acc[4 * k] = fmaf(x.x, f, acc[4 * k]);
+            acc[4 * k + 1] = fmaf(x.y, f, acc[4 * k + 1]);
+            acc[4 * k + 2] = fmaf(x.z, f, acc[4 * k + 2]);
+            acc[4 * k + 3] = fmaf(x.w, f, acc[4 * k + 3]);
           }
         }
         const int h = head0 + nt * 8 + hh;
         const int64_t row = static_cast<int64_t>(s.b) * p.H + h;
         if (whole) {
-          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const float inv = L != 0.f ? 1.f / L : 0.f;
           uint32_t out[kDims / 2];
 #pragma unroll
           for (int k = 0; k < kDims / 2; ++k) out[k] = pack2<kF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
@@ -516,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
           else
             *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
           if ((threadIdx.x & 15) == 0) {
-            const float e2 = L > 0.f ? M + log2f(L) : neg_inf();
-            if (p.lse) p.lse[row] = L > 0.f ? e2 * kLn2 : neg_inf();
+            const float e2 = L != 0.f ? M + log2f(L) : neg_inf();
+            if (p.lse) p.lse[row] = e2 * kLn2;
             if (p.scores) p.lse2[row] = e2;
           }
         } else {
@@ -582,15 +584,14 @@ __device__ __forceinline__ void join_head(const DecodeParams& p, int share, int 
     float to = M;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) to = fmaxf(to, ml[u].x);
-    if (to == neg_inf()) continue;
-    const float corr = ex2(M - to);
+    const float ref = reference(to), corr = ex2(M - ref);
     M = to;
     L *= corr;
 #pragma unroll
     for (int k = 0; k < kDims; ++k) acc[k] *= corr;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const float f = ex2(ml[u].x - M);
+      const float f = ex2(ml[u].x - ref);
       L = fmaf(ml[u].y, f, L);
 #pragma unroll
       for (int k = 0; k < kDims; ++k) acc[k] = fmaf(x[u][k], f, acc[k]);
@@ -609,19 +610,17 @@ __device__ __forceinline__ void join_head(const DecodeParams& p, int share, int 
   float a = 0.f, b = 0.f;
 #pragma unroll
   for (int i = 0; i < kFinishWarps; ++i) M = fmaxf(M, sm[i]);
-  if (M != neg_inf()) {
 #pragma unroll
-    for (int i = 0; i < kFinishWarps; ++i) {
-      const float f = ex2(sm[i] - M);
-      L = fmaf(sl[i], f, L);
-      a = fmaf(so[i][2 * threadIdx.x], f, a);
-      b = fmaf(so[i][2 * threadIdx.x + 1], f, b);
-    }
+  for (int i = 0; i < kFinishWarps; ++i) {
+    const float f = ex2(sm[i] - reference(M));
+    L = fmaf(sl[i], f, L);
+    a = fmaf(so[i][2 * threadIdx.x], f, a);
+    b = fmaf(so[i][2 * threadIdx.x + 1], f, b);
   }
   const int64_t row = static_cast<int64_t>(meta.x) * p.H + g * p.group + hb * p.block_heads + hh;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   reinterpret_cast<uint32_t*>(p.o + row * D)[threadIdx.x] = pack2<kF16>(a * inv, b * inv);
-  if (threadIdx.x == 0 && p.lse) p.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
+  if (threadIdx.x == 0 && p.lse) p.lse[row] = L != 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
 }
 
 // weights[b, g, t] += sum over the group's heads of 2^(s - lse). Each key's sum
@@ -667,12 +666,11 @@ __device__ __forceinline__ void add_weights(const DecodeParams& p, int b, int g,
             float M = neg_inf(), L = 0.f;
             for (int i = 0; i < meta.y; ++i) {
               const float2 ml = p.part_ml[part_slot(meta.x, i) * p.block_heads + threadIdx.x];
-              const float to = fmaxf(M, ml.x);
-              if (to == neg_inf()) continue;
-              L = fmaf(L, ex2(M - to), ml.y * ex2(ml.x - to));
+              const float to = fmaxf(M, ml.x), ref = reference(to);
+              L = fmaf(L, ex2(M - ref), ml.y * ex2(ml.x - ref));
               M = to;
             }
-            if (L > 0.f) e2 = M + log2f(L);
+            if (L != 0.f) e2 = M + log2f(L);
           }
           lse2[threadIdx.x] = e2;
         }
