@@ -592,8 +592,9 @@ OSS_API int64_t os_attention_decode_paged_workspace_bytes(int32_t H, const os_pa
  *
  *   q    [tokens_q, Hq, D], k, v [tokens_k, Hkv, D], device: element (t, h, d)
  *        at t * ld_token + h * ld_head + d, k and v with the same strides.
- *        q, k, v of the sequences are finite; rows outside every sequence
- *        and the other sequences' values do not reach a sequence's results,
+ *        k and v of the sequences are finite; a query whose scores are NaN
+ *        gives NaN in its own o and lse. Rows outside every sequence and
+ *        the other sequences' values do not reach a sequence's results,
  *        whatever they hold.
  *   o    [tokens_q, Hq, D] dense, the inputs' type (round to nearest even);
  *        lse [tokens_q, Hq] fp32, or NULL. Rows outside every sequence are

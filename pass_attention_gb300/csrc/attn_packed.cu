@@ -696,7 +696,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       const uint32_t stage = sbase + L::kOffQ + (kt & 1) * L::kTile + (warp - kEpiWarp) * (L::kTile / 4);  // [half][32 rows][128 bytes]
       if (u.s0 == 0 && u.s1 == u.n_kv) {
         // (a row without keys has O = 0: its weights are zeros and V is finite)
-        const float inv = ml.y > 0.f ? 1.0f / ml.y : 0.f;
+        const float inv = ml.y != 0.f ? 1.0f / ml.y : 0.f;
         OSS_ROLLED
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
@@ -727,7 +727,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         __syncwarp();
         if (p.lse && ((row0 + lane) >> head_shift) < u.n_pos)
-          p.lse[out_row(p, u.q_row, u.pack, row0 + lane)] = ml.y > 0.f ? (ml.x + __log2f(ml.y)) * kLn2 : neg_inf();
+          p.lse[out_row(p, u.q_row, u.pack, row0 + lane)] = ml.y != 0.f ? (ml.x + __log2f(ml.y)) * kLn2 : neg_inf();
       } else {
         const int64_t slot = 2 * static_cast<int64_t>(u.share) + (u.s0 == 0 ? 1 : 0);
         float4* dst = p.part_o + slot * (D / 4) * kBM + row0 + lane;
@@ -943,6 +943,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_packed_join_kernel(const Pa
   auto slot = [&](int i) -> int64_t { return 2 * (static_cast<int64_t>(share) + i) + (i == 0 ? 1 : 0); };
   float M = neg_inf();
   for (int i = 0; i < parts; ++i) M = fmaxf(M, p.part_ml[slot(i) * kBM + row].x);
+  const float ref = M == neg_inf() ? 0.f : M;
   float L = 0.f, acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
@@ -953,9 +954,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_packed_join_kernel(const Pa
     float4 v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = src[e * kBM];
-    // a part in which the row sees no key has m = -inf and adds nothing
-    if (ml.x == neg_inf()) continue;
-    const float f = ex2(ml.x - M);
+    // a part in which the row sees no key has l = 0 and adds nothing; one whose scores
+    // are NaN has NaN, although its maximum is -inf too
+    if (ml.y == 0.f) continue;
+    const float f = ex2(ml.x - ref);
     L = fmaf(ml.y, f, L);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -965,14 +967,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_packed_join_kernel(const Pa
       acc[4 * e + 3] = fmaf(v[e].w, f, acc[4 * e + 3]);
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   const int64_t at = out_row(p, meta.y, meta.w, row);
   uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + 4 * q4);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     dst[i] = make_uint4(pack16<kF16>(acc[8 * i] * inv, acc[8 * i + 1] * inv), pack16<kF16>(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
                         pack16<kF16>(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv), pack16<kF16>(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
-  if (q4 == 0 && p.lse) p.lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
+  if (q4 == 0 && p.lse) p.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
 }
 
 // ---------------------------------------------------------------------------

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import pass_attention_gb300 as oss
-from paged_reference import attend, check, check_decode, f64, gather
+from paged_reference import attend, check, check_decode, check_packed, f64, gather
+from test_gpu_packed import offsets, rand
 from test_gpu_paged_cache import make
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +47,22 @@ def test_decode(lens, columns, hq, hkv, d, dtype):
     assert torch.equal(w[0, :, lens[0]:], before[0, :, lens[0]:]) and torch.equal(w[2], before[2])
     if hkv > 1:
         assert torch.isfinite(w[0, 1:]).all()
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "f16")])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("lens", [[40, 0, 130], [5, 2500]])  # whole tiles; tiles cut along the keys and joined
+def test_packed(lens, hq, hkv, d, dtype):
+    total = sum(lens)
+    q, k, v = rand(1, total, hq, d, dtype=dtype), rand(2, total, hkv, d, dtype=dtype), rand(3, total, hkv, d, dtype=dtype)
+    rows = [2, total - 1, total - 57]
+    bad = q.clone()
+    bad[rows, 0, 5] = float("nan")
+    for causal in (True, False):
+        o, lse = oss.attention_fwd_packed(bad, k, v, offsets(lens), causal=causal)
+        assert oss.check_device_error() == 0
+        assert torch.isnan(o[rows, 0]).all() and torch.isnan(lse[rows, 0]).all()
+        # every other row has its answer
+        clean, clean_lse = oss.attention_fwd_packed(q, k, v, offsets(lens), causal=causal)
+        o[rows, 0], lse[rows, 0] = clean[rows, 0], clean_lse[rows, 0]
+        check_packed(o, lse, q, k, v, lens, lens, 1 / math.sqrt(d), causal)
