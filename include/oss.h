@@ -521,7 +521,9 @@ typedef struct os_paged_cache {
  *               has none.
  * Two rows that name the same slot (a page shared by two sequences) leave one
  * of the two there; which one is not determined.
- * Positions below 0 or without a page are left out and set the error word.
+ * Positions below 0 or without a page are left out and set the error word; so do
+ * offsets that run backwards or outside 0 .. tokens, whose missing rows would
+ * leave positions that kv_len counts unwritten.
  * Alignment: k and v 16-byte aligned, ld_token and ld_head multiples of 8.
  * Errors: OS_ERR_INVALID_ARGUMENT, OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED,
  * OS_ERR_CUDA. tokens == 0 is OS_OK and launches nothing.

@@ -55,6 +55,10 @@ kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                  uint16_t* k_pages, uint16_t* v_pages, int chunks_per_head, unsigned int* err) {
   let_next_kernel_start();
   wait_for_previous_kernel();
+  // offsets that do not fit the rows: tokens that kv_len counts are not written
+  if (cu)
+    for (int b = blockIdx.x * kAppendThreads + threadIdx.x; b < c.batch; b += gridDim.x * kAppendThreads)
+      if (row_range(cu[b], cu[b + 1], static_cast<int32_t>(tokens)).clamped) bad_index(err, kSiteBadOffsets);
   const int per_token = c.heads * chunks_per_head;
   const int64_t total = tokens * per_token;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x; i < total;
