@@ -687,10 +687,11 @@ def _on(dev: torch.device, stream):
 
 
 # The current device, and the raw current stream of a device, without making a
-# Stream object.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_capturing = torch._C._cuda_isCurrentStreamCapturing
+# Stream object. Where PyTorch lacks these names (a build without CUDA has none of
+# them), its public calls stand in, which fail when they are made, not at import.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 # Workspaces of the calls that launch two kernels, kept per (device, stream) up
 # to this size. The lock is held from taking one to the end of the launches:
