@@ -124,11 +124,54 @@ constexpr uint32_t kColO = 384;
 enum RescalePolicy : int { kRescaleThreshold = 0, kRescaleOnRise = 1, kRescaleAlways = 2 };
 constexpr float kRescaleSlack = 8.0f;
 
+// Bounded wait, slow path: polls until the phase completes, another thread
+// aborts, or the time limit passes (then it raises the abort flag and
+// records the site). Kept out of line; the fast path below is inlined
+// because every wait sits on the pipeline's critical path (measured: an
+// out-of-line call costs the caller a few hundred cycles).
+// A give-up is recorded in the device error word together with the launch's
+// tag (bits 16..31); the other CTAs of the same launch see the tag on their
+// next slow-path poll and give up too, so a failed launch ends after one
+// timeout instead of one per wave of CTAs.
+__device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           unsigned int* err, unsigned int site,
+                                           uint64_t timeout_ns, unsigned int tag) {
+  const uint64_t t0 = global_timer();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if ((n & 63u) == 0) {
+      const unsigned int e = *reinterpret_cast<volatile unsigned int*>(err);
+      if (e != 0 && (e >> 16) == tag) {
+        *abort_flag = 1;
+        return false;
+      }
+      if (global_timer() - t0 > timeout_ns) {
+        *abort_flag = 1;
+        report_error(err, kKernelAttnFwd | (site << 8) | (tag << 16));
+        return false;
+      }
+    }
+  }
+}
+
 // Bounded wait. Returns false on timeout or when another thread has aborted.
 // The limit is the kernel's timeout_ns (kTimeoutNs unless a test shortens it).
 #define wait_bar(bar, parity, abort_flag, err, site) \
   (mbar_test_wait((bar), (parity)) ||                 \
-   wait_bar_slow<kKernelAttnFwd>((bar), (parity), (abort_flag), (err), (site), p.timeout_ns, p.tag))
+   wait_bar_slow((bar), (parity), (abort_flag), (err), (site), p.timeout_ns, p.tag))
+
+// Bounded wait used while draining: ignores the abort flag.
+__device__ __noinline__ bool drain_bar(uint32_t bar, uint32_t parity, unsigned int* err) {
+  const uint64_t t0 = global_timer();
+  for (uint32_t n = 0;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63u) == 0 && global_timer() - t0 > kDrainNs) {
+      report_error(err, kKernelAttnFwd | (kSiteDrain << 8));
+      return false;
+    }
+  }
+}
 
 constexpr uint32_t kIdescQK = make_idesc(kBM, kBN, false);  // S = Q K^T (N = 128 keys)
 constexpr uint32_t kIdescPV = make_idesc(kBM, kD, true);    // O += P V (N = 128 dims)
@@ -467,11 +510,11 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       }
       // drain: every issued copy must land before the CTA may exit
-      if (q_loads > 0) drain_bar<kKernelAttnFwd>(qbar, (q_loads - 1) & 1, p.err);
+      if (q_loads > 0) drain_bar(qbar, (q_loads - 1) & 1, p.err);
       for (int i = k_issued - 1; i >= 0 && i >= k_issued - kStages; --i)
-        drain_bar<kKernelAttnFwd>(smem_addr(&bars.k_full[i % kStages]), (i / kStages) & 1, p.err);
+        drain_bar(smem_addr(&bars.k_full[i % kStages]), (i / kStages) & 1, p.err);
       for (int i = v_issued - 1; i >= 0 && i >= v_issued - kStages; --i)
-        if (i != skipped_v) drain_bar<kKernelAttnFwd>(smem_addr(&bars.v_full[i % kStages]), (i / kStages) & 1, p.err);
+        if (i != skipped_v) drain_bar(smem_addr(&bars.v_full[i % kStages]), (i / kStages) & 1, p.err);
     }
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ QK issuer
@@ -519,7 +562,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       // drain: no MMA of this thread may still write tensor memory when it is freed
       tc_commit(smem_addr(&bars.drain[0]));
-      drain_bar<kKernelAttnFwd>(smem_addr(&bars.drain[0]), 0, p.err);
+      drain_bar(smem_addr(&bars.drain[0]), 0, p.err);
     }
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------ PV issuer
@@ -563,7 +606,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       }
       tc_commit(smem_addr(&bars.drain[1]));
-      drain_bar<kKernelAttnFwd>(smem_addr(&bars.drain[1]), 0, p.err);
+      drain_bar(smem_addr(&bars.drain[1]), 0, p.err);
     }
   } else {
     // ------------------------------------------------------------ softmax

@@ -1,6 +1,6 @@
 // PTX wrappers shared by the attention kernels that run on the tcgen05 tensor
-// cores: mbarriers and their bounded waits, TMA loads, MMAs, tensor-memory
-// access, and the operand descriptors.
+// cores: mbarriers, TMA loads, MMAs, tensor-memory access, and the operand
+// descriptors.
 #pragma once
 
 #include <cuda.h>
@@ -73,51 +73,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
-}
-
-// Bounded wait, slow path: polls until the phase completes, another thread
-// aborts, or the time limit passes (then it raises the abort flag and
-// records the site). Kept out of line; the fast path below is inlined
-// because every wait sits on the pipeline's critical path (measured: an
-// out-of-line call costs the caller a few hundred cycles).
-// A give-up is recorded in the device error word together with the launch's
-// tag (bits 16..31); the other CTAs of the same launch see the tag on their
-// next slow-path poll and give up too, so a failed launch ends after one
-// timeout instead of one per wave of CTAs.
-template <unsigned int kKernel>
-__device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           unsigned int* err, unsigned int site,
-                                           uint64_t timeout_ns, unsigned int tag) {
-  const uint64_t t0 = global_timer();
-  for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if ((n & 63u) == 0) {
-      const unsigned int e = *reinterpret_cast<volatile unsigned int*>(err);
-      if (e != 0 && (e >> 16) == tag) {
-        *abort_flag = 1;
-        return false;
-      }
-      if (global_timer() - t0 > timeout_ns) {
-        *abort_flag = 1;
-        report_error(err, kKernel | (site << 8) | (tag << 16));
-        return false;
-      }
-    }
-  }
-}
-
-// Bounded wait used while draining: ignores the abort flag.
-template <unsigned int kKernel>
-__device__ __noinline__ bool drain_bar(uint32_t bar, uint32_t parity, unsigned int* err) {
-  const uint64_t t0 = global_timer();
-  for (uint32_t n = 0;; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((n & 63u) == 0 && global_timer() - t0 > kDrainNs) {
-      report_error(err, kKernel | (kSiteDrain << 8));
-      return false;
-    }
-  }
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
