@@ -278,8 +278,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictParam
     last |= found_digit << shift;
     ties = found_rank;
     if (ties == 0) {
-      // the whole bin is kept: every key from its first on (a digit is never 0 in
-      // front, -infinity's key being 0x007fffff)
+      // the whole bin is kept: every key from its first on (last is not 0 here: the
+      // least key, -infinity's, is 0x007fffff, so the first digit is 3 or more). Going
+      // on instead: 8 x 8 rows of up to 8192 37.3 against 37.0 us, 2 x 8 of 131072
+      // 68.7 against 68.4.
       --last;
       break;
     }
@@ -438,7 +440,9 @@ int resident_clusters(const EvictParams& p, int dev, int C) {
   return n;
 }
 
-PagedCache device_cache(const os_paged_cache& c) {
+}  // namespace
+
+PagedCache paged_cache(const os_paged_cache& c) {
   int shift = 0;
   while ((1 << shift) < c.page_size) ++shift;
   return PagedCache{static_cast<const uint16_t*>(c.k_pages), static_cast<const uint16_t*>(c.v_pages),
@@ -446,19 +450,17 @@ PagedCache device_cache(const os_paged_cache& c) {
                     c.num_pages, shift, c.max_pages, c.heads, c.batch};
 }
 
-}  // namespace
-
-PagedCache paged_cache(const os_paged_cache& c) { return device_cache(c); }
-
 cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t ld_token, int64_t ld_head,
                              int64_t tokens, const int32_t* cu, const os_paged_cache& cache,
                              unsigned int* err, cudaStream_t stream) {
   const int chunks = cache.head_dim / 8;
   const int64_t total = tokens * cache.heads * chunks;
   int64_t blocks = (total + kAppendThreads - 1) / kAppendThreads;
-  if (blocks > 152 * 64) blocks = 152 * 64;
+  const int sms = device_sms();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  if (blocks > sms * 64) blocks = sms * 64;
   return launch_after(kv_append_kernel, dim3(static_cast<unsigned>(blocks)), kAppendThreads, 0, stream, k, v, ld_token,
-                      ld_head, tokens, cu, device_cache(cache), static_cast<uint16_t*>(cache.k_pages),
+                      ld_head, tokens, cu, paged_cache(cache), static_cast<uint16_t*>(cache.k_pages),
                       static_cast<uint16_t*>(cache.v_pages), chunks, err);
 }
 
@@ -467,7 +469,7 @@ cudaError_t launch_kv_evict(const os_paged_cache& cache, const float* weights, i
                             int32_t new_max_pages, int32_t budget, int32_t recent, int32_t* kept,
                             int32_t* new_len, float* new_weights, unsigned int* err,
                             cudaStream_t stream) {
-  const EvictParams p{device_cache(cache), weights, ld_w_batch, ld_w_head, new_table, ld_new_table,
+  const EvictParams p{paged_cache(cache), weights, ld_w_batch, ld_w_head, new_table, ld_new_table,
                       new_max_pages, budget, recent, kept, new_len, new_weights};
   // CTAs of a row: as many (up to eight) as fit on the GPU for all rows at once while a
   // slice keeps at least kLeastSlice keys, and as many as it takes for a slice
