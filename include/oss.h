@@ -480,13 +480,14 @@ OSS_API os_status os_merge_partials(const float* part_m, const float* part_l, co
  *                     page * ld_page + head * ld_head + slot * ld_slot + d, the
  *                     same strides (in elements) for both. Any order of the
  *                     three is allowed ([page, head, slot, d] or [page, slot,
- *                     head, d], or K and V pages side by side).
+ *                     head, d], or K and V pages side by side). A stride is
+ *                     positive where its dimension is longer than 1.
  *   page_table        [batch, max_pages] int32, DEVICE, row stride ld_table;
  *                     only the entries of a sequence's ceil(len / page_size)
  *                     first pages are read.
- *   kv_len            [batch] int32, DEVICE; a value outside 0 .. max_pages *
- *                     page_size is clamped to it on the device.
- *                     Positive where the dimension is longer than 1.
+ *   kv_len            [batch] int32, DEVICE; the decode and the eviction
+ *                     clamp a value outside 0 .. max_pages * page_size to it
+ *                     on the device, appending has no position for it.
  *   page_size a power of two, 16 .. 1024 (others: OS_ERR_UNSUPPORTED).
  *   head_dim 64 or 128 (others: OS_ERR_UNSUPPORTED).  dtype an os_dtype.
  *   batch <= 65535, max_pages * page_size <= 2^30.
@@ -560,7 +561,9 @@ OSS_API os_status os_kv_cache_append(const void* k, const void* v, int64_t ld_to
  *         os_attention_decode_paged_workspace_bytes bytes, 16-byte aligned;
  *         it needs no initialising and keeps nothing between calls. Calls
  *         that may run at the same time need workspaces of their own.
- *   H a multiple of cache->heads.  scale finite and > 0.
+ *   H a multiple of cache->heads: up to 16 query heads of a key head share one
+ *   read of the cache; a larger group reads it once for every 16.
+ *   scale finite and > 0.
  * Alignment: q and o 16-byte aligned, q's strides multiples of 8.
  * Errors: OS_ERR_INVALID_ARGUMENT (also a workspace that is too small),
  * OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED, OS_ERR_CUDA.
@@ -574,7 +577,10 @@ OSS_API os_status os_attention_decode_paged(const void* q, int64_t ld_q_batch, i
 /* Bytes of workspace that os_attention_decode_paged uses for H query heads
  * over this cache on the current device, with or without weights; -1 when the
  * device cannot be queried, 0 for arguments that the call refuses. Reads only
- * heads, head_dim, batch, max_pages and page_size of the cache. */
+ * heads, head_dim, batch, max_pages and page_size of the cache. With weights it
+ * holds a score (4 bytes) for every query head, groups rounded up to a multiple
+ * of 4 (above 16: of 16), and every position of the page table, whatever the
+ * lengths are: 1 GiB for 64 sequences, 32 heads over 8 and 131072 positions. */
 OSS_API int64_t os_attention_decode_paged_workspace_bytes(int32_t H, const os_paged_cache* cache,
                                                           int weights);
 
@@ -673,9 +679,10 @@ OSS_API os_status os_kv_cache_evict(const os_paged_cache* cache, const float* we
  * wait for its row's bulk copies into shared memory gave up, 2 | (2 << 8) one
  * whose wait for the (max, sum) states of the other CTAs of its cluster gave
  * up; kernel 4 is os_attention_fwd_packed (sites as kernel 1). Kernel 3 is
- * not a wait: a call on a paged cache met an index outside the cache and left
- * that row out (site 1: a page number; site 2: a position without a page;
- * site 3: sequence offsets that run backwards or past the tokens). Returns
+ * not a wait: a call on a paged cache or on packed sequences met an index
+ * outside them and left that row out (site 1: a page number; site 2: a position
+ * without a page; site 3: sequence offsets that run backwards or past the
+ * tokens). Returns
  * OS_ERR_TIMEOUT when the word was set by a wait, OS_ERR_BAD_INDEX when it was
  * set by kernel 3, OS_ERR_CUDA when a CUDA call failed, OS_OK otherwise.
  * `code` may be NULL.

@@ -931,7 +931,9 @@ def debug_inject_fault(kind: int, step: int = 0, timeout_ns: int = 0) -> None:
 
 def check_device_error(stream=None) -> int:
     """Synchronise ``stream`` and read/clear the device error word; raises
-    OssError(OS_ERR_TIMEOUT) when a kernel gave up on a bounded wait."""
+    OssError(OS_ERR_TIMEOUT) when a kernel gave up on a bounded wait, and
+    OssError(OS_ERR_BAD_INDEX) when a call on a paged cache or packed sequences
+    met an index outside them."""
     code = _i32(0)
     dev = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
     with torch.cuda.device(dev):

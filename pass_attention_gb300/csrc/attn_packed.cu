@@ -16,11 +16,14 @@
 // Registers move to where they are needed: 184 a thread for the softmax, 80 for the
 // epilogue, 64 for the others (512 threads x 128 at launch).
 //
-// What it reaches: one causal sequence of 16384 in 1.54-1.59 ms (1400 TFLOP/s, 0.73
+// What it reaches: one causal sequence of 16384 in 1.52-1.59 ms (1400 TFLOP/s, 0.73
 // of the measured bf16 rate, 0.81 of the sustained one). A KV step takes about 1650
-// cycles where its MMAs need 1024 and its exponentials 1024 of the special-function
-// units; the chain scores - maximum - exponentials - P V sets it, as in the dense kernel. With 64
-// dims the MMAs halve and the step stays: the exponentials bound it.
+// cycles where its MMAs need 1024 and its exponentials 514 (31.9 a clock and SM):
+// neither bounds it, but the chain scores - maximum - weights - P V of the one
+// query tile in flight. With 64 dims the MMAs need 512 cycles, and the step stays. In turns
+// with the dense kernel on that sequence with 32 key heads: 1.58 against 1.48 ms (1.56
+// with 8 key heads). How much of the difference is the K ring, two stages here for the
+// second Q buffer and three there, and how much the waits, has not been separated.
 //
 // Rows. A tile's 128 rows are 128 / P' consecutive queries times P' query heads of
 // one key head, P' the largest power of two that divides G = Hq / Hkv (up to
@@ -480,6 +483,8 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  // (Before the wait: a CTA of this kernel takes the SM's whole register file, so none of
+  // the kernel before it that holds tensor memory can share the SM with it.)
   if (warp == kQkWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&tmem_base_slot)),
@@ -726,6 +731,9 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           if (at < u.n_pos) base[static_cast<int64_t>(at * p.Hq + head) * kChunks + c] = x;
         }
         __syncwarp();
+        // (__log2f: off by at most 2^-22 for l in 0.5 .. 2, by 2 units in the last place
+        // elsewhere. With log2f, which the join uses, 8 sequences of up to 2500 take 161.9
+        // against 161.2 us.)
         if (p.lse && ((row0 + lane) >> head_shift) < u.n_pos)
           p.lse[out_row(p, u.q_row, u.pack, row0 + lane)] = ml.y != 0.f ? (ml.x + __log2f(ml.y)) * kLn2 : neg_inf();
       } else {

@@ -8,7 +8,8 @@
 // share one read, and from G = 4 on the FMA pipes could not keep up with HBM.
 // The products therefore run on mma.sync (m16n8k16), with the keys on the wide side
 // and the heads on the narrow one, so that a group of 8 heads or fewer
-// fills the instruction:
+// fills the instruction (up to 16 heads share a read, in two instructions; a group of
+// more is cut into blocks of 16 that each read the cache):
 //   S^T [16 keys x 8 heads]  = K [16 x D] Q^T [D x 8]
 //   O^T [16 dims x 8 heads] += V^T [16 x 16 keys] P^T [16 x 8]
 // K and V tiles come out of shared memory by ldmatrix (transposed for V), and
@@ -29,10 +30,11 @@
 // one, beside the joins, adds 2^(s - lse) to the sums: 4 bytes a head against
 // the 2 D of reading the key again.
 //
-// What it reaches: 64 sequences of up to 8192 tokens, 32 heads over 8, 191 us (6.4
-// TB/s, 0.96 of the copy peak); 6 of up to 32768, 16 heads of 64 in fp16, 104 us
-// (0.93). A step over 1.2 MB of cache takes 8 us: the chain from the lengths over the page
-// table to the keys, and the join.
+// What it reaches: 64 sequences of up to 8192 tokens, 32 heads over 8, 193 us (6.4
+// TB/s, 0.95 of the copy peak); 6 of up to 32768, 16 heads of 64 in fp16, 104 us
+// (0.93). (A stream that is only read may exceed the copy's rate: the dense split decode
+// reads 7.35 TB/s.) A step over 1.2 MB of cache takes 8 us: the chain from the lengths over the
+// page table to the keys, on 8 SMs of 152.
 //
 // Each of a CTA's four warps streams tiles of 16 keys (every fourth one of its
 // segment) through its own ring in shared memory, by 16-byte asynchronous
@@ -61,7 +63,10 @@ constexpr int kMaxHeadBlock = 16;
 // most kWholeKeys tokens, or at most kWholeKeysMany and there are as many items
 // as shares. Replayed from a graph, 32 heads over 8, whole against cut: 1 x 128 tokens
 // 4.9 against 7.4 us, 1 x 333 7.8 / 7.6 (but 3 us of the host for the second launch),
-// 64 x 256 12 / 18, 64 x 512 26 / 33; and 1 x 512 9.2 / 7.5.
+// 64 x 256 12 / 18, 64 x 512 26 / 33; and 1 x 512 9.2 / 7.5. On the GPU the two meet
+// before 333; up to 384 it is the host's second launch that decides. The rule goes by
+// the table's width, because the lengths are on the device: short sequences in a wide
+// table are cut.
 constexpr int kWholeKeys = 384;
 constexpr int kWholeKeysMany = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
