@@ -657,8 +657,9 @@ OSS_API int64_t os_attention_fwd_packed_workspace_bytes(int64_t tokens_k, int32_
  *   new_len    [batch] int32: n.
  *   new_weights  fp32 [batch, heads, new_max_pages * page_size] dense: the kept
  *              tokens' weights, 0 behind them.
- *   new_table is not the cache's page_table, new_len does not overlap its
- *   kv_len, nor new_weights weights (OS_ERR_INVALID_ARGUMENT).
+ *   new_table is not the cache's page_table; kept, new_len and new_weights
+ *   overlap neither each other nor weights, kv_len or a page table
+ *   (OS_ERR_INVALID_ARGUMENT).
  *   1 <= budget <= new_max_pages * page_size; 0 <= recent <= budget.
  * Alignment: as the cache.
  * Errors: OS_ERR_INVALID_ARGUMENT, OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED,

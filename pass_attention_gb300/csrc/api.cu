@@ -487,13 +487,23 @@ os_status os_kv_cache_evict(const os_paged_cache* cache, const float* weights, i
        reinterpret_cast<uintptr_t>(new_weights)) & 3u)
     return OS_ERR_MISALIGNED;
   if (room > (int64_t(1) << 30)) return OS_ERR_UNSUPPORTED;
-  // what is read by one CTA while another writes
+  // an output must not lie in what other CTAs still read, nor in another output
   const int64_t rows = static_cast<int64_t>(cache->batch) * cache->heads;
-  const int64_t span = (cache->batch - 1) * ld_w_batch + (cache->heads - 1) * ld_w_head +
-                       static_cast<int64_t>(cache->max_pages) * cache->page_size;
-  if (new_table == cache->page_table || overlap(new_len, cache->batch, cache->kv_len, cache->batch) ||
-      overlap(new_weights, rows * room, weights, span))
-    return OS_ERR_INVALID_ARGUMENT;
+  const struct {
+    const void* at;
+    int64_t n;
+  } spans[] = {{kept, rows * budget},
+               {new_len, cache->batch},
+               {new_weights, rows * room},
+               {weights, (cache->batch - 1) * ld_w_batch + (cache->heads - 1) * ld_w_head +
+                             static_cast<int64_t>(cache->max_pages) * cache->page_size},
+               {cache->kv_len, cache->batch},
+               {cache->page_table, (cache->batch - 1) * cache->ld_table + cache->max_pages},
+               {new_table, (cache->batch - 1) * ld_new_table + new_max_pages}};
+  if (new_table == cache->page_table) return OS_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 7; ++j)
+      if (overlap(spans[i].at, spans[i].n, spans[j].at, spans[j].n)) return OS_ERR_INVALID_ARGUMENT;
   unsigned int* err = error_word();
   if (!err) return OS_ERR_CUDA;
   return from_cuda(oss::launch_kv_evict(*cache, weights, ld_w_batch, ld_w_head, new_table, ld_new_table,
