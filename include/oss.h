@@ -672,6 +672,130 @@ OSS_API os_status os_kv_cache_evict(const os_paged_cache* cache, const float* we
                                     float* new_weights, void* stream);
 
 /*
+ * os_attention_decode_shared -- attention of one query token per sequence,
+ * where groups of sequences share a prefix (a system prompt, a document that
+ * many questions are about). The keys of a sequence of group g are the
+ * prefix_len[g] tokens of the group's prefix and then the sequence's own
+ * kv_len tokens, all of them in pages of the same pools:
+ *     s_t = scale * q . k_t;  lse = ln sum_t exp(s_t);  o = sum_t exp(s_t - lse) v_t
+ * The prefix is read once for the whole group, on the tensor cores, and not
+ * once a sequence; the two parts' states (m, l, O) are joined in fp32 with the
+ * merge identity, in a fixed order, so every run gives the same bits. A sequence
+ * that no group names has its own tokens only; one without any key gives o = 0,
+ * lse = -inf. Rounding and NaN as in os_attention_decode_paged; k and v of a prefix
+ * are finite.
+ *
+ *   cache       the pools, and the sequences' own tokens (their new ones among
+ *               them: append first).
+ *   prefix_table  [groups, prefix_max_pages] int32, DEVICE, row stride
+ *               ld_prefix_table: the prefixes' pages in the same pools.
+ *   prefix_len  [groups] int32, DEVICE; clamped to 0 .. prefix_max_pages *
+ *               page_size on the device.
+ *   cu_groups   [groups + 1] int32, DEVICE, ascending, within 0 .. batch: group
+ *               g is sequences cu_groups[g] .. cu_groups[g + 1] - 1. Offsets that
+ *               are not are clamped on the device and set the error word
+ *               (OS_ERR_BAD_INDEX); results are then undefined. NULL: one group
+ *               of all sequences (groups == 1).
+ *   q, o, lse, scale, H  as in os_attention_decode_paged; q's strides are
+ *               positive where the dimension is longer than 1.
+ *   workspace   at least os_attention_decode_shared_workspace_bytes bytes,
+ *               16-byte aligned; no initialising, nothing kept between calls, one
+ *               for each call that may run at the same time.
+ *   groups <= 65535, prefix_max_pages * page_size <= 2^30.
+ * Alignment: as os_attention_decode_paged.
+ * Errors: OS_ERR_INVALID_ARGUMENT (also a workspace that is too small),
+ * OS_ERR_MISALIGNED, OS_ERR_UNSUPPORTED, OS_ERR_CUDA; a timed-out internal wait is
+ * reported by os_check_device_error.
+ */
+OSS_API os_status os_attention_decode_shared(const void* q, int64_t ld_q_batch, int64_t ld_q_head, int32_t H,
+                                             const os_paged_cache* cache, const int32_t* prefix_table,
+                                             int64_t ld_prefix_table, const int32_t* prefix_len,
+                                             int32_t prefix_max_pages, const int32_t* cu_groups, int32_t groups,
+                                             float scale, void* o, float* lse, void* workspace,
+                                             int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that os_attention_decode_shared uses for H query heads over
+ * this cache, `groups` prefixes of up to prefix_max_pages pages, on the current
+ * device; -1 when the device cannot be queried, 0 for arguments that the call
+ * refuses. Reads only heads, head_dim, batch, max_pages and page_size of the cache. */
+OSS_API int64_t os_attention_decode_shared_workspace_bytes(int32_t H, const os_paged_cache* cache,
+                                                           int32_t prefix_max_pages, int32_t groups);
+
+/*
+ * A paged key-value cache in 8 bits: half the memory, and half the bytes that a
+ * decode step reads. A row (a token's key or value in one key head) is D e4m3
+ * values and one scale 2^e; element d of it stands for code_d * 2^e.
+ *
+ *   pages     tables, lengths and pools as in os_paged_cache, with these
+ *             differences: an element of k_pages and v_pages is one e4m3 byte
+ *             (1 sign, 4 exponent and 3 fraction bits, bias 7, 0x7f and 0xff
+ *             NaN); strides are in elements, multiples of 16; dtype is the type
+ *             of the calls' 16-bit tensors, and may differ from call to call.
+ *   k_scales, v_scales  one byte a row, e + 127 (e8m0; 255: NaN): element (page,
+ *             head, slot) at page * ld_scale_page + head * ld_scale_head + slot, the
+ *             same strides for both.
+ * Alignment: pools and scales 16-byte aligned, all strides multiples of 16.
+ */
+typedef struct os_paged_cache_fp8 {
+  os_paged_cache pages;
+  void* k_scales;
+  void* v_scales;
+  int64_t ld_scale_page, ld_scale_head;
+} os_paged_cache_fp8;
+
+/*
+ * os_kv_cache_append_fp8 -- os_kv_cache_append into a cache in 8 bits: the keys
+ * and values of new tokens are quantised as they are written. For a row x:
+ *     e      = the smallest integer >= -127 with max_d |x_d| <= 448 * 2^e
+ *     code_d = x_d * 2^-e rounded to e4m3 (to nearest even)
+ * A row that holds NaN or infinity reads as NaN in every element (codes 0x7f, scale
+ * 255). k, v, tokens, cu_seqlens, positions and errors as in
+ * os_kv_cache_append; what a slot that two rows name then holds is not determined.
+ */
+OSS_API os_status os_kv_cache_append_fp8(const void* k, const void* v, int64_t ld_token, int64_t ld_head,
+                                         int64_t tokens, const int32_t* cu_seqlens,
+                                         const os_paged_cache_fp8* cache, void* stream);
+
+/*
+ * os_kv_cache_read_fp8 -- cached tokens back into packed rows of the cache's dtype,
+ * as os_attention_fwd_packed takes them when a prompt goes on behind what is
+ * cached. The mirror of appending: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 get
+ * the last positions of sequence b (all kv_len[b] of them where there are as many
+ * rows). Values are code * 2^e, rounded to nearest even where the type does not hold
+ * them (beyond fp16's range: infinity).
+ *
+ *   cu_seqlens  [batch + 1] int32, DEVICE, ascending.
+ *   k, v   [tokens, heads, D], device: element (token, head, d) at token * ld_token +
+ *          head * ld_head + d, the same strides for both, positive where the dimension is
+ *          longer than 1. Rows outside every sequence, and rows whose position is
+ *          below 0 or whose page is outside the pool (which set the error word, as in
+ *          appending), are left as they were.
+ * Alignment: k and v 16-byte aligned, ld_token and ld_head multiples of 8.
+ * Errors: as os_kv_cache_append_fp8. tokens == 0 is OS_OK and launches nothing.
+ */
+OSS_API os_status os_kv_cache_read_fp8(const os_paged_cache_fp8* cache, const int32_t* cu_seqlens, int64_t tokens,
+                                       void* k, void* v, int64_t ld_token, int64_t ld_head, void* stream);
+
+/*
+ * os_attention_decode_paged_fp8 -- os_attention_decode_paged (without the sums of
+ * weights) over a cache in 8 bits: k_t and v_t are the values that the cached rows
+ * stand for. The products run in fp16 with fp32 sums, with the rows' scales as
+ * exponents beside them: codes are exact in fp16, q is (a bf16 q by its head's
+ * power of two, elements below 2^-39 of the head's largest aside), and
+ * the weights are rounded to fp16. A key row that is NaN gives NaN in o and lse,
+ * a value row that is NaN in o.
+ * q, o, lse, scale, H, workspace, alignment and errors as in
+ * os_attention_decode_paged.
+ */
+OSS_API os_status os_attention_decode_paged_fp8(const void* q, int64_t ld_q_batch, int64_t ld_q_head, int32_t H,
+                                                const os_paged_cache_fp8* cache, float scale, void* o, float* lse,
+                                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that os_attention_decode_paged_fp8 uses, as
+ * os_attention_decode_paged_workspace_bytes. */
+OSS_API int64_t os_attention_decode_paged_fp8_workspace_bytes(int32_t H, const os_paged_cache_fp8* cache);
+
+/*
  * os_check_device_error -- synchronise `stream`, then read and clear the
  * current device's error word. *code receives 0 when no kernel gave up on a
  * wait since the last check, otherwise an OS_ERR_TIMEOUT detail code

@@ -41,6 +41,10 @@ __all__ = [
     "kv_cache_append",
     "attention_decode_paged",
     "kv_cache_evict",
+    "attention_decode_shared",
+    "kv_cache_append_fp8",
+    "kv_cache_read_fp8",
+    "attention_decode_paged_fp8",
     "check_device_error",
     "debug_inject_fault",
     "set_rescale_policy",
@@ -75,6 +79,8 @@ _f32 = ctypes.c_float
 # dtype, batch, max_pages (its bytes take the place of a pointer to it; a
 # ctypes.Structure costs a microsecond more per call)
 _PAGED_CACHE = struct.Struct("@PPqqqPqPiiiiiii")
+# os_paged_cache_fp8: the same, then k_scales, v_scales, ld_scale_page, ld_scale_head
+_PAGED_CACHE_FP8 = struct.Struct("@PPqqqPqPiiiiiiiPPqq")
 
 # name -> (restype, argtypes), the signatures of include/oss.h
 _SIGNATURES = {
@@ -111,6 +117,13 @@ _SIGNATURES = {
     "os_attention_decode_paged_workspace_bytes": (_i64, [_i32, _vp, ctypes.c_int]),
     "os_kv_cache_evict": (_i32, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
                                  _vp, _vp]),
+    "os_attention_decode_shared": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i32, _vp, _i32,
+                                          _f32, _vp, _vp, _vp, _i64, _vp]),
+    "os_attention_decode_shared_workspace_bytes": (_i64, [_i32, _vp, _i32, _i32]),
+    "os_kv_cache_append_fp8": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "os_kv_cache_read_fp8": (_i32, [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "os_attention_decode_paged_fp8": (_i32, [_vp, _i64, _i64, _i32, _vp, _f32, _vp, _vp, _vp, _i64, _vp]),
+    "os_attention_decode_paged_fp8_workspace_bytes": (_i64, [_i32, _vp]),
     "os_check_device_error": (_i32, [_vp, ctypes.POINTER(_i32)]),
     "os_attention_set_rescale_policy": (_i32, [_i32]),
     "os_attention_rescale_policy": (_i32, []),
@@ -903,6 +916,230 @@ def kv_cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.
                                   new_len.data_ptr(), new_weights.data_ptr(), _raw_stream(dev.index))
     _check(st, "os_kv_cache_evict")
     return kept, new_len, new_weights
+
+
+def attention_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                            prefix_table: torch.Tensor, prefix_len: torch.Tensor, page_table: torch.Tensor,
+                            kv_len: torch.Tensor, cu_groups: Optional[torch.Tensor] = None,
+                            scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None, stream=None):
+    """``attention_decode_paged`` for sequences that share prefixes: the keys of a
+    sequence of group g are the prefix_len[g] tokens in the pages of row g of
+    prefix_table [groups, max_prefix_pages], then its own (page_table, kv_len) in
+    the same pools. A prefix is read once for its whole group. cu_groups [groups + 1]:
+    group g is sequences cu_groups[g] .. cu_groups[g + 1] - 1 (None: one group of all).
+    All of them int32 on the device. Returns ``(o, lse)``, [batch, Hq, D] and fp32
+    [batch, Hq]. See ``os_attention_decode_shared``."""
+    cache, dev, batch, heads, d, _, _ = _cache(k_pages, v_pages, page_table, kv_len)
+    dtype = k_pages.dtype
+    sq = _strides(q, "q", 3, dtype, dev)
+    bq, hq, dq = q.shape
+    if bq != batch or dq != d:
+        raise ValueError(f"q must be [{batch}, Hq, {d}] like the cache")
+    if heads < 1 or hq < 1 or hq % heads:
+        raise ValueError(f"{hq} query heads cannot share {heads} key heads")
+    _ints(prefix_table, "prefix_table", 2, dev)
+    _ints(prefix_len, "prefix_len", 1, dev)
+    groups, prefix_pages = prefix_table.shape
+    if prefix_len.shape[0] != groups:
+        raise ValueError("prefix_len must have one entry for each row of prefix_table")
+    cu = None
+    if cu_groups is not None:
+        _ints(cu_groups, "cu_groups", 1, dev)
+        if cu_groups.shape[0] != groups + 1:
+            raise ValueError("cu_groups must have one entry more than prefix_table has rows")
+        cu = cu_groups.data_ptr()
+    elif groups != 1:
+        raise ValueError("several groups need cu_groups")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if o is not None:
+        _out(o, "o", dtype, (batch, hq, d), dev)
+    if lse is not None:
+        _out(lse, "lse", torch.float32, (batch, hq), dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attention_decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, kv_len, cu_groups,
+                                           scale, o, lse)
+    if o is None:
+        o = torch.empty((batch, hq, d), dtype=dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
+    lib = load()
+    need = lib.os_attention_decode_shared_workspace_bytes(hq, cache, prefix_pages, groups)
+    if need < 0:
+        raise OssError(4, "os_attention_decode_shared_workspace_bytes")
+    sp = _raw_stream(dev.index)
+    with _LAUNCH_LOCK:
+        ws = _scratch(dev, sp, need)
+        st = lib.os_attention_decode_shared(q.data_ptr(), sq[0], sq[1], hq, cache, prefix_table.data_ptr(),
+                                            prefix_table.stride(0), prefix_len.data_ptr(), prefix_pages, cu, groups,
+                                            scale, o.data_ptr(), lse.data_ptr(), ws.data_ptr(), need, sp)
+    _check(st, "os_attention_decode_shared")
+    return o, lse
+
+
+# -- the cache in 8 bits ---------------------------------------------------------------------
+
+def _scale_strides(t: torch.Tensor, name: str, shape, device: torch.device):
+    """Strides of the scales [pages, heads, page_size] of a pool."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float8_e8m0fnu or t.dim() != 3 or t.device != device \
+            or t.stride(2) != 1:
+        _refuse(t, name, 3, torch.float8_e8m0fnu, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, a scale for each row of the pages")
+    st = t.stride()
+    if (st[0] | st[1]) & 15:
+        # a stride off the 16-byte grid matters only where it is walked
+        return tuple(0 if n == 1 else x for n, x in zip(shape, st))
+    return st
+
+
+def _cache_fp8(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype):
+    """``(os_paged_cache_fp8, device, batch, heads, head_dim)`` of these tensors, for
+    calls whose 16-bit tensors are of ``dtype``."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype is not torch.float8_e4m3fn:
+        raise TypeError("k_pages must be a float8_e4m3fn torch.Tensor")
+    if not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor (liboss has no CPU path)")
+    if dtype not in _DTYPE_CODES:
+        raise TypeError(f"{dtype} is neither bfloat16 nor float16")
+    dev = k_pages.device
+    st = _pair(k_pages, v_pages, ("k_pages", "v_pages"), 4, torch.float8_e4m3fn, dev)
+    shape = k_pages.shape
+    if (st[0] | st[1] | st[2]) & 15:
+        st = tuple(0 if n == 1 and x & 15 else x for n, x in zip(shape, st))
+    ss = _scale_strides(k_scales, "k_scales", shape[:3], dev)
+    sv = _scale_strides(v_scales, "v_scales", shape[:3], dev)
+    if sv != ss and any(n > 1 and a != b for n, a, b in zip(shape, ss, sv)):
+        raise ValueError("k_scales and v_scales must have the same strides")
+    _ints(page_table, "page_table", 2, dev)
+    _ints(kv_len, "kv_len", 1, dev)
+    pages, heads, page_size, d = shape
+    batch, max_pages = page_table.shape
+    if kv_len.shape[0] != batch:
+        raise ValueError("kv_len must have one entry for each row of page_table")
+    try:
+        packed = _PAGED_CACHE_FP8.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
+                                       page_table.data_ptr(), page_table.stride(0), kv_len.data_ptr(), pages, heads,
+                                       page_size, d, _DTYPE_CODES[dtype], batch, max_pages, k_scales.data_ptr(),
+                                       v_scales.data_ptr(), ss[0], ss[1])
+    except struct.error:
+        raise ValueError("more pages than 32 bits count") from None
+    return packed, dev, batch, heads, d
+
+
+def _seqlens(cu_seqlens: torch.Tensor, batch: int, dev: torch.device) -> int:
+    _ints(cu_seqlens, "cu_seqlens", 1, dev)
+    if cu_seqlens.shape[0] != batch + 1:
+        raise ValueError("cu_seqlens must have batch + 1 entries")
+    return cu_seqlens.data_ptr()
+
+
+def kv_cache_append_fp8(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                        k_scales: torch.Tensor, v_scales: torch.Tensor, page_table: torch.Tensor,
+                        kv_len: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``kv_cache_append`` into a cache in 8 bits: k and v [tokens, Hkv, D] (bf16 or
+    fp16) are quantised as they are written. k_pages and v_pages [pages, Hkv,
+    page_size, D] float8_e4m3fn (any strides, multiples of 16, the same for both),
+    k_scales and v_scales [pages, Hkv, page_size] float8_e8m0fnu: a row's values are
+    its codes times its scale, the smallest power of two with which they fit. See
+    ``os_kv_cache_append_fp8``."""
+    dev = _cuda_device(k, "k")
+    dtype = k.dtype
+    cache, pool_dev, batch, heads, d = _cache_fp8(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype)
+    if pool_dev != dev:
+        raise ValueError(f"k is on {dev}, the cache on {pool_dev}")
+    sk = _pair(k, v, ("k", "v"), 3, dtype, dev)
+    tokens, hk, dk = k.shape
+    if hk != heads or dk != d:
+        raise ValueError(f"k and v must be [tokens, {heads}, {d}] like the cache")
+    cu = None if cu_seqlens is None else _seqlens(cu_seqlens, batch, dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv_cache_append_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, kv_len, cu_seqlens)
+    st = load().os_kv_cache_append_fp8(k.data_ptr(), v.data_ptr(), sk[0], sk[1], tokens, cu, cache,
+                                       _raw_stream(dev.index))
+    _check(st, "os_kv_cache_append_fp8")
+
+
+def kv_cache_read_fp8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                      page_table: torch.Tensor, kv_len: torch.Tensor, cu_seqlens: torch.Tensor, tokens: int,
+                      dtype: torch.dtype = torch.bfloat16, k: Optional[torch.Tensor] = None,
+                      v: Optional[torch.Tensor] = None, stream=None):
+    """Cached tokens of a cache in 8 bits (see ``kv_cache_append_fp8``) as packed rows
+    of ``dtype`` (bf16 or fp16), the k and v that ``attention_fwd_packed`` takes: rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of ``tokens`` get the last positions of
+    sequence b, all of them where there are kv_len[b] rows. Returns ``(k, v)`` [tokens,
+    Hkv, D]; given ones may be views with the same strides. Rows outside every sequence
+    are left as they were. See ``os_kv_cache_read_fp8``."""
+    cache, dev, batch, heads, d = _cache_fp8(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype)
+    cu = _seqlens(cu_seqlens, batch, dev)
+    tokens = int(tokens)
+    if tokens < 0:
+        raise ValueError("tokens must be >= 0")
+    if (k is None) != (v is None):
+        raise ValueError("k and v are given together or not at all")
+    if k is not None:
+        sk = _pair(k, v, ("k", "v"), 3, dtype, dev)
+        if tuple(k.shape) != (tokens, heads, d):
+            raise ValueError(f"k and v must be [{tokens}, {heads}, {d}]")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv_cache_read_fp8(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, cu_seqlens, tokens, dtype,
+                                     k, v)
+    if k is None:
+        k = torch.empty((tokens, heads, d), dtype=dtype, device=dev)
+        v = torch.empty_like(k)
+        sk = k.stride()
+    st = load().os_kv_cache_read_fp8(cache, cu, tokens, k.data_ptr(), v.data_ptr(), sk[0], sk[1], _raw_stream(dev.index))
+    _check(st, "os_kv_cache_read_fp8")
+    return k, v
+
+
+def attention_decode_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
+                               v_scales: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                               scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                               lse: Optional[torch.Tensor] = None, stream=None):
+    """``attention_decode_paged`` (without weights) over a cache in 8 bits (see
+    ``kv_cache_append_fp8``): q [batch, Hq, D] bf16 or fp16. Returns ``(o, lse)``,
+    [batch, Hq, D] of q's type and fp32 [batch, Hq]. See
+    ``os_attention_decode_paged_fp8``."""
+    dev = _cuda_device(q, "q")
+    dtype = q.dtype
+    cache, pool_dev, batch, heads, d = _cache_fp8(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype)
+    if pool_dev != dev:
+        raise ValueError(f"q is on {dev}, the cache on {pool_dev}")
+    sq = _strides(q, "q", 3, dtype, dev)
+    bq, hq, dq = q.shape
+    if bq != batch or dq != d:
+        raise ValueError(f"q must be [{batch}, Hq, {d}] like the cache")
+    if heads < 1 or hq < 1 or hq % heads:
+        raise ValueError(f"{hq} query heads cannot share {heads} key heads")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if o is not None:
+        _out(o, "o", dtype, (batch, hq, d), dev)
+    if lse is not None:
+        _out(lse, "lse", torch.float32, (batch, hq), dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attention_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, page_table, kv_len, scale, o, lse)
+    if o is None:
+        o = torch.empty((batch, hq, d), dtype=dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
+    lib = load()
+    need = lib.os_attention_decode_paged_fp8_workspace_bytes(hq, cache)
+    if need < 0:
+        raise OssError(4, "os_attention_decode_paged_fp8_workspace_bytes")
+    sp = _raw_stream(dev.index)
+    with _LAUNCH_LOCK:
+        ws = _scratch(dev, sp, need)
+        st = lib.os_attention_decode_paged_fp8(q.data_ptr(), sq[0], sq[1], hq, cache, scale, o.data_ptr(),
+                                               lse.data_ptr(), ws.data_ptr(), need, sp)
+    _check(st, "os_attention_decode_paged_fp8")
+    return o, lse
 
 
 RESCALE_POLICIES = {"threshold": 0, "on_rise": 1, "always": 2}

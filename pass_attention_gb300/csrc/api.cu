@@ -85,6 +85,36 @@ os_status check_cache(const os_paged_cache* c) {
   return OS_OK;
 }
 
+// The same for a cache in 8 bits.
+os_status check_cache_fp8(const os_paged_cache_fp8* c) {
+  if (!c || !c->k_scales || !c->v_scales) return OS_ERR_INVALID_ARGUMENT;
+  const os_status st = check_cache(&c->pages);
+  if (st != OS_OK) return st;
+  if (c->ld_scale_page < (c->pages.num_pages > 1) || c->ld_scale_head < (c->pages.heads > 1)) return OS_ERR_INVALID_ARGUMENT;
+  if (!aligned16(c->k_scales) || !aligned16(c->v_scales) ||
+      ((c->pages.ld_page | c->pages.ld_head | c->pages.ld_slot | c->ld_scale_page | c->ld_scale_head) & 15))
+    return OS_ERR_MISALIGNED;
+  return OS_OK;
+}
+
+// What the appending calls ask of the new rows, and the reading one of where they go.
+os_status check_rows(const void* k, const void* v, int64_t ld_token, int64_t ld_head, int64_t tokens, const int32_t* cu) {
+  if (!k || !v) return OS_ERR_INVALID_ARGUMENT;
+  if (tokens > 0x7fffffff) return OS_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || ((ld_token | ld_head) & 7)) return OS_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(cu) & 3u) return OS_ERR_MISALIGNED;
+  return OS_OK;
+}
+
+// Whether a workspace size may be asked for H query heads over this cache.
+bool sized_cache(int32_t H, const os_paged_cache& c) {
+  if (c.heads <= 0 || H <= 0 || H % c.heads) return false;
+  if (c.batch <= 0 || c.batch > 65535 || c.max_pages <= 0 || c.page_size <= 0 ||
+      static_cast<int64_t>(c.max_pages) * c.page_size > (int64_t(1) << 30))
+    return false;
+  return c.head_dim == 64 || c.head_dim == 128;
+}
+
 // Set by os_attention_set_rescale_policy; kept for the host thread's later
 // attention calls.
 thread_local int t_rescale_policy = OS_RESCALE_THRESHOLD;
@@ -427,6 +457,104 @@ os_status os_attention_decode_paged(const void* q, int64_t ld_q_batch, int64_t l
   return from_cuda(oss::launch_decode_paged(static_cast<const uint16_t*>(q), ld_q_batch, ld_q_head, H, *cache,
                                             scale, static_cast<uint16_t*>(o), lse, weights, ld_w_batch,
                                             ld_w_head, workspace, err, static_cast<cudaStream_t>(stream)));
+}
+
+os_status os_kv_cache_append_fp8(const void* k, const void* v, int64_t ld_token, int64_t ld_head, int64_t tokens,
+                                 const int32_t* cu_seqlens, const os_paged_cache_fp8* cache, void* stream) {
+  os_status st = check_cache_fp8(cache);
+  if (st != OS_OK) return st;
+  if (tokens < 0 || ld_token < 0 || ld_head < 0 || (!cu_seqlens && tokens != cache->pages.batch))
+    return OS_ERR_INVALID_ARGUMENT;
+  if (tokens == 0) return OS_OK;
+  if ((st = check_rows(k, v, ld_token, ld_head, tokens, cu_seqlens)) != OS_OK) return st;
+  unsigned int* err = error_word();
+  if (!err) return OS_ERR_CUDA;
+  return from_cuda(oss::launch_kv_append_fp8(static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), ld_token,
+                                             ld_head, tokens, cu_seqlens, *cache, err,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+os_status os_kv_cache_read_fp8(const os_paged_cache_fp8* cache, const int32_t* cu_seqlens, int64_t tokens, void* k,
+                               void* v, int64_t ld_token, int64_t ld_head, void* stream) {
+  os_status st = check_cache_fp8(cache);
+  if (st != OS_OK) return st;
+  if (tokens < 0 || !cu_seqlens) return OS_ERR_INVALID_ARGUMENT;
+  // a stride of 0 would put several rows in one place
+  if (ld_token < (tokens > 1) || ld_head < (cache->pages.heads > 1)) return OS_ERR_INVALID_ARGUMENT;
+  if (tokens == 0) return OS_OK;
+  if ((st = check_rows(k, v, ld_token, ld_head, tokens, cu_seqlens)) != OS_OK) return st;
+  unsigned int* err = error_word();
+  if (!err) return OS_ERR_CUDA;
+  return from_cuda(oss::launch_kv_read_fp8(*cache, cu_seqlens, tokens, static_cast<uint16_t*>(k),
+                                           static_cast<uint16_t*>(v), ld_token, ld_head, err,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int64_t os_attention_decode_paged_fp8_workspace_bytes(int32_t H, const os_paged_cache_fp8* cache) {
+  if (!cache || !sized_cache(H, cache->pages)) return 0;
+  return oss::decode_paged_fp8_workspace_bytes(H, cache->pages);
+}
+
+os_status os_attention_decode_paged_fp8(const void* q, int64_t ld_q_batch, int64_t ld_q_head, int32_t H,
+                                        const os_paged_cache_fp8* cache, float scale, void* o, float* lse,
+                                        void* workspace, int64_t workspace_bytes, void* stream) {
+  const os_status st = check_cache_fp8(cache);
+  if (st != OS_OK) return st;
+  if (!q || !o || !workspace || H <= 0 || H % cache->pages.heads || !valid_scale(scale)) return OS_ERR_INVALID_ARGUMENT;
+  if (ld_q_batch < 0 || ld_q_head < 0) return OS_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || ((ld_q_batch | ld_q_head) & 7))
+    return OS_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return OS_ERR_MISALIGNED;
+  if (H > 65535) return OS_ERR_UNSUPPORTED;
+  const int64_t need = oss::decode_paged_fp8_workspace_bytes(H, cache->pages);
+  if (need < 0) return OS_ERR_CUDA;
+  if (workspace_bytes < need) return OS_ERR_INVALID_ARGUMENT;
+  unsigned int* err = error_word();
+  if (!err) return OS_ERR_CUDA;
+  return from_cuda(oss::launch_decode_paged_fp8(static_cast<const uint16_t*>(q), ld_q_batch, ld_q_head, H, *cache, scale,
+                                                static_cast<uint16_t*>(o), lse, workspace, err,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+int64_t os_attention_decode_shared_workspace_bytes(int32_t H, const os_paged_cache* cache, int32_t prefix_max_pages,
+                                                   int32_t groups) {
+  if (!cache || !sized_cache(H, *cache) || groups <= 0 || groups > 65535 || prefix_max_pages <= 0 ||
+      static_cast<int64_t>(prefix_max_pages) * cache->page_size > (int64_t(1) << 30))
+    return 0;
+  return oss::decode_shared_workspace_bytes(H, *cache, groups, prefix_max_pages);
+}
+
+os_status os_attention_decode_shared(const void* q, int64_t ld_q_batch, int64_t ld_q_head, int32_t H,
+                                     const os_paged_cache* cache, const int32_t* prefix_table, int64_t ld_prefix_table,
+                                     const int32_t* prefix_len, int32_t prefix_max_pages, const int32_t* cu_groups,
+                                     int32_t groups, float scale, void* o, float* lse, void* workspace,
+                                     int64_t workspace_bytes, void* stream) {
+  const os_status st = check_cache(cache);
+  if (st != OS_OK) return st;
+  if (!q || !o || !workspace || H <= 0 || H % cache->heads || !valid_scale(scale)) return OS_ERR_INVALID_ARGUMENT;
+  if (!prefix_table || !prefix_len || ld_prefix_table < 0 || prefix_max_pages <= 0 || groups <= 0 ||
+      (!cu_groups && groups != 1))
+    return OS_ERR_INVALID_ARGUMENT;
+  // a tensor map wants a positive stride for a dimension that is walked
+  if (ld_q_batch < (cache->batch > 1) || ld_q_head < (H > 1)) return OS_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || ((ld_q_batch | ld_q_head) & 7))
+    return OS_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(prefix_table) |
+       reinterpret_cast<uintptr_t>(prefix_len) | reinterpret_cast<uintptr_t>(cu_groups)) & 3u)
+    return OS_ERR_MISALIGNED;
+  if (H > 65535 || groups > 65535 || static_cast<int64_t>(prefix_max_pages) * cache->page_size > (int64_t(1) << 30))
+    return OS_ERR_UNSUPPORTED;
+  const int64_t need = oss::decode_shared_workspace_bytes(H, *cache, groups, prefix_max_pages);
+  if (need < 0) return OS_ERR_CUDA;
+  if (workspace_bytes < need) return OS_ERR_INVALID_ARGUMENT;
+  unsigned int* err = error_word();
+  if (!err) return OS_ERR_CUDA;
+  const oss::PrefixTables prefix{prefix_table, ld_prefix_table, prefix_len, cu_groups, groups, prefix_max_pages};
+  const oss::AttnFault fault = t_fault;
+  t_fault = oss::AttnFault();
+  return from_cuda(oss::launch_decode_shared(static_cast<const uint16_t*>(q), ld_q_batch, ld_q_head, H, *cache, prefix,
+                                             scale, static_cast<uint16_t*>(o), lse, workspace, err, fault,
+                                             static_cast<cudaStream_t>(stream)));
 }
 
 int64_t os_attention_fwd_packed_workspace_bytes(int64_t tokens_k, int32_t Hkv, int32_t D) {

@@ -1,0 +1,220 @@
+// The paged key-value cache in 8 bits: appending new tokens, and reading them back.
+//
+// A row (a token's key or value in one key head) is D e4m3 values and one
+// power-of-two scale 2^e, e the smallest integer >= -127 with max |x| <= 448 * 2^e (448 is
+// e4m3's largest value), stored as the byte e + 127 (e8m0; 255 is NaN). Dividing by a
+// power of two is exact, so the only rounding is the one to e4m3, and the codes do not
+// depend on how a division rounds. A scale that is no power of two would buy
+// nothing: e4m3 is a floating format, and its values' relative error is the same
+// anywhere between 448 and 2^-6.
+//
+// Both are copies bound by HBM: 2 D and D + 1 bytes a row on either side.
+
+#include <cstdint>
+
+#include "device_common.cuh"
+#include "fp8.cuh"
+#include "launch.cuh"
+#include "oss_internal.h"
+#include "paged.h"
+
+namespace oss {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void bad_index(unsigned int* err, unsigned int site) {
+  report_error(err, kKernelPaged | (site << 8));
+}
+
+// Offsets that do not fit the rows: tokens that kv_len counts have no row.
+__device__ __forceinline__ void check_offsets(const int32_t* cu, int32_t batch, int64_t tokens, unsigned int* err) {
+  for (int b = blockIdx.x * kThreads + threadIdx.x; b < batch; b += gridDim.x * kThreads)
+    if (row_range(cu[b], cu[b + 1], static_cast<int32_t>(tokens)).clamped) bad_index(err, kSiteBadOffsets);
+}
+
+// Page and slot of packed row `token` (cu null: the last token of sequence `token`);
+// false for a row without one.
+__device__ __forceinline__ bool locate(int32_t token, const int32_t* __restrict__ cu, const PagedCache& c, int* page,
+                                       int* slot, unsigned int* err) {
+  int seq = token;
+  int64_t behind = 1;  // tokens of the sequence from this one on
+  if (cu) {
+    seq = sequence_of(token, cu, c.batch);
+    if (seq < 0) return false;  // a row of no sequence
+    behind = cu[seq + 1] - token;
+  }
+  const int32_t len = c.kv_len[seq];
+  if (!cu && len == 0) return false;  // an empty place of the batch
+  const int64_t pos = len - behind;
+  if (pos < 0 || (pos >> c.page_shift) >= c.max_pages) {
+    bad_index(err, kSiteBadPosition);
+    return false;
+  }
+  *page = c.table[static_cast<int64_t>(seq) * c.ld_table + (pos >> c.page_shift)];
+  if (!page_ok(*page, c.num_pages)) {
+    bad_index(err, kSiteBadPage);
+    return false;
+  }
+  *slot = static_cast<int>(pos) & ((1 << c.page_shift) - 1);
+  return true;
+}
+
+// The larger of two pairs of 16-bit magnitudes.
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// One thread's 16 values of a row, as they were loaded.
+struct Chunk {
+  uint4 a, b;
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+  }
+};
+
+__device__ __forceinline__ Chunk load_chunk(const uint16_t* p) {
+  const uint4* x = reinterpret_cast<const uint4*>(p);
+  return Chunk{x[0], x[1]};
+}
+
+// Codes of this thread's 16 values and the scale of the row that kLanes threads hold.
+template <bool kF16, int kLanes>
+__device__ __forceinline__ uint4 quantise(const Chunk& x, uint32_t lanes, uint32_t* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_pair(top, x.word(i) & 0x7fff7fffu);
+  top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+  for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(lanes, top, off));
+  const uint32_t s = fp8_scale_byte(__float_as_uint(widen2<kF16>(top).x));
+  *scale = s;
+  // a row with NaN or infinity reads as NaN
+  if (s == kFp8ScaleNan) return make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+  const float down = __uint_as_float((254u - s) << 23);  // 2^-e
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 lo = widen2<kF16>(x.word(2 * i)), hi = widen2<kF16>(x.word(2 * i + 1));
+    w[i] = to_e4m3x2(lo.x * down, lo.y * down) | (to_e4m3x2(hi.x * down, hi.y * down) << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// D / 16 threads a row, 16 values of K and of V each.
+template <bool kF16, int kLanes>
+__global__ void __launch_bounds__(kThreads)
+kv_append_fp8_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t ld_token, int64_t ld_head,
+                     int64_t tokens, const int32_t* __restrict__ cu, PagedCache c, Fp8Pools f, unsigned int* err) {
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  if (cu) check_offsets(cu, c.batch, tokens, err);
+  const int part = threadIdx.x % kLanes;
+  const uint32_t lanes = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));  // of this row, in the warp
+  const int64_t rows = tokens * c.heads;
+  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes; row < rows;
+       row += static_cast<int64_t>(gridDim.x) * (kThreads / kLanes)) {
+    const int32_t token = static_cast<int32_t>(row / c.heads);
+    const int head = static_cast<int>(row - static_cast<int64_t>(token) * c.heads);
+    const int64_t from = token * ld_token + head * ld_head + part * 16;
+    const Chunk kx = load_chunk(k + from), vx = load_chunk(v + from);
+    int page, slot;
+    const bool there = locate(token, cu, c, &page, &slot, err);  // the same for all threads of the row
+    uint32_t ks, vs;
+    const uint4 kc = quantise<kF16, kLanes>(kx, lanes, &ks), vc = quantise<kF16, kLanes>(vx, lanes, &vs);
+    if (!there) continue;
+    const int64_t to = pool_offset(page, head, slot, c.ld_page, c.ld_head, c.ld_slot) + part * 16;
+    *reinterpret_cast<uint4*>(f.k + to) = kc;
+    *reinterpret_cast<uint4*>(f.v + to) = vc;
+    if (part == 0) {
+      const int64_t at = pool_offset(page, head, slot, f.ld_page, f.ld_head, 1);
+      f.k_scales[at] = static_cast<uint8_t>(ks);
+      f.v_scales[at] = static_cast<uint8_t>(vs);
+    }
+  }
+}
+
+template <bool kF16>
+__device__ __forceinline__ void store_values(uint16_t* to, uint4 codes, float scale) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t c = i < 2 ? codes.x : i < 4 ? codes.y : i < 6 ? codes.z : codes.w;
+    const float2 x = widen2<true>(from_e4m3x2(c >> (16 * (i & 1))));
+    w[i] = pack2<kF16>(x.x * scale, x.y * scale);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(to);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <bool kF16, int kLanes>
+__global__ void __launch_bounds__(kThreads)
+kv_read_fp8_kernel(PagedCache c, Fp8Pools f, const int32_t* __restrict__ cu, int64_t tokens, uint16_t* __restrict__ k,
+                   uint16_t* __restrict__ v, int64_t ld_token, int64_t ld_head, unsigned int* err) {
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  check_offsets(cu, c.batch, tokens, err);
+  const int part = threadIdx.x % kLanes;
+  const int64_t rows = tokens * c.heads;
+  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes; row < rows;
+       row += static_cast<int64_t>(gridDim.x) * (kThreads / kLanes)) {
+    const int32_t token = static_cast<int32_t>(row / c.heads);
+    const int head = static_cast<int>(row - static_cast<int64_t>(token) * c.heads);
+    int page, slot;
+    if (!locate(token, cu, c, &page, &slot, err)) continue;
+    const int64_t from = pool_offset(page, head, slot, c.ld_page, c.ld_head, c.ld_slot) + part * 16;
+    const int64_t at = pool_offset(page, head, slot, f.ld_page, f.ld_head, 1);
+    const uint4 kc = *reinterpret_cast<const uint4*>(f.k + from), vc = *reinterpret_cast<const uint4*>(f.v + from);
+    const float ks = fp8_scale_value(f.k_scales[at]), vs = fp8_scale_value(f.v_scales[at]);
+    const int64_t to = token * ld_token + head * ld_head + part * 16;
+    store_values<kF16>(k + to, kc, ks);
+    store_values<kF16>(v + to, vc, vs);
+  }
+}
+
+// CTAs for `rows` rows of `lanes` threads: at most 64 an SM, whose threads go on to further rows.
+unsigned copy_blocks(int64_t rows, int lanes, int sms) {
+  const int64_t n = (rows * lanes + kThreads - 1) / kThreads, most = static_cast<int64_t>(sms) * 64;
+  return static_cast<unsigned>(n < most ? n : most);
+}
+
+}  // namespace
+
+Fp8Pools fp8_pools(const os_paged_cache_fp8& c) {
+  return Fp8Pools{static_cast<uint8_t*>(c.pages.k_pages), static_cast<uint8_t*>(c.pages.v_pages),
+                  static_cast<uint8_t*>(c.k_scales), static_cast<uint8_t*>(c.v_scales), c.ld_scale_page, c.ld_scale_head};
+}
+
+cudaError_t launch_kv_append_fp8(const uint16_t* k, const uint16_t* v, int64_t ld_token, int64_t ld_head, int64_t tokens,
+                                 const int32_t* cu, const os_paged_cache_fp8& cache, unsigned int* err,
+                                 cudaStream_t stream) {
+  const int sms = device_sms();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  const int lanes = cache.pages.head_dim / 16;
+  const dim3 grid(copy_blocks(tokens * cache.pages.heads, lanes, sms));
+  const PagedCache c = paged_cache(cache.pages);
+  const Fp8Pools f = fp8_pools(cache);
+  const auto launch = [&](auto* kernel) {
+    return launch_after(kernel, grid, kThreads, 0, stream, k, v, ld_token, ld_head, tokens, cu, c, f, err);
+  };
+  if (cache.pages.dtype == OS_DTYPE_F16)
+    return lanes == 8 ? launch(kv_append_fp8_kernel<true, 8>) : launch(kv_append_fp8_kernel<true, 4>);
+  return lanes == 8 ? launch(kv_append_fp8_kernel<false, 8>) : launch(kv_append_fp8_kernel<false, 4>);
+}
+
+cudaError_t launch_kv_read_fp8(const os_paged_cache_fp8& cache, const int32_t* cu, int64_t tokens, uint16_t* k,
+                               uint16_t* v, int64_t ld_token, int64_t ld_head, unsigned int* err, cudaStream_t stream) {
+  const int sms = device_sms();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  const int lanes = cache.pages.head_dim / 16;
+  const dim3 grid(copy_blocks(tokens * cache.pages.heads, lanes, sms));
+  const PagedCache c = paged_cache(cache.pages);
+  const Fp8Pools f = fp8_pools(cache);
+  const auto launch = [&](auto* kernel) {
+    return launch_after(kernel, grid, kThreads, 0, stream, c, f, cu, tokens, k, v, ld_token, ld_head, err);
+  };
+  if (cache.pages.dtype == OS_DTYPE_F16)
+    return lanes == 8 ? launch(kv_read_fp8_kernel<true, 8>) : launch(kv_read_fp8_kernel<true, 4>);
+  return lanes == 8 ? launch(kv_read_fp8_kernel<false, 8>) : launch(kv_read_fp8_kernel<false, 4>);
+}
+
+}  // namespace oss

@@ -125,6 +125,33 @@ cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t l
                                 float* weights, int64_t ld_w_batch, int64_t ld_w_head,
                                 void* workspace, unsigned int* err, cudaStream_t stream);
 
+// The pools of a validated os_paged_cache_fp8, for kernels.
+struct Fp8Pools;
+Fp8Pools fp8_pools(const os_paged_cache_fp8& c);
+
+cudaError_t launch_kv_append_fp8(const uint16_t* k, const uint16_t* v, int64_t ld_token, int64_t ld_head, int64_t tokens,
+                                 const int32_t* cu, const os_paged_cache_fp8& cache, unsigned int* err,
+                                 cudaStream_t stream);
+
+cudaError_t launch_kv_read_fp8(const os_paged_cache_fp8& cache, const int32_t* cu, int64_t tokens, uint16_t* k,
+                               uint16_t* v, int64_t ld_token, int64_t ld_head, unsigned int* err, cudaStream_t stream);
+
+// Workspace of the 8-bit paged decode on the current device (-1: it could not be queried).
+int64_t decode_paged_fp8_workspace_bytes(int H, const os_paged_cache& pages);
+
+cudaError_t launch_decode_paged_fp8(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
+                                    const os_paged_cache_fp8& cache, float scale, uint16_t* o, float* lse,
+                                    void* workspace, unsigned int* err, cudaStream_t stream);
+
+// Workspace of the decode behind shared prefixes on the current device (-1: it could not be
+// queried).
+int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache, int groups, int prefix_max_pages);
+
+cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
+                                 const os_paged_cache& cache, const PrefixTables& prefix, float scale, uint16_t* o,
+                                 float* lse, void* workspace, unsigned int* err, const AttnFault& fault,
+                                 cudaStream_t stream);
+
 // Arguments of the packed attention forward, as os_attention_fwd_packed's.
 struct PackedArgs {
   const uint16_t *q, *k, *v;

@@ -82,12 +82,45 @@ OSS_HD RowRange row_range(int32_t begin, int32_t end, int32_t tokens) {
   return r;
 }
 
+// The prefixes that groups of sequences share: group g is sequences cu[g] .. cu[g + 1] - 1
+// (cu null: one group of all), and its tokens are those of row g of the table.
+struct PrefixTables {
+  const int32_t* table;
+  int64_t ld_table;
+  const int32_t* len;
+  const int32_t* cu;
+  int32_t groups, max_pages;
+};
+
+// Group of sequence b, or -1.
+OSS_HD int32_t prefix_group(const PrefixTables& p, int32_t b) {
+  return p.cu ? sequence_of(b, p.cu, p.groups) : 0;
+}
+
 // Order of fp32 weights as unsigned integers: a larger weight has a larger
 // key, -0 equals 0, NaN is above infinity.
 OSS_HD uint32_t weight_key_bits(uint32_t u) {
   if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;  // NaN
   if (u == 0x80000000u) u = 0u;                             // -0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// The scale byte e + 127 of a row of the 8-bit cache, from the fp32 bits of its largest
+// magnitude f * 2^n, f in [1, 2). With 448 = 1.75 * 2^8, e = n - 8, or n - 7 for f >
+// 1.75, which is where adding 2^21 - 1 to the 23 bits of f carries into n. Magnitudes up
+// to 1.75 * 2^-119, 0 among them, take the least scale, 2^-127; infinity and NaN 255.
+constexpr uint32_t kFp8ScaleNan = 255;
+
+OSS_HD uint32_t fp8_scale_byte(uint32_t bits) {
+  if (bits >= 0x7f800000u) return kFp8ScaleNan;
+  const uint32_t field = (bits + 0x1fffffu) >> 23;
+  return field > 8 ? field - 8 : 0;
+}
+
+// The fp32 bits of the scale that a byte stands for.
+OSS_HD uint32_t fp8_scale_bits(uint32_t byte) {
+  if (byte == kFp8ScaleNan) return 0x7fffffffu;
+  return byte ? byte << 23 : 0x00400000u;  // 2^-127 is subnormal
 }
 
 }  // namespace oss
