@@ -1,0 +1,367 @@
+// Attention of one new token per sequence over a paged key-value cache in 8 bits.
+//
+//   s_t = scale 2^ek_t q.kcode_t;  lse = ln sum exp s_t;  o = sum exp(s_t - lse) 2^ev_t vcode_t
+//
+// The walk, the division of the work and the join are those of the 16-bit decode
+// (decode_paged.cu). What differs:
+//
+// Products. Codes are exact in fp16 (4 significant bits, 2^-9 to 448), so both products
+// run as fp16 mma.sync with fp32 sums, whatever the type of q and o. (An e4m3 MMA would want q
+// and the weights in 8 bits.) A bf16 q is brought into fp16's range by a power of two per
+// head: its largest element comes to 2^14 .. 2^15, and what then falls below fp16's
+// normal range is below 2^-28 of it.
+//
+// Scales. The key's is a factor on the score. The value's goes into the weight's
+// exponent, 2^(s + ev - m'), so V needs no multiplication. Weights of values far larger
+// than others would leave fp16's range if they were taken relative to the largest score
+// alone; so O has a reference of its own, m' = max (s + ev), and l keeps m = max s: two
+// exponentials a score. Where warps and parts meet, O comes to m.
+//
+// Fragments. ldmatrix moves 16-bit elements, here pairs of codes. A K register holds
+// four consecutive dims of a key; the MMA's k index is permuted to fit (dims 4 q, 4 q + 1 in
+// its columns 2 q, 2 q + 1, and 4 q + 2, 4 q + 3 in 2 q + 8, 2 q + 9), and q's fragments
+// likewise. A transposed V register holds two dims of two keys; a byte permutation
+// sorts them by dim, and rows r and r + 8 of the MMA are dims 2 r and 2 r + 1.
+
+#include <atomic>
+#include <cstdint>
+
+#include "decode_paged.cuh"
+#include "device_common.cuh"
+#include "fp8.cuh"
+#include "launch.cuh"
+#include "oss_internal.h"
+
+namespace oss {
+namespace {
+
+using namespace decode;
+
+#ifndef FP8_CTAS
+#define FP8_CTAS 3
+#endif
+#ifndef FP8_STAGES
+#define FP8_STAGES (kCtas == 3 ? 3 : 5)
+#endif
+constexpr int ctas_per_sm(int NT) { return NT == 1 ? FP8_CTAS : 2; }
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kCtas = ctas_per_sm(NT);
+  static constexpr int kStages = FP8_STAGES * (128 / D);
+  static constexpr int kTileBytes = kTileKeys * D;   // K or V
+  static constexpr int kScaleBytes = 2 * kTileKeys;  // K's, then V's
+  static constexpr int kRingBytes = kWarps * kStages * 2 * kTileBytes;
+  static constexpr int kScaleRing = kWarps * kStages * kScaleBytes;
+  static constexpr int kSmemBytes = kRingBytes + kScaleRing + kMergeBytes<D>;
+};
+
+// Byte offset of 16-byte chunk c of row r of a tile, so that eight rows of a chunk
+// touch all banks.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+}
+
+// NT: blocks of 8 query heads.
+template <bool kF16, int D, int NT>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(const DecodeParams p, const Fp8Pools f) {
+  using S = Shape<D, NT>;
+  constexpr int kChunks = D / 16;             // 16-byte chunks of a row
+  constexpr int kRowsPerCopy = 32 / kChunks;  // rows a warp's copy instruction covers
+  constexpr int kStages = S::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float merge_m[kWarps][8], merge_l[kWarps][8];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = lane & 3, row8 = lane >> 2;
+
+  Walk w;
+  ShareCut share;
+  const bool has_share = find_share(p, &w, &share);
+  if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (!has_share) return;
+
+  const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * S::kTileBytes;
+  const uint8_t* scale_ring = smem + S::kRingBytes + warp * kStages * S::kScaleBytes;
+  float* merge = reinterpret_cast<float*>(smem + S::kRingBytes + S::kScaleRing);
+  const int copy_row = lane / kChunks, copy_chunk = lane % kChunks;
+
+  // ---- the loads' cursor: the tile to be loaded next, and its page
+  Walk lw = w;
+  int lt = lw.s.r0 * p.unit_tiles + warp;
+  bool more = true;
+  int page = 0;
+  auto settle = [&]() {  // move to the next tile that exists, fetch its page number
+    while (lt >= lw.tile_end(p)) {
+      if (!(more = lw.next(p))) return;
+      lt = lw.s.r0 * p.unit_tiles + warp;
+    }
+    page = p.c.table[static_cast<int64_t>(lw.s.b) * p.c.ld_table + ((lt * kTileKeys) >> p.c.page_shift)];
+  };
+  uint32_t bad = 0;  // stages whose tile has a page outside the pool
+  auto load = [&](int stage) {
+    if (more) {
+      const int key0 = lt * kTileKeys;
+      const bool ok = page_ok(page, p.c.num_pages);
+      if (!ok) report_error(p.err, kKernelPaged | (kSiteBadPage << 8));
+      bad = (bad & ~(1u << stage)) | (ok ? 0u : 1u << stage);
+      const int g = lw.s.j / p.head_blocks, slot0 = key0 & ((1 << p.c.page_shift) - 1);
+      const int64_t at = ok ? pool_offset(page, g, slot0 + copy_row, p.c.ld_page, p.c.ld_head, p.c.ld_slot) + copy_chunk * 16
+                            : 0;
+      const int rows = ok ? lw.s.len - key0 : 0;  // rows of the tile that hold a token
+      const uint32_t dst = ring + stage * 2 * S::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < kTileKeys / kRowsPerCopy; ++i) {
+        const int r = i * kRowsPerCopy + copy_row;
+        const bool there = r < rows;
+        const int64_t src = there ? at + i * kRowsPerCopy * p.c.ld_slot : 0;
+        const uint32_t d = dst + chunk_at<D>(r, copy_chunk);
+        copy16(d, f.k + src, there);
+        copy16(d + S::kTileBytes, f.v + src, there);
+      }
+      if (lane < 2) {
+        const int64_t sc = ok ? pool_offset(page, g, slot0, f.ld_page, f.ld_head, 1) : 0;
+        copy16(smem_u32(scale_ring) + stage * S::kScaleBytes + lane * kTileKeys, (lane ? f.v_scales : f.k_scales) + sc, ok);
+      }
+      lt += kUnitTiles;
+      settle();
+    }
+    copy_commit();
+  };
+  settle();
+#pragma unroll 1
+  for (int i = 0; i < kStages; ++i) load(i);
+
+  int stage = 0;
+  bool go = true;
+  while (go) {
+    const Segment s = w.s;
+    const int g = s.j / p.head_blocks, hb = s.j - g * p.head_blocks;
+    const int head0 = g * p.group + hb * p.block_heads;          // first query head of the block
+    const int heads = min(p.block_heads, p.group - hb * p.block_heads);
+    // Q^T fragments in fp16: head row8 of each 8, dims 16 kk + 4 quad + {0, 1} and {2, 3}
+    uint32_t qf[NT][D / 16][2];
+    float qs[NT][2];  // factors of the scores of heads 8 nt + 2 quad + {0, 1}
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool live = nt * 8 + row8 < heads;
+      const uint2* src = reinterpret_cast<const uint2*>(
+          p.q + s.b * p.ld_q_batch + static_cast<int64_t>(live ? head0 + nt * 8 + row8 : 0) * p.ld_q_head);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint2 x = live ? src[4 * kk + quad] : make_uint2(0u, 0u);
+        qf[nt][kk][0] = x.x;
+        qf[nt][kk][1] = x.y;
+      }
+      float up = 1.f;
+      if constexpr (!kF16) {
+        uint32_t top = 0;  // the head's largest magnitude
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) top = __vmaxu2(top, qf[nt][kk][e] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // exponent field n of the largest: times 2^(127 + 14 - n); NaN, infinity and 0 as
+        // they are, and below 2^-100 no further up than from there
+        const uint32_t n = max(top >> 7, 27u);
+        const bool plain = top >= 0x7f80u;
+        const float to = plain ? 1.f : __uint_as_float((127u + 127u + 14u - n) << 23);
+        up = plain ? 1.f : __uint_as_float((n - 14u) << 23);  // 1 / to
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = widen2<false>(qf[nt][kk][e]);
+            qf[nt][kk][e] = pack2<true>(x.x * to, x.y * to);
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qs[nt][e] = __shfl_sync(0xffffffffu, up, (2 * quad + e) * 4) * p.scale2;
+    }
+    float m[NT][2], l[NT][2];   // heads 8 nt + 2 quad + {0, 1}; l: this thread's keys
+    float mo[NT][2];            // O's reference
+    float od[NT][D / 16][4];    // dims 16 i + 2 row8 (+ 1), the same heads
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = mo[nt][0] = mo[nt][1] = neg_inf();
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) od[nt][i][e] = 0.f;
+    }
+    const int t_end = w.tile_end(p);
+    for (int t = s.r0 * p.unit_tiles + warp; t < t_end; t += kUnitTiles) {
+      copy_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t kt = ring + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes;
+      // lanes 0 .. 15: the keys' scales, 16 .. 31: the values' exponents
+      const uint32_t byte = scale_ring[stage * S::kScaleBytes + lane];
+      const float ev = byte == kFp8ScaleNan ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | byte) - 8388735.f;
+      const float sv = lane < 16 ? fp8_scale_value(byte) : ev;
+      float sc[NT][2][4];  // two sums: even and odd dims' chunks
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[4];
+        ldmatrix4(x, kt + chunk_at<D>(lane & 15, 2 * c + (lane >> 4)));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t a[4] = {from_e4m3x2(x[2 * half]), from_e4m3x2(x[2 * half + 1]), from_e4m3x2(x[2 * half] >> 16),
+                                 from_e4m3x2(x[2 * half + 1] >> 16)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<true>(sc[nt][half], a, qf[nt][2 * c + half][0], qf[nt][2 * c + half][1]);
+        }
+      }
+      const float ka = __shfl_sync(0xffffffffu, sv, row8), kb = __shfl_sync(0xffffffffu, sv, row8 + 8);
+      const float va = __shfl_sync(0xffffffffu, sv, row8 + 16), vb = __shfl_sync(0xffffffffu, sv, row8 + 24);
+      const int key = t * kTileKeys + row8;
+      const bool masked = (bad >> stage) & 1u;
+      const bool live_a = key < s.len && !masked, live_b = key + 8 < s.len && !masked;
+      float x[NT][4], y[NT][4];  // scores in base 2, and with the value's exponent
+      bool rise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool live = e < 2 ? live_a : live_b;
+          const float z = (sc[nt][0][e] + sc[nt][1][e]) * qs[nt][e & 1] * (e < 2 ? ka : kb);
+          x[nt][e] = live ? z : neg_inf();
+          y[nt][e] = live ? z + (e < 2 ? va : vb) : neg_inf();
+          rise |= x[nt][e] > m[nt][e & 1] + kSlack || y[nt][e] > mo[nt][e & 1] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float corr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(x[nt][e], x[nt][e + 2]), my = fmaxf(y[nt][e], y[nt][e + 2]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+              my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, off));
+            }
+            mx = fmaxf(mx, m[nt][e]);
+            my = fmaxf(my, mo[nt][e]);
+            l[nt][e] *= mx == neg_inf() ? 1.f : ex2(m[nt][e] - mx);
+            corr[e] = my == neg_inf() ? 1.f : ex2(mo[nt][e] - my);
+            m[nt][e] = mx;
+            mo[nt][e] = my;
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) od[nt][i][e] *= corr[e & 1];
+        }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float pe[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          l[nt][e & 1] += ex2(x[nt][e] - reference(m[nt][e & 1]));
+          pe[e] = ex2(y[nt][e] - reference(mo[nt][e & 1]));
+        }
+        pf[nt][0] = transpose8x8(pack2<true>(pe[0], pe[1]));
+        pf[nt][1] = transpose8x8(pack2<true>(pe[2], pe[3]));
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[4];
+        ldmatrix4_trans(v, vt + chunk_at<D>(lane & 15, 2 * c + (lane >> 4)));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // bytes {key, dim}: 00 01 10 11 -> 00 10 01 11
+          const uint32_t lo = __byte_perm(v[2 * half], 0, 0x3120), hi = __byte_perm(v[2 * half + 1], 0, 0x3120);
+          const uint32_t a[4] = {from_e4m3x2(lo), from_e4m3x2(lo >> 16), from_e4m3x2(hi), from_e4m3x2(hi >> 16)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<true>(od[nt][2 * c + half], a, pf[nt][0], pf[nt][1]);
+        }
+      }
+      __syncwarp();
+      load(stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    // ---- the four warps' states, 8 heads at a time
+    const bool whole = s.r0 == 0 && s.r1 == s.units;
+    const int slot = open_segment(p, w, share, whole);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float to[2];  // O from its own reference to l's, in two steps: 2^-127 is no normal number
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
+        to[e] = ex2(0.5f * (reference(mo[nt][e]) - reference(m[nt][e])));
+      }
+      float* mine = merge + warp * 8 * kMergeLd<D>;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(mine + (2 * quad + e) * kMergeLd<D> + 16 * i + 2 * row8) =
+              make_float2(od[nt][i][e] * to[e] * to[e], od[nt][i][e + 2] * to[e] * to[e]);
+      if (row8 == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          merge_m[warp][2 * quad + e] = m[nt][e];
+          merge_l[warp][2 * quad + e] = l[nt][e];
+        }
+      }
+      __syncthreads();
+      merge_warps<kF16, D>(p, s, whole, slot, head0, nt * 8, heads, merge, merge_m, merge_l);
+      __syncthreads();
+    }
+    go = w.next(p);
+  }
+  copy_wait<0>();
+}
+
+template <bool kF16, int D, int NT>
+cudaError_t launch_shape(const DecodeParams& p, const Fp8Pools& f, int shares, cudaStream_t stream) {
+  constexpr int smem = Shape<D, NT>::kSmemBytes;
+  static std::atomic<bool> smem_set[kMaxDevices];
+  const cudaError_t e = raise_smem(decode_fp8_kernel<kF16, D, NT>, smem, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_after(decode_fp8_kernel<kF16, D, NT>, dim3(shares), kThreads, smem, stream, p, f);
+}
+
+template <bool kF16, int D>
+cudaError_t launch_heads(const DecodeParams& p, const Fp8Pools& f, int shares, cudaStream_t stream) {
+  const cudaError_t e = p.block_heads == 8 ? launch_shape<kF16, D, 1>(p, f, shares, stream) : launch_shape<kF16, D, 2>(p, f, shares, stream);
+  return e != cudaSuccess ? e : launch_join(p, kF16, D, shares, stream);
+}
+
+int ctas_of(int H, const os_paged_cache& c) { return ctas_per_sm(heads_of_block(H / c.heads) / 8); }
+
+}  // namespace
+
+int64_t decode_paged_fp8_workspace_bytes(int H, const os_paged_cache& pages) {
+  Plan pl;
+  return make_plan(H, pages, ctas_of(H, pages), false, &pl) ? pl.bytes : -1;
+}
+
+cudaError_t launch_decode_paged_fp8(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
+                                    const os_paged_cache_fp8& cache, float scale, uint16_t* o, float* lse,
+                                    void* workspace, unsigned int* err, cudaStream_t stream) {
+  Plan pl;
+  if (!make_plan(H, cache.pages, ctas_of(H, cache.pages), false, &pl)) return cudaErrorInvalidDevice;
+  const DecodeParams p = decode_params(pl, paged_cache(cache.pages), q, ld_q_batch, ld_q_head, H, scale, o, lse, workspace, err);
+  const Fp8Pools f = fp8_pools(cache);
+  if (cache.pages.dtype == OS_DTYPE_F16)
+    return cache.pages.head_dim == 128 ? launch_heads<true, 128>(p, f, pl.shares, stream)
+                                       : launch_heads<true, 64>(p, f, pl.shares, stream);
+  return cache.pages.head_dim == 128 ? launch_heads<false, 128>(p, f, pl.shares, stream)
+                                     : launch_heads<false, 64>(p, f, pl.shares, stream);
+}
+
+}  // namespace oss

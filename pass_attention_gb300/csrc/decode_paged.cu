@@ -44,36 +44,17 @@
 #include <atomic>
 #include <cstdint>
 
+#include "decode_paged.cuh"
 #include "device_common.cuh"
 #include "launch.cuh"
 #include "oss_internal.h"
-#include "packed_plan.h"
-#include "paged.h"
 
 namespace oss {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTileKeys = 16;
-constexpr int kUnitTiles = kWarps;  // a unit: one tile per warp
+using namespace decode;
+
 constexpr int kCtasPerSm = 2;
-constexpr int kMaxHeadBlock = 16;
-// Items are not cut, and nothing is joined, when a row of the page table holds at
-// most kWholeKeys tokens, or at most kWholeKeysMany and there are as many items
-// as shares. Replayed from a graph, 32 heads over 8, whole against cut: 1 x 128 tokens
-// 4.9 against 7.4 us, 1 x 333 7.8 / 7.6 (but 3 us of the host for the second launch),
-// 64 x 256 12 / 18, 64 x 512 26 / 33; and 1 x 512 9.2 / 7.5. On the GPU the two meet
-// before 333; up to 384 it is the host's second launch that decides. The rule goes by
-// the table's width, because the lengths are on the device: short sequences in a wide
-// table are cut.
-constexpr int kWholeKeys = 384;
-constexpr int kWholeKeysMany = 512;
-constexpr float kLn2 = 0.69314718055994530942f;
-// The reference maximum moves only when a score exceeds it by more than
-// 2^kSlack: any reference gives the same quotient O / l, and weights up to 2^8 are
-// as exact in bf16 and fp16 as weights up to 1.
-constexpr float kSlack = 8.0f;
 
 template <int D>
 struct Shape {
@@ -82,185 +63,8 @@ struct Shape {
   static constexpr int kTileBytes = kTileKeys * kRowBytes;  // K or V
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kMergeLd = D + 4;  // floats; conflict-free for the accumulators' layout
-  static constexpr int kMergeBytes = kWarps * 8 * kMergeLd * 4;
-  static constexpr int kSmemBytes = kRingBytes + kMergeBytes;
+  static constexpr int kSmemBytes = kRingBytes + kMergeBytes<D>;
 };
-
-struct DecodeParams {
-  PagedCache c;
-  const uint16_t* q;
-  int64_t ld_q_batch, ld_q_head;
-  int32_t H, group, head_blocks, block_heads;  // block_heads: 8 or 16
-  int32_t unit_tiles;                          // tiles of a unit: 4, or all of an item
-  float scale2;                                // scale * log2(e)
-  uint16_t* o;
-  float* lse;
-  // workspace
-  float* part_o;    // [2 N][block_heads][D]
-  float2* part_ml;  // [2 N][block_heads]
-  int4* meta;       // [N]: {sequence, key head and head block, parts, first slot}
-  float* lse2;      // [batch][H], base 2: of items that were not cut (only with scores)
-  int2* item_meta;  // [batch][heads * head_blocks]: {first share, parts} (only with scores)
-  float* scores;    // [batch][heads * head_blocks][capacity][score_heads], or null
-  int32_t score_heads;
-  unsigned int* err;
-};
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// 16 bytes from global to shared memory, zeros when !there.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int n>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
-}
-
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-template <bool kF16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (kF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <bool kF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t w;
-  if constexpr (kF16)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  return w;
-}
-
-// What exponents are taken relative to where the maximum is m: 0 in place of -inf.
-// A part without a key then adds zeros, and one whose scores are NaN (which no
-// maximum shows) adds NaN instead of nothing.
-__device__ __forceinline__ float reference(float m) { return m == neg_inf() ? 0.f : m; }
-
-// Units [r0, r1) of an item: sequence b, key head and head block j.
-struct Segment {
-  int b, j, len, units, r0, r1;
-};
-
-// The walk of one CTA over its share [u, end) of the units.
-struct Walk {
-  Segment s;
-  int64_t u, end;
-
-  // (an empty sequence has a unit, to be answered)
-  __device__ __forceinline__ static int units_of(const DecodeParams& p, int len) {
-    if (p.unit_tiles != kUnitTiles) return 1;
-    const int n = (len + kTileKeys * kUnitTiles - 1) / (kTileKeys * kUnitTiles);
-    return n > 0 ? n : 1;
-  }
-  __device__ __forceinline__ void clip() {
-    const int64_t r1 = s.r0 + (end - u);
-    s.r1 = r1 < s.units ? static_cast<int>(r1) : s.units;
-  }
-  // The next segment of the share; false when there is none.
-  __device__ __forceinline__ bool next(const DecodeParams& p) {
-    u += s.r1 - s.r0;
-    if (u >= end) return false;
-    if (++s.j == p.c.heads * p.head_blocks) {
-      s.j = 0;
-      ++s.b;
-      s.len = paged_length(p.c.kv_len[s.b], p.c.max_pages, p.c.page_shift);
-      s.units = units_of(p, s.len);
-    }
-    s.r0 = 0;
-    clip();
-    return true;
-  }
-  // One past the last tile of the segment that holds a key.
-  __device__ __forceinline__ int tile_end(const DecodeParams& p) const {
-    return min(s.r1 * p.unit_tiles, (s.len + kTileKeys - 1) / kTileKeys);
-  }
-};
-
-// This CTA's share, from the lengths: every thread sums a run of sequences, a
-// block scan places the runs, and the thread whose run holds the first unit
-// finds the sequence in it. False when the CTA has no share.
-__device__ bool find_share(const DecodeParams& p, Walk* w, ShareCut* share) {
-  __shared__ int64_t warp_sum[kWarps];
-  __shared__ Walk found;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (p.c.batch + kThreads - 1) / kThreads;
-  const int b0 = min(p.c.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.c.batch, b0 + per);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b)
-    mine += Walk::units_of(p, paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift));
-  int64_t upto = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += y;
-  }
-  if (lane == 31) warp_sum[warp] = upto;
-  __syncthreads();
-  int64_t before = upto - mine, all = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) before += warp_sum[i];
-    all += warp_sum[i];
-  }
-  const int per_seq = p.c.heads * p.head_blocks;
-  const int64_t W = all * per_seq;
-  const ShareCut cut = share_cut(W, W < gridDim.x ? static_cast<int>(W) : static_cast<int>(gridDim.x));
-  *share = cut;
-  if (blockIdx.x >= cut.count) return false;
-  const int64_t first = share_begin(cut, blockIdx.x), last = share_begin(cut, blockIdx.x + 1);
-  if (first >= before * per_seq && first < (before + mine) * per_seq) {
-    int64_t at = before * per_seq;
-    for (int b = b0; b < b1; ++b) {
-      const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
-      const int units = Walk::units_of(p, len);
-      if (first < at + static_cast<int64_t>(units) * per_seq) {
-        Walk f;
-        f.s.b = b;
-        f.s.j = small_quotient(first - at, units);
-        f.s.len = len;
-        f.s.units = units;
-        f.s.r0 = static_cast<int>((first - at) - static_cast<int64_t>(f.s.j) * units);
-        f.s.r1 = 0;
-        f.u = first;
-        f.end = last;
-        f.clip();
-        found = f;
-        break;
-      }
-      at += static_cast<int64_t>(units) * per_seq;
-    }
-  }
-  __syncthreads();
-  *w = found;
-  return true;
-}
 
 // NT: blocks of 8 query heads.
 template <bool kF16, int D, int NT>
@@ -456,29 +260,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
     }
     // ---- the four warps' states, 8 heads at a time
     const bool whole = s.r0 == 0 && s.r1 == s.units;
-    const int slot = 2 * blockIdx.x + (s.r0 == 0 ? 1 : 0);
-    if (s.r0 == 0 && threadIdx.x == 0) {
-      int parts = 1;
-      if (!whole) {
-        // the item's last unit lies in the last of its shares
-        parts = static_cast<int>(last_boundary(share, w.u + s.units - 1) - blockIdx.x) + 1;
-        p.meta[blockIdx.x] = make_int4(s.b, s.j, parts, slot);
-      }
-      if (p.scores)
-        p.item_meta[static_cast<int64_t>(s.b) * p.c.heads * p.head_blocks + s.j] = make_int2(blockIdx.x, parts);
-    }
+    const int slot = open_segment(p, w, share, whole);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
-      float* mine = merge + warp * 8 * S::kMergeLd;
+      float* mine = merge + warp * 8 * kMergeLd<D>;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          mine[(2 * quad + (e & 1)) * S::kMergeLd + 16 * i + row8 + (e >> 1) * 8] = od[nt][i][e];
+          mine[(2 * quad + (e & 1)) * kMergeLd<D> + 16 * i + row8 + (e >> 1) * 8] = od[nt][i][e];
       if (row8 == 0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -500,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
         for (int i = 0; i < kWarps; ++i) {
           const float f = ex2(merge_m[i][hh] - reference(M));
           L = fmaf(merge_l[i][hh], f, L);
-          const float4* src = reinterpret_cast<const float4*>(merge + (i * 8 + hh) * S::kMergeLd + d0);
+          const float4* src = reinterpret_cast<const float4*>(merge + (i * 8 + hh) * kMergeLd<D> + d0);
 #pragma unroll
           for (int k = 0; k < kDims / 4; ++k) {
             const float4 x = src[k];
@@ -550,11 +344,6 @@ constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
 constexpr int kAddKeysPerThread = 4;
 constexpr int kAddKeys = kAddKeysPerThread * kFinishThreads;
-
-// Slot of part i of an item that begins in share c: part 0 in 2 c + 1, part i > 0 in 2 (c + i).
-__device__ __forceinline__ int64_t part_slot(int c, int i) {
-  return 2 * (static_cast<int64_t>(c) + i) + (i == 0 ? 1 : 0);
-}
 
 template <bool kF16, int D>
 __device__ __forceinline__ void join_head(const DecodeParams& p, int share, int hh) {
@@ -713,20 +502,54 @@ decode_finish_kernel(const DecodeParams p, int adds, int chunks, float* weights,
   join_head<kF16, D>(p, i / p.block_heads, i % p.block_heads);
 }
 
-// Layout of the workspace, the same for its size and its use.
-struct Plan {
-  int shares, block_heads, head_blocks, score_heads;
-  bool whole;  // items are not cut
-  int64_t part_o, part_ml, meta, lse2, item_meta, scores, bytes;  // offsets, then the size
-};
+template <bool kF16, int D>
+cudaError_t launch_finish(const DecodeParams& p, int shares, float* weights, int64_t ld_w_batch, int64_t ld_w_head,
+                          cudaStream_t stream) {
+  const int64_t joins = p.unit_tiles == kUnitTiles ? static_cast<int64_t>(shares) * p.block_heads : 0;
+  const int64_t chunks = weights ? ((static_cast<int64_t>(p.c.max_pages) << p.c.page_shift) + kAddKeys - 1) / kAddKeys : 0;
+  const int64_t adds = chunks * p.c.heads * p.c.batch, ctas = adds + joins;
+  if (ctas > 0x7fffffff) return cudaErrorNotSupported;
+  if (ctas == 0) return cudaSuccess;
+  return launch_after(decode_finish_kernel<kF16, D>, dim3(static_cast<unsigned>(ctas)), kFinishThreads, 0, stream, p,
+                      static_cast<int>(adds), static_cast<int>(chunks), weights, ld_w_batch, ld_w_head);
+}
 
-bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
+template <bool kF16, int D, int NT>
+cudaError_t launch_shape(const DecodeParams& p, int shares, cudaStream_t stream) {
+  constexpr int smem = Shape<D>::kSmemBytes;
+  static std::atomic<bool> smem_set[kMaxDevices];
+  const cudaError_t e = raise_smem(decode_paged_kernel<kF16, D, NT>, smem, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_after(decode_paged_kernel<kF16, D, NT>, dim3(shares), kThreads, smem, stream, p);
+}
+
+template <bool kF16, int D>
+cudaError_t launch_both(const DecodeParams& p, int shares, float* weights, int64_t ld_w_batch, int64_t ld_w_head,
+                        cudaStream_t stream) {
+  const cudaError_t e = p.block_heads == 8 ? launch_shape<kF16, D, 1>(p, shares, stream) : launch_shape<kF16, D, 2>(p, shares, stream);
+  return e != cudaSuccess || p.state_o ? e : launch_finish<kF16, D>(p, shares, weights, ld_w_batch, ld_w_head, stream);
+}
+
+cudaError_t launch_decode(const DecodeParams& p, bool f16, int D, int shares, float* weights, int64_t ld_w_batch,
+                          int64_t ld_w_head, cudaStream_t stream) {
+  if (D == 128)
+    return f16 ? launch_both<true, 128>(p, shares, weights, ld_w_batch, ld_w_head, stream)
+               : launch_both<false, 128>(p, shares, weights, ld_w_batch, ld_w_head, stream);
+  return f16 ? launch_both<true, 64>(p, shares, weights, ld_w_batch, ld_w_head, stream)
+             : launch_both<false, 64>(p, shares, weights, ld_w_batch, ld_w_head, stream);
+}
+
+}  // namespace
+
+namespace decode {
+
+bool make_plan(int H, const os_paged_cache& c, int ctas_per_sm, bool weights, Plan* out) {
   const int sms = device_sms();
   if (sms < 1) return false;
   const int group = H / c.heads;
   Plan pl;
-  pl.shares = sms * kCtasPerSm;
-  pl.block_heads = group <= 8 ? 8 : kMaxHeadBlock;
+  pl.shares = sms * ctas_per_sm;
+  pl.block_heads = heads_of_block(group);
   pl.head_blocks = (group + pl.block_heads - 1) / pl.block_heads;
   pl.score_heads = pl.head_blocks > 1 ? pl.block_heads : (group + 3) / 4 * 4;
   const int64_t capacity = static_cast<int64_t>(c.max_pages) * c.page_size;
@@ -753,59 +576,16 @@ bool make_plan(int H, const os_paged_cache& c, bool weights, Plan* out) {
   return true;
 }
 
-template <bool kF16, int D, int NT>
-cudaError_t launch_shape(const DecodeParams& p, int shares, float* weights, int64_t ld_w_batch, int64_t ld_w_head,
-                         cudaStream_t stream) {
-  constexpr int smem = Shape<D>::kSmemBytes;
-  // the kernel's shared-memory limit, raised once per device
-  constexpr int kMaxDevices = 64;
-  static std::atomic<bool> smem_set[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices || !smem_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(decode_paged_kernel<kF16, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices) smem_set[dev].store(true, std::memory_order_release);
-  }
-  if ((e = launch_after(decode_paged_kernel<kF16, D, NT>, dim3(shares), kThreads, smem, stream, p)) != cudaSuccess) return e;
-  const int64_t joins = p.unit_tiles == kUnitTiles ? static_cast<int64_t>(shares) * p.block_heads : 0;
-  const int64_t chunks = weights ? ((static_cast<int64_t>(p.c.max_pages) << p.c.page_shift) + kAddKeys - 1) / kAddKeys : 0;
-  const int64_t adds = chunks * p.c.heads * p.c.batch, ctas = adds + joins;
-  if (ctas > 0x7fffffff) return cudaErrorNotSupported;
-  if (ctas == 0) return cudaSuccess;
-  return launch_after(decode_finish_kernel<kF16, D>, dim3(static_cast<unsigned>(ctas)), kFinishThreads, 0, stream, p,
-                      static_cast<int>(adds), static_cast<int>(chunks), weights, ld_w_batch, ld_w_head);
-}
-
-template <bool kF16, int D>
-cudaError_t launch_heads(const DecodeParams& p, int shares, float* weights, int64_t ld_w_batch, int64_t ld_w_head,
-                         cudaStream_t stream) {
-  return p.block_heads == 8 ? launch_shape<kF16, D, 1>(p, shares, weights, ld_w_batch, ld_w_head, stream)
-                            : launch_shape<kF16, D, 2>(p, shares, weights, ld_w_batch, ld_w_head, stream);
-}
-
-}  // namespace
-
-int64_t decode_paged_workspace_bytes(int H, const os_paged_cache& cache, bool weights) {
-  Plan pl;
-  return make_plan(H, cache, weights, &pl) ? pl.bytes : -1;
-}
-
-cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
-                                const os_paged_cache& cache, float scale, uint16_t* o, float* lse,
-                                float* weights, int64_t ld_w_batch, int64_t ld_w_head,
-                                void* workspace, unsigned int* err, cudaStream_t stream) {
-  Plan pl;
-  if (!make_plan(H, cache, weights != nullptr, &pl)) return cudaErrorInvalidDevice;
+DecodeParams decode_params(const Plan& pl, const PagedCache& c, const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head,
+                           int H, float scale, uint16_t* o, float* lse, void* workspace, unsigned int* err) {
   char* ws = static_cast<char*>(workspace);
-  DecodeParams p;
-  p.c = paged_cache(cache);
+  DecodeParams p = {};
+  p.c = c;
   p.q = q;
   p.ld_q_batch = ld_q_batch;
   p.ld_q_head = ld_q_head;
   p.H = H;
-  p.group = H / cache.heads;
+  p.group = H / c.heads;
   p.head_blocks = pl.head_blocks;
   p.block_heads = pl.block_heads;
   p.unit_tiles = pl.whole ? kWholeKeysMany / kTileKeys : kUnitTiles;
@@ -816,16 +596,37 @@ cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t l
   p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
   p.meta = reinterpret_cast<int4*>(ws + pl.meta);
-  p.lse2 = reinterpret_cast<float*>(ws + pl.lse2);
-  p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
-  p.scores = weights ? reinterpret_cast<float*>(ws + pl.scores) : nullptr;
   p.err = err;
-  const bool f16 = cache.dtype == OS_DTYPE_F16;
-  if (cache.head_dim == 128)
-    return f16 ? launch_heads<true, 128>(p, pl.shares, weights, ld_w_batch, ld_w_head, stream)
-               : launch_heads<false, 128>(p, pl.shares, weights, ld_w_batch, ld_w_head, stream);
-  return f16 ? launch_heads<true, 64>(p, pl.shares, weights, ld_w_batch, ld_w_head, stream)
-             : launch_heads<false, 64>(p, pl.shares, weights, ld_w_batch, ld_w_head, stream);
+  return p;
+}
+
+cudaError_t launch_join(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream) {
+  if (D == 128)
+    return f16 ? launch_finish<true, 128>(p, shares, nullptr, 0, 0, stream) : launch_finish<false, 128>(p, shares, nullptr, 0, 0, stream);
+  return f16 ? launch_finish<true, 64>(p, shares, nullptr, 0, 0, stream) : launch_finish<false, 64>(p, shares, nullptr, 0, 0, stream);
+}
+
+}  // namespace decode
+
+int64_t decode_paged_workspace_bytes(int H, const os_paged_cache& cache, bool weights) {
+  Plan pl;
+  return make_plan(H, cache, kCtasPerSm, weights, &pl) ? pl.bytes : -1;
+}
+
+cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
+                                const os_paged_cache& cache, float scale, uint16_t* o, float* lse,
+                                float* weights, int64_t ld_w_batch, int64_t ld_w_head,
+                                void* workspace, unsigned int* err, cudaStream_t stream) {
+  Plan pl;
+  if (!make_plan(H, cache, kCtasPerSm, weights != nullptr, &pl)) return cudaErrorInvalidDevice;
+  DecodeParams p = decode_params(pl, paged_cache(cache), q, ld_q_batch, ld_q_head, H, scale, o, lse, workspace, err);
+  if (weights) {
+    char* ws = static_cast<char*>(workspace);
+    p.lse2 = reinterpret_cast<float*>(ws + pl.lse2);
+    p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
+    p.scores = reinterpret_cast<float*>(ws + pl.scores);
+  }
+  return launch_decode(p, cache.dtype == OS_DTYPE_F16, cache.head_dim, pl.shares, weights, ld_w_batch, ld_w_head, stream);
 }
 
 }  // namespace oss

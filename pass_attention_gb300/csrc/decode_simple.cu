@@ -139,15 +139,6 @@ float base2(float scale) { return static_cast<float>(static_cast<double>(scale) 
 
 }  // namespace
 
-int64_t decode_paged_fp8_workspace_bytes(int, const os_paged_cache&) { return 16; }
-
-cudaError_t launch_decode_paged_fp8(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
-                                    const os_paged_cache_fp8& cache, float scale, uint16_t* o, float* lse, void*,
-                                    unsigned int* err, cudaStream_t stream) {
-  const Params p{paged_cache(cache.pages), fp8_pools(cache), PrefixTables{}, q, ld_q_batch, ld_q_head, H, base2(scale), o, lse, err};
-  return launch<true>(p, cache.pages.dtype == OS_DTYPE_F16, cache.pages.head_dim, stream);
-}
-
 int64_t decode_shared_workspace_bytes(int, const os_paged_cache&, int, int) { return 16; }
 
 cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,

@@ -28,16 +28,6 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
     return make_float2(bf16_lo(w), bf16_hi(w));
 }
 
-template <bool kF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t w;
-  if constexpr (kF16)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  return w;
-}
-
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t w;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(w) : "f"(hi), "f"(lo));
