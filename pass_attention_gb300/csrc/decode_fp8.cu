@@ -56,6 +56,10 @@ struct Shape {
   static constexpr int kSmemBytes = kRingBytes + kScaleRing + kMergeBytes<D>;
 };
 
+// The references before the first key: below every finite score, so that no weight needs
+// a special case (-inf - kNone is -inf still).
+constexpr float kNone = -3.402823466e+38f;
+
 // Byte offset of 16-byte chunk c of row r of a tile, so that eight rows of a chunk
 // touch all banks.
 template <int D>
@@ -88,48 +92,75 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
   float* merge = reinterpret_cast<float*>(smem + S::kRingBytes + S::kScaleRing);
   const int copy_row = lane / kChunks, copy_chunk = lane % kChunks;
 
-  // ---- the loads' cursor: the tile to be loaded next, and its page
+  // ---- the loads' cursor: the tile to be loaded next and its page, and what of its
+  // address the segment decides
   Walk lw = w;
-  int lt = lw.s.r0 * p.unit_tiles + warp;
+  int lt, lt_end;
   bool more = true;
   int page = 0;
+  const int32_t* row;
+  int64_t head_at, scale_at;
+  const int64_t lane_at = copy_row * p.c.ld_slot + copy_chunk * 16, copy_step = kRowsPerCopy * p.c.ld_slot;
+  const int slot_mask = (1 << p.c.page_shift) - 1;
+  auto enter = [&]() {
+    const int g = lw.s.j / p.head_blocks;
+    lt = lw.s.r0 * p.unit_tiles + warp;
+    lt_end = lw.tile_end(p);
+    row = p.c.table + static_cast<int64_t>(lw.s.b) * p.c.ld_table;
+    head_at = g * p.c.ld_head + lane_at;
+    scale_at = g * f.ld_head;
+  };
   auto settle = [&]() {  // move to the next tile that exists, fetch its page number
-    while (lt >= lw.tile_end(p)) {
+    while (lt >= lt_end) {
       if (!(more = lw.next(p))) return;
-      lt = lw.s.r0 * p.unit_tiles + warp;
+      enter();
     }
-    page = p.c.table[static_cast<int64_t>(lw.s.b) * p.c.ld_table + ((lt * kTileKeys) >> p.c.page_shift)];
+    page = row[(lt * kTileKeys) >> p.c.page_shift];
   };
   uint32_t bad = 0;  // stages whose tile has a page outside the pool
   auto load = [&](int stage) {
     if (more) {
-      const int key0 = lt * kTileKeys;
-      const bool ok = page_ok(page, p.c.num_pages);
-      if (!ok) report_error(p.err, kKernelPaged | (kSiteBadPage << 8));
-      bad = (bad & ~(1u << stage)) | (ok ? 0u : 1u << stage);
-      const int g = lw.s.j / p.head_blocks, slot0 = key0 & ((1 << p.c.page_shift) - 1);
-      const int64_t at = ok ? pool_offset(page, g, slot0 + copy_row, p.c.ld_page, p.c.ld_head, p.c.ld_slot) + copy_chunk * 16
-                            : 0;
-      const int rows = ok ? lw.s.len - key0 : 0;  // rows of the tile that hold a token
-      const uint32_t dst = ring + stage * 2 * S::kTileBytes;
+      const int key0 = lt * kTileKeys, slot0 = key0 & slot_mask;
+      const int rows = lw.s.len - key0;  // rows of the tile that hold a token
+      const uint32_t dst = ring + stage * 2 * S::kTileBytes + chunk_at<D>(copy_row, copy_chunk);
+      const uint32_t sc = smem_u32(scale_ring) + stage * S::kScaleBytes + lane * kTileKeys;
+      // (rows kRowsPerCopy apart have the same swizzle but in D 128's second four of eight)
+      auto at_copy = [&](int i) { return D == 128 && (i & 1) ? (dst ^ 64) + i * kRowsPerCopy * D : dst + i * kRowsPerCopy * D; };
+      bad &= ~(1u << stage);
+      if (page_ok(page, p.c.num_pages)) {
+        const int64_t at = static_cast<int64_t>(page) * p.c.ld_page + head_at + slot0 * p.c.ld_slot;
+        const uint8_t *k = f.k + at, *v = f.v + at;
+        if (rows >= kTileKeys) {
 #pragma unroll
-      for (int i = 0; i < kTileKeys / kRowsPerCopy; ++i) {
-        const int r = i * kRowsPerCopy + copy_row;
-        const bool there = r < rows;
-        const int64_t src = there ? at + i * kRowsPerCopy * p.c.ld_slot : 0;
-        const uint32_t d = dst + chunk_at<D>(r, copy_chunk);
-        copy16(d, f.k + src, there);
-        copy16(d + S::kTileBytes, f.v + src, there);
-      }
-      if (lane < 2) {
-        const int64_t sc = ok ? pool_offset(page, g, slot0, f.ld_page, f.ld_head, 1) : 0;
-        copy16(smem_u32(scale_ring) + stage * S::kScaleBytes + lane * kTileKeys, (lane ? f.v_scales : f.k_scales) + sc, ok);
+          for (int i = 0; i < kTileKeys / kRowsPerCopy; ++i, k += copy_step, v += copy_step) {
+            copy16(at_copy(i), k);
+            copy16(at_copy(i) + S::kTileBytes, v);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTileKeys / kRowsPerCopy; ++i) {
+            const bool there = i * kRowsPerCopy + copy_row < rows;
+            copy16(at_copy(i), there ? k + i * copy_step : f.k, there);
+            copy16(at_copy(i) + S::kTileBytes, there ? v + i * copy_step : f.v, there);
+          }
+        }
+        if (lane < 2) copy16(sc, (lane ? f.v_scales : f.k_scales) + page * f.ld_page + scale_at + slot0);
+      } else {
+        report_error(p.err, kKernelPaged | (kSiteBadPage << 8));
+        bad |= 1u << stage;
+#pragma unroll
+        for (int i = 0; i < kTileKeys / kRowsPerCopy; ++i) {
+          copy16(at_copy(i), f.k, false);
+          copy16(at_copy(i) + S::kTileBytes, f.v, false);
+        }
+        if (lane < 2) copy16(sc, f.k_scales, false);
       }
       lt += kUnitTiles;
       settle();
     }
     copy_commit();
   };
+  enter();
   settle();
 #pragma unroll 1
   for (int i = 0; i < kStages; ++i) load(i);
@@ -187,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
     float od[NT][D / 16][4];    // dims 16 i + 2 row8 (+ 1), the same heads
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = mo[nt][0] = mo[nt][1] = neg_inf();
+      m[nt][0] = m[nt][1] = mo[nt][0] = mo[nt][1] = kNone;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -222,21 +253,27 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
       }
       const float ka = __shfl_sync(0xffffffffu, sv, row8), kb = __shfl_sync(0xffffffffu, sv, row8 + 8);
       const float va = __shfl_sync(0xffffffffu, sv, row8 + 16), vb = __shfl_sync(0xffffffffu, sv, row8 + 24);
-      const int key = t * kTileKeys + row8;
-      const bool masked = (bad >> stage) & 1u;
-      const bool live_a = key < s.len && !masked, live_b = key + 8 < s.len && !masked;
       float x[NT][4], y[NT][4];  // scores in base 2, and with the value's exponent
       bool rise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool live = e < 2 ? live_a : live_b;
-          const float z = (sc[nt][0][e] + sc[nt][1][e]) * qs[nt][e & 1] * (e < 2 ? ka : kb);
-          x[nt][e] = live ? z : neg_inf();
-          y[nt][e] = live ? z + (e < 2 ? va : vb) : neg_inf();
-          rise |= x[nt][e] > m[nt][e & 1] + kSlack || y[nt][e] > mo[nt][e & 1] + kSlack;
+          x[nt][e] = (sc[nt][0][e] + sc[nt][1][e]) * qs[nt][e & 1] * (e < 2 ? ka : kb);
+          y[nt][e] = x[nt][e] + (e < 2 ? va : vb);
         }
+      if (t * kTileKeys + kTileKeys > s.len || bad) {  // some tile has a bad page, perhaps this one
+        const int live = (bad >> stage) & 1u ? 0 : s.len - t * kTileKeys;  // its rows that hold a token
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (row8 + (e < 2 ? 0 : 8) >= live) x[nt][e] = y[nt][e] = neg_inf();
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rise |= x[nt][e] > m[nt][e & 1] + kSlack || y[nt][e] > mo[nt][e & 1] + kSlack;
       if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -251,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
             }
             mx = fmaxf(mx, m[nt][e]);
             my = fmaxf(my, mo[nt][e]);
-            l[nt][e] *= mx == neg_inf() ? 1.f : ex2(m[nt][e] - mx);
-            corr[e] = my == neg_inf() ? 1.f : ex2(mo[nt][e] - my);
+            l[nt][e] *= ex2(m[nt][e] - mx);
+            corr[e] = ex2(mo[nt][e] - my);
             m[nt][e] = mx;
             mo[nt][e] = my;
           }
@@ -268,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
         float pe[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          l[nt][e & 1] += ex2(x[nt][e] - reference(m[nt][e & 1]));
-          pe[e] = ex2(y[nt][e] - reference(mo[nt][e & 1]));
+          l[nt][e & 1] += ex2(x[nt][e] - m[nt][e & 1]);
+          pe[e] = ex2(y[nt][e] - mo[nt][e & 1]);
         }
         pf[nt][0] = transpose8x8(pack2<true>(pe[0], pe[1]));
         pf[nt][1] = transpose8x8(pack2<true>(pe[2], pe[3]));
@@ -301,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
-        to[e] = ex2(0.5f * (reference(mo[nt][e]) - reference(m[nt][e])));
+        to[e] = ex2(0.5f * (mo[nt][e] - m[nt][e]));
       }
       float* mine = merge + warp * 8 * kMergeLd<D>;
 #pragma unroll

@@ -9,6 +9,9 @@
     python -m pass_attention_gb300.profile_case packed [--B --H --Hkv --S] [--reps N]
     python -m pass_attention_gb300.profile_case paged [--B --H --Hkv --Lmax] [--weights] [--reps N]
     python -m pass_attention_gb300.profile_case evict [--B --Hkv --Lmax] [--reps N]
+    python -m pass_attention_gb300.profile_case paged8 [--B --H --Hkv --Lmax --D] [--reps N]
+    python -m pass_attention_gb300.profile_case append8|read8 [--B --Hkv --Lmax --D] [--reps N]
+    python -m pass_attention_gb300.profile_case shared [--B --H --Hkv --S --Lmax --D] [--reps N]
 
 ``merge`` runs the split-KV decode once and then the merge ``--reps`` times on
 its partials: the merge's inputs are the decode's (B, H, splits) partial
@@ -18,6 +21,9 @@ merge launch with little memory held.
 ``packed``, ``paged`` and ``evict`` run ``attention_fwd_packed`` (causal),
 ``attention_decode_paged`` and ``kv_cache_evict`` (to an eighth) on B sequences
 whose lengths spread evenly up to S or Lmax, head dimension 128, pages of 16.
+``paged8``, ``append8`` and ``read8`` run ``attention_decode_paged_fp8``,
+``kv_cache_append_fp8`` and ``kv_cache_read_fp8`` on such sequences, ``shared``
+``attention_decode_shared`` on them behind one prefix of S tokens.
 
 ``--no-ws`` calls ``os_softmax_rows`` / ``os_softmax_rows_16bit`` without a
 workspace, so rows over 1.6 MB take the kernels that stream them twice from
@@ -90,16 +96,54 @@ def _cache_case(a):
     print("tokens", sum(lens))
 
 
+def _cache8_case(a):
+    B, H, page, d = a.B or 8, a.H or 32, 16, a.D
+    lens = [max(1, a.Lmax * (b + 1) // B) for b in range(B)]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    draw = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    columns, prefix = -(-a.Lmax // page), -(-a.S // page) if a.case == "shared" else 0
+    pages = B * columns + prefix
+    order = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+    table, kv_len, q = order[:B * columns].view(B, columns), ints(lens), draw(B, H, d)
+    if a.case == "shared":
+        kp, vp = draw(pages, a.Hkv, page, d), draw(pages, a.Hkv, page, d)
+        prefix_table, prefix_len = order[None, B * columns:], ints([a.S])
+        call = lambda: oss.attention_decode_shared(q, kp, vp, prefix_table, prefix_len, table, kv_len)  # noqa: E731
+    else:
+        cu, total = ints([sum(lens[:b]) for b in range(B + 1)]), sum(lens)
+        kp, vp = (torch.zeros((pages, a.Hkv, page, d), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+                  for _ in range(2))
+        ks, vs = (torch.zeros((pages, a.Hkv, page), dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+                  for _ in range(2))
+        k, v = draw(total, a.Hkv, d), draw(total, a.Hkv, d)
+        cache = (kp, vp, ks, vs, table, kv_len)
+        oss.kv_cache_append_fp8(k, v, *cache, cu)
+        if a.case == "append8":
+            call = lambda: oss.kv_cache_append_fp8(k, v, *cache, cu)  # noqa: E731
+        elif a.case == "read8":
+            call = lambda: oss.kv_cache_read_fp8(*cache, cu, total, k=k, v=v)  # noqa: E731
+        else:
+            call = lambda: oss.attention_decode_paged_fp8(q, *cache)  # noqa: E731
+    for _ in range(a.reps):
+        call()
+        torch.cuda.synchronize()
+    oss.check_device_error()
+    print("tokens", sum(lens))
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["softmax", "softmax16", "multipass", "attn", "decode", "merge",
-                                     "packed", "paged", "evict"])
+                                     "packed", "paged", "evict", "paged8", "append8", "read8", "shared"])
     ap.add_argument("--passes", type=int, default=3)
     ap.add_argument("--rows", type=int, default=32768)
     ap.add_argument("--cols", type=int, default=8192)
     ap.add_argument("--B", type=int, default=None)
     ap.add_argument("--H", type=int, default=None)
     ap.add_argument("--Hkv", type=int, default=8)
+    ap.add_argument("--D", type=int, choices=[64, 128], default=128)
     ap.add_argument("--S", type=int, default=4096)
     ap.add_argument("--Lmax", type=int, default=32768)
     ap.add_argument("--splits", type=int, default=16)
@@ -144,6 +188,8 @@ def main(argv=None):
         oss.check_device_error()
     elif a.case in ("packed", "paged", "evict"):
         _cache_case(a)
+    elif a.case in ("paged8", "append8", "read8", "shared"):
+        _cache8_case(a)
     elif a.case == "merge":
         B, H = a.B or 64, a.H or 32
         q, k, v, kv = workloads.decode_inputs(B, H, a.Lmax, 128, seed=4, device="cuda")
