@@ -95,6 +95,16 @@ struct Smem {
   static constexpr int kBytes = kOffV + kScores * kTile + 1024;  // + alignment slack
 };
 
+// What the prefix kernels read and write beside the others' parameters: KV tiles come
+// from pages, and states go to a join with the sequences' own tokens.
+struct PrefixOut {
+  PrefixTables tables;
+  int32_t num_pages, page_shift, box_shift;  // a TMA box: 2^box_shift slots of a page
+  int4* where;      // [tokens_q][packs]: {share, parts (0: not cut), row of the first head in the tile}
+  float* state_o;   // [tokens_q][Hq][D]: unnormalised O of items that are not cut
+  float2* state_ml;  // [tokens_q][Hq]
+};
+
 struct PackedParams {
   uint16_t* o;
   float* lse;
@@ -109,6 +119,7 @@ struct PackedParams {
   float4* part_o;   // [2 shares][D / 4][128 rows]: unnormalised O, 4 dims of a row
   float2* part_ml;  // [2 shares][128 rows]: base-2 m, l
   int4* meta;       // [shares]: {parts, first query row, queries, pack} of the item cut at its end
+  PrefixOut prefix;  // of the prefix kernels
 };
 
 // Bounded wait, small: it is inlined some twenty times, the step and hand-over
@@ -205,18 +216,26 @@ struct Shares {
   ShareCut cut;
 };
 
+// (Prefix: sequence b is a group, its keys the group's prefix.)
+template <bool kPrefix>
 __device__ __forceinline__ PackedSeq load_seq(const PackedParams& p, int b) {
+  if constexpr (kPrefix) {
+    const PrefixTables& t = p.prefix.tables;
+    const RowRange q = p.cu_q ? row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q) : RowRange{0, p.tokens_q, false};
+    return packed_seq(q, RowRange{0, paged_length(t.len[b], t.max_pages, p.prefix.page_shift), false}, p.pos_shift);
+  }
   return packed_seq(row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q),
                     row_range(p.cu_k[b], p.cu_k[b + 1], p.tokens_k), p.pos_shift);
 }
 
 // Length of the items of sequences [b0, b1), in one pack, and their tiles.
+template <bool kPrefix>
 __device__ __forceinline__ int64_t run_length(const PackedParams& p, int b0, int b1, uint32_t* tiles) {
   int64_t sum = 0;
   uint32_t n = 0;
   OSS_ROLLED
   for (int b = b0; b < b1; ++b) {
-    const PackedSeq s = load_seq(p, b);
+    const PackedSeq s = load_seq<kPrefix>(p, b);
     sum += length_before(s, s.tiles, p.pos_shift, p.causal != 0);
     n += static_cast<uint32_t>(s.tiles);
   }
@@ -243,6 +262,7 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x) {
 // launch; rolled loops, because code that runs once is paid for in instruction
 // fetches.)
 static_assert(2 * kMaxRounds <= kThreads / 32, "a warp for every boundary");
+template <bool kPrefix>
 __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, int64_t* scratch /* [kThreads / 32] */, uint32_t* tile_scratch) {
   constexpr int kWarps = kThreads / 32;
   constexpr uint32_t kAll = 0xffffffffu;
@@ -259,13 +279,14 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
     // the lanes' runs of [lo, hi)
     const int per = (hi - lo + 31) / 32;
     const int b0 = min(hi, lo + lane * per), b1 = min(hi, b0 + per);
-    sum = run_length(p, b0, b1, &tiles);
+    sum = run_length<kPrefix>(p, b0, b1, &tiles);
     const int64_t upto = warp_scan(sum);
     if (level == 0) {
       if (blockIdx.x == 0) {
         OSS_ROLLED
         for (int b = b0; b < b1; ++b)
-          if (row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q).clamped || row_range(p.cu_k[b], p.cu_k[b + 1], p.tokens_k).clamped)
+          if ((!kPrefix || p.cu_q) && (row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q).clamped ||
+                                       (!kPrefix && row_range(p.cu_k[b], p.cu_k[b + 1], p.tokens_k).clamped)))
             report_error(p.err, kKernelPaged | (kSiteBadOffsets << 8));
       }
       tiles = __reduce_add_sync(kAll, tiles);
@@ -306,7 +327,7 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
     const int64_t len = __shfl_sync(kAll, sum, k);
     const int pack = small_quotient(at - before, len);
     before += pack * len;
-    const PackedSeq s = load_seq(p, lo);
+    const PackedSeq s = load_seq<kPrefix>(p, lo);
     int tile = 0;
     int64_t stride = 1;
     while (stride * 32 < s.tiles) stride *= 32;
@@ -336,7 +357,7 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
 // A piece of an item: KV steps [s0, s1) of its n_kv.
 struct Unit {
   int q_row, n_pos;       // first query row, queries of the tile
-  int k_row, k_len, vis;  // first key row, keys, keys that the tile's first query sees
+  int k_row, k_len, vis;  // first key row (or row of the prefix table), keys, keys that the tile's first query sees
   int n_kv, n_diag, s0, s1, pack, share;
   int parts;              // parts of the item, if it begins here and is cut
   int end;                // no unit: the shares are done
@@ -354,6 +375,7 @@ struct Walk {
     w = end_w = 0;
     end_step = 0;
   }
+  template <bool kPrefix>
   __device__ __forceinline__ bool next(const PackedParams& p, const Shares& sh, Unit& u) {
     const bool causal = p.causal != 0;
     OSS_ROLLED
@@ -375,7 +397,7 @@ struct Walk {
         fetch = false;
         OSS_ROLLED
         do {
-          s = load_seq(p, ++seq);
+          s = load_seq<kPrefix>(p, ++seq);
         } while (s.tiles == 0 && seq + 1 < p.batch);
       }
       const int steps = kv_tiles(s, tile, p.pos_shift, causal);
@@ -385,7 +407,7 @@ struct Walk {
         const int pos0 = tile << p.pos_shift;
         u.q_row = s.q_start + pos0;
         u.n_pos = min(1 << p.pos_shift, s.q_len - pos0);
-        u.k_row = s.k_start;
+        u.k_row = kPrefix ? seq : s.k_start;
         u.k_len = s.k_len;
         u.vis = visible_keys(s, pos0, causal);
         u.n_kv = steps;
@@ -435,7 +457,39 @@ __device__ __forceinline__ int64_t out_row(const PackedParams& p, int q_row, int
   return static_cast<int64_t>(q_row + (r >> head_shift)) * p.Hq + (pack << head_shift) + (r & ((1 << head_shift) - 1));
 }
 
-template <int D, bool kF16>
+constexpr int kBadRing = 8;  // steps whose masks of bad pages are kept: no reader is more than 4 behind
+
+// A prefix's KV tile comes in pieces of 2^box_shift rows, a lane's each: its page, or
+// num_pages (a box outside the pool: zeros) for pieces behind the last key and bad
+// pages. *bad: a bit for every 16 keys that belong to the prefix and whose page is
+// outside the pool.
+__device__ __forceinline__ int piece_page(const PrefixOut& x, int group, int tile, int k_len, uint32_t* bad) {
+  const int lane = threadIdx.x & 31, key = tile * kBN + (lane << x.box_shift);
+  const bool mine = lane < (kBN >> x.box_shift) && key < k_len;
+  const int page = mine ? x.tables.table[group * x.tables.ld_table + (key >> x.page_shift)] : x.num_pages;
+  const bool ok = page_ok(page, x.num_pages);
+  const uint32_t pieces = __ballot_sync(0xffffffffu, mine && !ok);
+  *bad = __ballot_sync(0xffffffffu, lane < kBN / 16 && ((pieces >> (lane >> (x.box_shift - 4))) & 1u));
+  return ok ? page : x.num_pages;
+}
+
+// Loads this lane's piece of a KV tile (its halves of 64 dims) to `dst`, when the
+// barrier knows of the tile's bytes.
+template <int D>
+__device__ __forceinline__ void load_piece(const PrefixOut& x, const CUtensorMap* map, uint32_t dst, uint32_t bar, int page,
+                                           int head, int tile) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) mbar_expect_tx(bar, (D / 64) * kHalf);
+  __syncwarp();
+  if (lane < (kBN >> x.box_shift)) {
+    const int slot = (tile * kBN) & ((1 << x.page_shift) - 1);  // 0 for pages of a tile or less
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) tma_load_4d(dst + h * kHalf + (lane << (x.box_shift + 7)), map, bar, h * 64, slot, head, page);
+  }
+  __syncwarp();
+}
+
+template <int D, bool kF16, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const PackedParams p) {
@@ -450,6 +504,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   __shared__ Unit units[kUnits];
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag_s;
+  __shared__ uint32_t bad_keys[kBadRing];  // of the steps' KV tiles (prefix)
   volatile int* abort_flag = &abort_flag_s;
   let_next_kernel_start();
 
@@ -494,8 +549,8 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     tc_fence_before();
   }
   wait_for_previous_kernel();
-  if (threadIdx.x < p.rounds) p.meta[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
-  find_shares(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
+  if (!kPrefix && threadIdx.x < p.rounds) p.meta[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
+  find_shares<kPrefix>(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
   tc_fence_after();
   const uint32_t tbase = tmem_base_slot;
 
@@ -523,7 +578,92 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   };
   if (warp >= kProducerWarp && warp < kEpiWarp)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-  if (warp == kProducerWarp) {
+  if (kPrefix && warp == kProducerWarp) {
+    // ------------------------------------------- the same as below, with K in pieces
+    // Lane 0 walks; every lane has a piece of the tile. A lane's page number is on its way
+    // while the warp waits for the stage.
+    Ring<kKStages> rk;
+    Ring<kScores> sk;
+    Walk walk;
+    walk.begin();
+    int kt = 0, g = 0;
+    bool ok = true;
+    OSS_ROLLED
+    for (;; ++kt) {
+      const int slot = kt % kUnits, buf = kt & 1;
+      if (kt >= kUnits && !__all_sync(0xffffffffu, wait_bar(smem_addr(&bars.unit_free[slot]), (kt / kUnits - 1) & 1, kSiteUnitFree))) break;
+      if (lane == 0) {
+        Unit u;
+        u.end = 1;
+        walk.next<kPrefix>(p, shares, u);
+        units[slot] = u;
+        mbar_arrive(smem_addr(&bars.unit_full[slot]));
+      }
+      __syncwarp();
+      const Unit u = units[slot];
+      if (u.end) break;
+      const uint32_t qb = smem_addr(&bars.q_full[buf]);
+      if (kt >= kKStages && !__all_sync(0xffffffffu, wait_bar(smem_addr(&bars.q_free[buf]), ((kt >> 1) - 1) & 1, kSiteQEmpty))) break;
+      if (lane == 0) {
+        mbar_expect_tx(qb, L::kTile);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          tma_load_4d(sbase + L::kOffQ + buf * L::kTile + h * kHalf, &tmap_q, qb, h * 64, 0, u.pack, u.q_row);
+      }
+      const int head = u.pack / p.packs_per_key_head;
+      OSS_ROLLED
+      for (int j = u.s0; j < u.s1; ++j, ++g, rk.next()) {
+        uint32_t bad;
+        const int tile = kv_tile(u, j), page = piece_page(p.prefix, u.k_row, tile, u.k_len, &bad);
+        if (g >= kKStages) {
+          if (!(ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.s_full[sk.at]), sk.phase, kSiteKEmpty)))) break;
+          sk.next();
+        }
+        if (lane == 0) {
+          bad_keys[g % kBadRing] = bad;
+          if (bad) report_error(p.err, kKernelPaged | (kSiteBadPage << 8));
+        }
+        load_piece<D>(p.prefix, &tmap_k, sbase + L::kOffK + rk.at * L::kTile, smem_addr(&bars.k_full[rk.at]), page, head, tile);
+      }
+      if (!ok) {
+        ++kt;  // its Q load has been issued
+        break;
+      }
+    }
+    if (lane == 0) {
+      OSS_ROLLED
+      for (int i = max(0, kt - kKStages); i < kt; ++i)
+        drain_phase(smem_addr(&bars.q_full[i & 1]), (i >> 1) & 1, abort_flag);
+      OSS_ROLLED
+      for (int i = max(0, g - kKStages); i < g; ++i)
+        drain_phase(smem_addr(&bars.k_full[i & 1]), (i >> 1) & 1, abort_flag);
+    }
+  } else if (kPrefix && warp == kVWarp) {
+    Ring<kScores> r;
+    Unit u;
+    int g = 0, skipped = -1;
+    bool ok = true;
+    OSS_ROLLED
+    for (int kt = 0; ok && take_unit_warp(kt, u); ++kt) {
+      const int head = u.pack / p.packs_per_key_head;
+      OSS_ROLLED
+      for (int j = u.s0; j < u.s1; ++j, ++g, r.next()) {
+        uint32_t bad;
+        const int tile = kv_tile(u, j), page = piece_page(p.prefix, u.k_row, tile, u.k_len, &bad);
+        if (g >= kScores && !(ok = __all_sync(0xffffffffu, wait_bar(smem_addr(&bars.o_done[r.at]), r.phase ^ 1, kSiteVEmpty)))) break;
+        if (g == p.skip_v_step) {
+          skipped = g;  // test hook: this V tile never arrives
+          continue;
+        }
+        load_piece<D>(p.prefix, &tmap_v, sbase + L::kOffV + r.at * L::kTile, smem_addr(&bars.v_full[r.at]), page, head, tile);
+      }
+    }
+    if (lane == 0) {
+      OSS_ROLLED
+      for (int i = max(0, g - kScores); i < g; ++i)
+        if (i != skipped) drain_phase(smem_addr(&bars.v_full[i % kScores]), (i / kScores) & 1, abort_flag);
+    }
+  } else if (warp == kProducerWarp) {
     // ------------------------------------------- walk over the shares, Q and K
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
@@ -542,7 +682,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int slot = kt % kUnits, buf = kt & 1;
         if (kt >= kUnits && !wait_bar(smem_addr(&bars.unit_free[slot]), (kt / kUnits - 1) & 1, kSiteUnitFree)) break;
         u.end = 1;
-        const bool have = walk.next(p, shares, u);
+        const bool have = walk.next<kPrefix>(p, shares, u);
         units[slot] = u;
         mbar_arrive(smem_addr(&bars.unit_full[slot]));
         if (!have) break;
@@ -699,7 +839,36 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (!ok) break;
       tc_fence_after();
       const uint32_t stage = sbase + L::kOffQ + (kt & 1) * L::kTile + (warp - kEpiWarp) * (L::kTile / 4);  // [half][32 rows][128 bytes]
-      if (u.s0 == 0 && u.s1 == u.n_kv) {
+      if (kPrefix && u.s0 == 0) {
+        // where the rows' states lie, for the kernel that joins them with the sequences' own tokens
+        const int at = threadIdx.x - kEpiWarp * 32;
+        if (at < u.n_pos) p.prefix.where[static_cast<int64_t>(u.q_row + at) * p.packs + u.pack] = make_int4(u.share, u.parts, at << head_shift, 0);
+      }
+      if (kPrefix && u.s0 == 0 && u.s1 == u.n_kv) {
+        // The state as it is. 16 rows x 64 dims a load, of which 4 threads store the
+        // 32 bytes of a row's sector.
+        OSS_ROLLED
+        for (int part = 0; part < 2 * kHalves; ++part) {
+          const int half = part & 1, h = part >> 1;
+          uint32_t v[32];
+          tmem_ld16x256_x8(t_o + (static_cast<uint32_t>(16 * half) << 16) + 64 * h, v);
+          tmem_ld_wait(v);
+          if (part == 2 * kHalves - 1) {
+            tc_fence_before();
+            mbar_arrive(smem_addr(&bars.o_free));
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = row0 + 16 * half + 8 * e + (lane >> 2);
+            if ((row >> head_shift) >= u.n_pos) continue;
+            float* dst = p.prefix.state_o + out_row(p, u.q_row, u.pack, row) * D + 64 * h + 2 * (lane & 3);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(__uint_as_float(v[4 * k + 2 * e]), __uint_as_float(v[4 * k + 2 * e + 1]));
+          }
+        }
+        if (((row0 + lane) >> head_shift) < u.n_pos) p.prefix.state_ml[out_row(p, u.q_row, u.pack, row0 + lane)] = ml;
+      } else if (!kPrefix && u.s0 == 0 && u.s1 == u.n_kv) {
         // (a row without keys has O = 0: its weights are zeros and V is finite)
         const float inv = ml.y != 0.f ? 1.0f / ml.y : 0.f;
         OSS_ROLLED
@@ -754,7 +923,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                                  __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
         }
         p.part_ml[slot * kBM + row0 + lane] = ml;
-        if (u.parts > 0 && threadIdx.x == kEpiWarp * 32) p.meta[u.share] = make_int4(u.parts, u.q_row, u.n_pos, u.pack);
+        if (!kPrefix && u.parts > 0 && threadIdx.x == kEpiWarp * 32) p.meta[u.share] = make_int4(u.parts, u.q_row, u.n_pos, u.pack);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next Q tile lands where O's rows were
       __syncwarp();
@@ -775,6 +944,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const float C = p.C;
     bool ok = true;
     Ring<kScores> r, before;  // of this step and of the one before
+    int g = 0;                // steps so far (prefix)
     Unit u;
     OSS_ROLLED
     for (int kt = 0; ok && take_unit_warp(kt, u); ++kt) {
@@ -811,6 +981,14 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
         }
         const int key0 = kv_tile(u, j) * kBN;
+        if constexpr (kPrefix) {
+          const uint32_t bad = bad_keys[g++ % kBadRing];
+          if (bad) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((bad >> (4 * (i >> 4) + ((i >> 2) & 3))) & 1u) sa[i] = sb[i] = neg_inf();
+          }
+        }
         if (key0 + kBN > (p.causal ? u.vis : u.k_len)) {
           const int lim_a = vis_a - key0, lim_b = vis_b - key0;
 #pragma unroll
@@ -1046,7 +1224,7 @@ int round_count(int64_t tokens_k, int Hkv, int D) {
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kPrefix>
 cudaError_t launch_shape(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PackedParams& p,
                          int ctas, cudaStream_t stream) {
   static std::atomic<bool> smem_set[kMaxDevices];
@@ -1054,13 +1232,40 @@ cudaError_t launch_shape(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !smem_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attn_packed_kernel<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    e = cudaFuncSetAttribute(attn_packed_kernel<D, kF16, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) smem_set[dev].store(true, std::memory_order_release);
   }
-  e = launch_after(attn_packed_kernel<D, kF16>, dim3(ctas), kThreads, Smem<D>::kBytes, stream, mq, mk, mv, p);
-  if (e != cudaSuccess) return e;
+  e = launch_after(attn_packed_kernel<D, kF16, kPrefix>, dim3(ctas), kThreads, Smem<D>::kBytes, stream, mq, mk, mv, p);
+  if (e != cudaSuccess || kPrefix) return e;
   return launch_after(attn_packed_join_kernel<D, kF16>, dim3(ctas * p.rounds, D / 32), kJoinThreads, 0, stream, p);
+}
+
+template <bool kPrefix>
+cudaError_t launch_kernel(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PackedParams& p, int D,
+                          bool f16, int ctas, cudaStream_t stream) {
+  if (D == 128)
+    return f16 ? launch_shape<128, true, kPrefix>(mq, mk, mv, p, ctas, stream) : launch_shape<128, false, kPrefix>(mq, mk, mv, p, ctas, stream);
+  return f16 ? launch_shape<64, true, kPrefix>(mq, mk, mv, p, ctas, stream) : launch_shape<64, false, kPrefix>(mq, mk, mv, p, ctas, stream);
+}
+
+// Query positions of a tile whose rows hold `heads` heads each, as a shift.
+int tile_positions(int heads) {
+  int pos_shift = 7;
+  while ((kBM >> pos_shift) < heads) --pos_shift;
+  return pos_shift;
+}
+
+bool make_q_map(CUtensorMap* map, const uint16_t* q, bool f16, int D, int H, int heads, int64_t tokens, int64_t ld_head,
+                int64_t ld_token) {
+  const int64_t dims[4] = {D, heads, H / heads, tokens}, strides[3] = {ld_head, ld_head * heads, ld_token};
+  const int box[4] = {64, heads, 1, kBM / heads};
+  return make_map(map, q, f16, 4, dims, strides, box);
+}
+
+uint32_t wait_limit(const AttnFault& fault) {
+  const uint64_t timeout_ns = fault.timeout_ns > 0 ? static_cast<uint64_t>(fault.timeout_ns) : kTimeoutNs;
+  return static_cast<uint32_t>(timeout_ns < kTimeoutNs ? timeout_ns * 2 : kTimeoutNs * 2);  // about 2 GHz
 }
 
 }  // namespace
@@ -1087,24 +1292,18 @@ cudaError_t launch_attn_packed(const PackedArgs& a, void* workspace, unsigned in
   const int sms = device_sms();
   if (sms < 1) return cudaErrorInvalidDevice;
   const int group = a.Hq / a.Hkv, heads = pack_heads(group);
-  int pos_shift = 7;
-  while ((kBM >> pos_shift) < heads) --pos_shift;
-
   CUtensorMap mq, mk, mv;
-  const int64_t q_dims[4] = {a.D, heads, a.Hq / heads, a.tokens_q};
-  const int64_t q_strides[3] = {a.ld_q_head, a.ld_q_head * heads, a.ld_q_token};
-  const int q_box[4] = {64, heads, 1, kBM / heads};
   // without keys nothing of k and v is read: any mapped row stands in for them
   const bool keys = a.tokens_k > 0;
   const int64_t k_dims[3] = {a.D, keys ? a.Hkv : 1, keys ? a.tokens_k : 1};
   const int64_t k_strides[2] = {a.ld_kv_head, a.ld_kv_token};
   const int k_box[3] = {64, 1, kBN};
-  if (!make_map(&mq, a.q, a.f16, 4, q_dims, q_strides, q_box) ||
+  if (!make_q_map(&mq, a.q, a.f16, a.D, a.Hq, heads, a.tokens_q, a.ld_q_head, a.ld_q_token) ||
       !make_map(&mk, keys ? a.k : a.q, a.f16, 3, k_dims, k_strides, k_box) ||
       !make_map(&mv, keys ? a.v : a.q, a.f16, 3, k_dims, k_strides, k_box))
     return cudaErrorInvalidValue;
 
-  PackedParams p;
+  PackedParams p = {};
   p.o = a.o;
   p.lse = a.lse;
   p.cu_q = a.cu_q;
@@ -1115,13 +1314,12 @@ cudaError_t launch_attn_packed(const PackedArgs& a, void* workspace, unsigned in
   p.Hq = a.Hq;
   p.packs = a.Hq / heads;
   p.packs_per_key_head = group / heads;
-  p.pos_shift = pos_shift;
+  p.pos_shift = tile_positions(heads);
   p.rounds = round_count(a.tokens_k, a.Hkv, a.D);
   p.C = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634074);
   p.causal = a.causal ? 1 : 0;
   p.err = err;
-  const uint64_t timeout_ns = fault.timeout_ns > 0 ? static_cast<uint64_t>(fault.timeout_ns) : kTimeoutNs;
-  p.wait_cycles = static_cast<uint32_t>(timeout_ns < kTimeoutNs ? timeout_ns * 2 : kTimeoutNs * 2);  // about 2 GHz
+  p.wait_cycles = wait_limit(fault);
   p.skip_v_step = fault.skip_v_step;
   const int64_t shares = static_cast<int64_t>(sms) * p.rounds;
   char* ws = static_cast<char*>(workspace);
@@ -1130,9 +1328,72 @@ cudaError_t launch_attn_packed(const PackedArgs& a, void* workspace, unsigned in
   p.part_ml = reinterpret_cast<float2*>(ws);
   ws += round256(2 * shares * kBM * 8);
   p.meta = reinterpret_cast<int4*>(ws);
-  if (a.D == 128)
-    return a.f16 ? launch_shape<128, true>(mq, mk, mv, p, sms, stream) : launch_shape<128, false>(mq, mk, mv, p, sms, stream);
-  return a.f16 ? launch_shape<64, true>(mq, mk, mv, p, sms, stream) : launch_shape<64, false>(mq, mk, mv, p, sms, stream);
+  return launch_kernel<false>(mq, mk, mv, p, a.D, a.f16, sms, stream);
+}
+
+PrefixPlan prefix_plan(int H, const os_paged_cache& c, int groups, int prefix_max_pages) {
+  PrefixPlan pl;
+  const int heads = pack_heads(H / c.heads);
+  pl.head_shift = 7 - tile_positions(heads);
+  pl.packs = H / heads;
+  const int tiles = (c.batch + (kBM >> pl.head_shift) - 1) >> (7 - pl.head_shift);  // of the largest group at most
+  const int64_t tokens = static_cast<int64_t>(groups) * prefix_max_pages * c.page_size;
+  const int rounds = tiles <= 2 ? 1 : round_count(tokens, c.heads, c.head_dim);
+  pl.shares = device_sms() * rounds;
+  int64_t at = 0;
+  const auto take = [&](int64_t n) {
+    const int64_t here = at;
+    at += round256(n);
+    return here;
+  };
+  const int64_t rows = static_cast<int64_t>(c.batch) * H;
+  pl.part_o = take(2 * static_cast<int64_t>(pl.shares) * c.head_dim * kBM * 4);
+  pl.part_ml = take(2 * static_cast<int64_t>(pl.shares) * kBM * 8);
+  pl.where = take(static_cast<int64_t>(c.batch) * pl.packs * 16);
+  pl.state_o = take(rows * c.head_dim * 4);
+  pl.state_ml = take(rows * 8);
+  pl.bytes = at;
+  return pl;
+}
+
+cudaError_t launch_attn_prefix(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H, const os_paged_cache& c,
+                               const PrefixTables& tables, float scale, const PrefixPlan& pl, void* workspace,
+                               unsigned int* err, const AttnFault& fault, cudaStream_t stream) {
+  const int sms = device_sms();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  const int heads = 1 << pl.head_shift, box_rows = c.page_size < kBN ? c.page_size : kBN;
+  const bool f16 = c.dtype == OS_DTYPE_F16;
+  CUtensorMap mq, mk, mv;
+  const int64_t dims[4] = {c.head_dim, c.page_size, c.heads, c.num_pages}, strides[3] = {c.ld_slot, c.ld_head, c.ld_page};
+  const int box[4] = {64, box_rows, 1, 1};
+  if (!make_q_map(&mq, q, f16, c.head_dim, H, heads, c.batch, ld_q_head, ld_q_batch) ||
+      !make_map(&mk, static_cast<const uint16_t*>(c.k_pages), f16, 4, dims, strides, box) ||
+      !make_map(&mv, static_cast<const uint16_t*>(c.v_pages), f16, 4, dims, strides, box))
+    return cudaErrorInvalidValue;
+  char* ws = static_cast<char*>(workspace);
+  PackedParams p = {};
+  p.cu_q = tables.cu;
+  p.batch = tables.groups;
+  p.tokens_q = c.batch;
+  p.Hq = H;
+  p.packs = pl.packs;
+  p.packs_per_key_head = pl.packs / c.heads;
+  p.pos_shift = 7 - pl.head_shift;
+  p.rounds = pl.shares / sms;
+  p.C = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.err = err;
+  p.wait_cycles = wait_limit(fault);
+  p.skip_v_step = fault.skip_v_step;
+  p.part_o = reinterpret_cast<float4*>(ws + pl.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
+  p.prefix.tables = tables;
+  p.prefix.num_pages = c.num_pages;
+  while ((1 << p.prefix.page_shift) < c.page_size) ++p.prefix.page_shift;
+  while ((1 << p.prefix.box_shift) < box_rows) ++p.prefix.box_shift;
+  p.prefix.where = reinterpret_cast<int4*>(ws + pl.where);
+  p.prefix.state_o = reinterpret_cast<float*>(ws + pl.state_o);
+  p.prefix.state_ml = reinterpret_cast<float2*>(ws + pl.state_ml);
+  return launch_kernel<true>(mq, mk, mv, p, c.head_dim, f16, sms, stream);
 }
 
 }  // namespace oss

@@ -54,8 +54,6 @@ namespace {
 
 using namespace decode;
 
-constexpr int kCtasPerSm = 2;
-
 template <int D>
 struct Shape {
   static constexpr int kStages = D == 128 ? 3 : 6;  // 24 KB of K and V in flight per warp
@@ -281,55 +279,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
         }
       }
       __syncthreads();
-      // thread: head threadIdx.x / 16 of the 8, D / 16 dims
-      constexpr int kDims = D / 16;
-      const int hh = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * kDims;
-      if (nt * 8 + hh < heads) {
-        float M = neg_inf(), L = 0.f, acc[kDims];
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, merge_m[i][hh]);
-#pragma unroll
-        for (int k = 0; k < kDims; ++k) acc[k] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          const float f = ex2(merge_m[i][hh] - reference(M));
-          L = fmaf(merge_l[i][hh], f, L);
-          const float4* src = reinterpret_cast<const float4*>(merge + (i * 8 + hh) * kMergeLd<D> + d0);
-#pragma unroll
-          for (int k = 0; k < kDims / 4; ++k) {
-            const float4 x = src[k];
-            acc[4 * k] = fmaf(x.x, f, acc[4 * k]);
-            acc[4 * k + 1] = fmaf(x.y, f, acc[4 * k + 1]);
-            acc[4 * k + 2] = fmaf(x.z, f, acc[4 * k + 2]);
-            acc[4 * k + 3] = fmaf(x.w, f, acc[4 * k + 3]);
-          }
-        }
-        const int h = head0 + nt * 8 + hh;
-        const int64_t row = static_cast<int64_t>(s.b) * p.H + h;
-        if (whole) {
-          const float inv = L != 0.f ? 1.f / L : 0.f;
-          uint32_t out[kDims / 2];
-#pragma unroll
-          for (int k = 0; k < kDims / 2; ++k) out[k] = pack2<kF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-          uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + d0);
-          if constexpr (kDims == 8)
-            *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-          else
-            *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-          if ((threadIdx.x & 15) == 0) {
-            const float e2 = L != 0.f ? M + log2f(L) : neg_inf();
-            if (p.lse) p.lse[row] = e2 * kLn2;
-            if (p.scores) p.lse2[row] = e2;
-          }
-        } else {
-          const int64_t at = static_cast<int64_t>(slot) * p.block_heads + nt * 8 + hh;
-          float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + d0);
-#pragma unroll
-          for (int k = 0; k < kDims / 4; ++k)
-            dst[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
-          if ((threadIdx.x & 15) == 0) p.part_ml[at] = make_float2(M, L);
-        }
-      }
+      merge_warps<kF16, D>(p, s, whole, slot, head0, nt * 8, heads, merge, merge_m, merge_l);
       __syncthreads();
     }
     go = w.next(p);
@@ -598,6 +548,10 @@ DecodeParams decode_params(const Plan& pl, const PagedCache& c, const uint16_t* 
   p.meta = reinterpret_cast<int4*>(ws + pl.meta);
   p.err = err;
   return p;
+}
+
+cudaError_t launch_states(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream) {
+  return launch_decode(p, f16, D, shares, nullptr, 0, 0, stream);
 }
 
 cudaError_t launch_join(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream) {

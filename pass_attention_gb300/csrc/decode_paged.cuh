@@ -21,6 +21,7 @@ constexpr int kMaxDevices = 64;
 constexpr int kTileKeys = 16;
 constexpr int kUnitTiles = kWarps;  // a unit: one tile per warp
 constexpr int kMaxHeadBlock = 16;
+constexpr int kCtasPerSm = 2;  // of the 16-bit decode
 // Items are not cut, and nothing is joined, when a row of the page table holds at
 // most kWholeKeys tokens, or at most kWholeKeysMany and there are as many items
 // as shares. Replayed from a graph, 32 heads over 8, whole against cut: 1 x 128 tokens
@@ -310,6 +311,9 @@ bool make_plan(int H, const os_paged_cache& c, int ctas_per_sm, bool weights, Pl
 // The parameters of a launch that writes o and lse, without weights and states.
 DecodeParams decode_params(const Plan& pl, const PagedCache& c, const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head,
                            int H, float scale, uint16_t* o, float* lse, void* workspace, unsigned int* err);
+
+// The first kernel alone, ending in states (p.state_o) and the parts of cut items.
+cudaError_t launch_states(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream);
 
 // The second kernel of a launch that cuts items: their join.
 cudaError_t launch_join(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream);

@@ -1,0 +1,210 @@
+// Attention of one new token per sequence, where groups of sequences share a prefix.
+//
+// With sequence b's keys the prefix P of its group and its own tokens S, o and lse come from
+// the states (m, l, O) of both:  m = max(m_P, m_S);  l = l_P 2^(m_P - m) + l_S 2^(m_S - m);  O
+// likewise;  o = O / l.
+//
+// Three kernels. (1) The prefixes, on the tensor cores (attn_packed.cu, prefix
+// kernels): the queries of a group, times the query heads of a key head, fill the
+// 128 rows of a tile, so a prefix is read once for 128 rows instead of once for every
+// sequence. (2) The sequences' own tokens, by the paged decode's first kernel
+// (decode_paged.cu). (3) The join below, of the parts and states that the two have left.
+
+#include <cstdint>
+
+#include "decode_paged.cuh"
+#include "device_common.cuh"
+#include "launch.cuh"
+#include "oss_internal.h"
+
+namespace oss {
+namespace {
+
+using namespace decode;
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+
+// What the first kernel has left.
+struct PrefixStates {
+  PrefixTables tables;
+  const int4* where;
+  const float4* part_o;  // [2 shares][D / 4][128]
+  const float2* part_ml;
+  const float* state_o;
+  const float2* state_ml;
+  int32_t shares, packs, head_shift;
+};
+
+// CTA: one row (sequence, query head). Its warps take the parts in turn, first the
+// prefix's, then those of the own tokens; a lane holds D / 32 dims.
+template <bool kF16, int D>
+__global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const DecodeParams p, const PrefixStates x) {
+  constexpr int kDims = D / 32;
+  __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const int64_t row = blockIdx.x;
+  const int b = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<int64_t>(b) * p.H);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d0 = lane * kDims;
+
+  int first = 0, parts = 0, tile_row = 0;  // the prefix's; parts 0 and first -1: it was not cut
+  if (prefix_group(x.tables, b) >= 0) {
+    const int4 w = x.where[static_cast<int64_t>(b) * x.packs + (h >> x.head_shift)];
+    first = w.x;
+    parts = w.y;
+    tile_row = (w.z + (h & ((1 << x.head_shift) - 1))) & 127;
+    if (parts == 0) {
+      first = -1;
+      parts = 1;
+    } else if (static_cast<uint32_t>(first) >= static_cast<uint32_t>(x.shares) || parts < 0 || parts > x.shares - first) {
+      parts = 0;  // a launch that gave up on a wait has not written this
+    }
+  }
+  const int g = h / p.group, in_group = h - g * p.group, hb = in_group / p.block_heads;
+  const int2 own = p.item_meta[(static_cast<int64_t>(b) * p.c.heads + g) * p.head_blocks + hb];
+  const int in_block = in_group - hb * p.block_heads;
+
+  float M = neg_inf(), L = 0.f, acc[kDims];
+#pragma unroll
+  for (int k = 0; k < kDims; ++k) acc[k] = 0.f;
+  constexpr int kBatch = 4;
+  const int all = parts + own.y;
+  for (int i0 = warp; i0 < all; i0 += kJoinWarps * kBatch) {
+    float2 ml[kBatch];
+    float v[kBatch][kDims];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kJoinWarps;
+      ml[u] = make_float2(neg_inf(), 0.f);
+#pragma unroll
+      for (int k = 0; k < kDims; ++k) v[u][k] = 0.f;
+      if (i >= all) continue;
+      const float* src;
+      if (i < parts) {
+        if (first < 0) {
+          ml[u] = x.state_ml[row];
+          src = x.state_o + row * D + d0;
+        } else {
+          const int64_t slot = part_slot(first, i);
+          ml[u] = x.part_ml[slot * 128 + tile_row];
+          // dims d0 .. of the vector of 4 that they lie in
+          src = reinterpret_cast<const float*>(x.part_o + (slot * (D / 4) + d0 / 4) * 128 + tile_row) + d0 % 4;
+        }
+      } else if (own.y == 1) {
+        ml[u] = p.state_ml[row];
+        src = p.state_o + row * D + d0;
+      } else {
+        const int64_t at = part_slot(own.x, i - parts) * p.block_heads + in_block;
+        ml[u] = p.part_ml[at];
+        src = p.part_o + at * D + d0;
+      }
+      if constexpr (kDims == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        v[u][0] = y.x, v[u][1] = y.y, v[u][2] = y.z, v[u][3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(src);
+        v[u][0] = y.x, v[u][1] = y.y;
+      }
+    }
+    float to = M;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) to = fmaxf(to, ml[u].x);
+    const float ref = reference(to), corr = ex2(M - ref);
+    M = to;
+    L *= corr;
+#pragma unroll
+    for (int k = 0; k < kDims; ++k) acc[k] *= corr;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float f = ex2(ml[u].x - ref);
+      L = fmaf(ml[u].y, f, L);
+#pragma unroll
+      for (int k = 0; k < kDims; ++k) acc[k] = fmaf(v[u][k], f, acc[k]);
+    }
+  }
+  if (lane == 0) {
+    sm[warp] = M;
+    sl[warp] = L;
+  }
+#pragma unroll
+  for (int k = 0; k < kDims; ++k) so[warp][d0 + k] = acc[k];
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  M = neg_inf();
+  L = 0.f;
+  float a = 0.f, c = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) M = fmaxf(M, sm[i]);
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) {
+    const float f = ex2(sm[i] - reference(M));
+    L = fmaf(sl[i], f, L);
+    a = fmaf(so[i][2 * threadIdx.x], f, a);
+    c = fmaf(so[i][2 * threadIdx.x + 1], f, c);
+  }
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  reinterpret_cast<uint32_t*>(p.o + row * D)[threadIdx.x] = pack2<kF16>(a * inv, c * inv);
+  if (threadIdx.x == 0 && p.lse) p.lse[row] = L != 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
+}
+
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Layout of the workspace: the prefixes' part, the decode's, and its states.
+struct SharedPlan {
+  PrefixPlan prefix;
+  Plan own;
+  int64_t own_at, item_meta, state_o, state_ml, bytes;
+};
+
+bool make_shared_plan(int H, const os_paged_cache& c, int groups, int prefix_max_pages, SharedPlan* out) {
+  if (!make_plan(H, c, kCtasPerSm, false, &out->own)) return false;
+  out->prefix = prefix_plan(H, c, groups, prefix_max_pages);
+  const int64_t rows = static_cast<int64_t>(c.batch) * H;
+  out->own_at = out->prefix.bytes;
+  out->item_meta = out->own_at + out->own.bytes;
+  out->state_o = out->item_meta + round256(static_cast<int64_t>(c.batch) * c.heads * out->own.head_blocks * 8);
+  out->state_ml = out->state_o + round256(rows * c.head_dim * 4);
+  out->bytes = out->state_ml + round256(rows * 8);
+  return true;
+}
+
+}  // namespace
+
+int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache, int groups, int prefix_max_pages) {
+  SharedPlan pl;
+  return make_shared_plan(H, cache, groups, prefix_max_pages, &pl) ? pl.bytes : -1;
+}
+
+cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
+                                 const os_paged_cache& cache, const PrefixTables& prefix, float scale, uint16_t* o,
+                                 float* lse, void* workspace, unsigned int* err, const AttnFault& fault,
+                                 cudaStream_t stream) {
+  SharedPlan pl;
+  if (!make_shared_plan(H, cache, prefix.groups, prefix.max_pages, &pl)) return cudaErrorInvalidDevice;
+  const int64_t rows = static_cast<int64_t>(cache.batch) * H;
+  if (rows > 0x7fffffff) return cudaErrorNotSupported;
+  char* ws = static_cast<char*>(workspace);
+  cudaError_t e = launch_attn_prefix(q, ld_q_batch, ld_q_head, H, cache, prefix, scale, pl.prefix, ws, err, fault, stream);
+  if (e != cudaSuccess) return e;
+  const bool f16 = cache.dtype == OS_DTYPE_F16;
+  DecodeParams p = decode_params(pl.own, paged_cache(cache), q, ld_q_batch, ld_q_head, H, scale, o, lse, ws + pl.own_at, err);
+  p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
+  p.state_o = reinterpret_cast<float*>(ws + pl.state_o);
+  p.state_ml = reinterpret_cast<float2*>(ws + pl.state_ml);
+  if ((e = launch_states(p, f16, cache.head_dim, pl.own.shares, stream)) != cudaSuccess) return e;
+  const PrefixStates x{prefix,
+                       reinterpret_cast<const int4*>(ws + pl.prefix.where),
+                       reinterpret_cast<const float4*>(ws + pl.prefix.part_o),
+                       reinterpret_cast<const float2*>(ws + pl.prefix.part_ml),
+                       reinterpret_cast<const float*>(ws + pl.prefix.state_o),
+                       reinterpret_cast<const float2*>(ws + pl.prefix.state_ml),
+                       pl.prefix.shares, pl.prefix.packs, pl.prefix.head_shift};
+  const dim3 grid(static_cast<unsigned>(rows));
+  const auto join = [&](auto* kernel) { return launch_after(kernel, grid, kJoinThreads, 0, stream, p, x); };
+  if (cache.head_dim == 128)
+    return f16 ? join(decode_shared_join_kernel<true, 128>) : join(decode_shared_join_kernel<false, 128>);
+  return f16 ? join(decode_shared_join_kernel<true, 64>) : join(decode_shared_join_kernel<false, 64>);
+}
+
+}  // namespace oss

@@ -174,6 +174,20 @@ int64_t attn_packed_workspace_bytes(int64_t tokens_k, int Hkv, int D);
 cudaError_t launch_attn_packed(const PackedArgs& args, void* workspace, unsigned int* err,
                                const AttnFault& fault, cudaStream_t stream);
 
+// Layout of the workspace of the prefixes' part of os_attention_decode_shared: offsets, then
+// the size.
+struct PrefixPlan {
+  int shares, packs, head_shift;  // 2^head_shift query heads of a key head side by side in a tile
+  int64_t part_o, part_ml, where, state_o, state_ml, bytes;
+};
+
+PrefixPlan prefix_plan(int H, const os_paged_cache& cache, int groups, int prefix_max_pages);
+
+// Attention of every sequence's token over its group's prefix, ending in states (m, l, O).
+cudaError_t launch_attn_prefix(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H, const os_paged_cache& cache,
+                               const PrefixTables& tables, float scale, const PrefixPlan& plan, void* workspace,
+                               unsigned int* err, const AttnFault& fault, cudaStream_t stream);
+
 // log2(e) split into a float and the float nearest to the remainder, so that
 // hi + lo carries about 48 bits of it.
 void split_constant(double c, float* hi, float* lo);
