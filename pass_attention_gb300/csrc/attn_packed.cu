@@ -100,7 +100,7 @@ struct Smem {
 struct PrefixOut {
   PrefixTables tables;
   int32_t num_pages, page_shift, box_shift;  // a TMA box: 2^box_shift slots of a page
-  int4* where;      // [tokens_q][packs]: {share, parts (0: not cut), row of the first head in the tile}
+  int4* where;      // [tokens_q][packs]: {first slot / 2, parts (0: not cut), row of the first head in the tile, lanes}
   float* state_o;   // [tokens_q][Hq][D]: unnormalised O of items that are not cut
   float2* state_ml;  // [tokens_q][Hq]
 };
@@ -200,6 +200,16 @@ struct Barriers {
   uint64_t drain[2];
 };
 
+// Lanes (prefix; others: 1 of 1). With several query tiles on one prefix, `count` CTAs take the
+// same shares, each with a tile of its own (tile number at * count + lane), and so
+// read the same K and V at the same time, which then come from HBM once. As items of their
+// own the tiles were half a share apart: 64 sequences, 4 heads a key head, behind 65536
+// tokens read the prefix's 268 MB twice (87 us, the kernel alone).
+struct Lanes {
+  int32_t count, lane;
+  uint32_t sets, set;  // sets of `count` CTAs, and this CTA's
+};
+
 // Where a share begins and ends: the item at place w of the row of items, and
 // the KV step inside it.
 struct ShareStart {
@@ -214,15 +224,18 @@ struct Shares {
   ShareStart start[kMaxRounds];
   ShareEnd end[kMaxRounds];
   ShareCut cut;
+  Lanes lanes;
 };
 
-// (Prefix: sequence b is a group, its keys the group's prefix.)
+// (Prefix: sequence b is a group, its keys the group's prefix, and a tile one of every lane.)
 template <bool kPrefix>
-__device__ __forceinline__ PackedSeq load_seq(const PackedParams& p, int b) {
+__device__ __forceinline__ PackedSeq load_seq(const PackedParams& p, int b, int lanes) {
   if constexpr (kPrefix) {
     const PrefixTables& t = p.prefix.tables;
     const RowRange q = p.cu_q ? row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q) : RowRange{0, p.tokens_q, false};
-    return packed_seq(q, RowRange{0, paged_length(t.len[b], t.max_pages, p.prefix.page_shift), false}, p.pos_shift);
+    PackedSeq s = packed_seq(q, RowRange{0, paged_length(t.len[b], t.max_pages, p.prefix.page_shift), false}, p.pos_shift);
+    s.tiles = (s.tiles + lanes - 1) / lanes;
+    return s;
   }
   return packed_seq(row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q),
                     row_range(p.cu_k[b], p.cu_k[b + 1], p.tokens_k), p.pos_shift);
@@ -230,12 +243,12 @@ __device__ __forceinline__ PackedSeq load_seq(const PackedParams& p, int b) {
 
 // Length of the items of sequences [b0, b1), in one pack, and their tiles.
 template <bool kPrefix>
-__device__ __forceinline__ int64_t run_length(const PackedParams& p, int b0, int b1, uint32_t* tiles) {
+__device__ __forceinline__ int64_t run_length(const PackedParams& p, int lanes, int b0, int b1, uint32_t* tiles) {
   int64_t sum = 0;
   uint32_t n = 0;
   OSS_ROLLED
   for (int b = b0; b < b1; ++b) {
-    const PackedSeq s = load_seq<kPrefix>(p, b);
+    const PackedSeq s = load_seq<kPrefix>(p, b, lanes);
     sum += length_before(s, s.tiles, p.pos_shift, p.causal != 0);
     n += static_cast<uint32_t>(s.tiles);
   }
@@ -254,6 +267,35 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x) {
   return x;
 }
 
+// The lanes of a prefix launch: as many as the group with the most tiles has, up to 8 (beyond
+// that in equal shares of its tiles), if that leaves at most a fifth of the CTAs' time
+// idle in groups of fewer tiles; else 1. `sums` [3] is shared and cleared here.
+constexpr int kMaxLanes = 8;
+
+__device__ __forceinline__ Lanes find_lanes(const PackedParams& p, unsigned long long* sums) {
+  Lanes x;
+  if (threadIdx.x < 3) sums[threadIdx.x] = 0;
+  __syncthreads();
+  OSS_ROLLED
+  for (int b = threadIdx.x; b < p.batch; b += kThreads) atomicMax(&sums[0], static_cast<unsigned long long>(load_seq<true>(p, b, 1).tiles));
+  __syncthreads();
+  const int most = max(1, static_cast<int>(sums[0])), per = (most + kMaxLanes - 1) / kMaxLanes;
+  x.count = (most + per - 1) / per;
+  OSS_ROLLED
+  for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+    const PackedSeq s = load_seq<true>(p, b, 1);
+    const unsigned long long steps = kTileWeight + kv_tiles(s, 0, p.pos_shift, false);
+    atomicAdd(&sums[1], s.tiles * steps);
+    atomicAdd(&sums[2], (s.tiles + x.count - 1) / x.count * x.count * steps);
+  }
+  __syncthreads();
+  if (x.count > static_cast<int>(gridDim.x) || sums[2] * 4 > sums[1] * 5) x.count = 1;
+  x.sets = gridDim.x / x.count;
+  x.set = blockIdx.x / x.count;
+  x.lane = static_cast<int>(blockIdx.x - x.set * x.count);
+  return x;
+}
+
 // Finds this CTA's shares. The sequences are cut into a run per warp, and each of
 // those into a run per lane. All warps measure theirs; then warp 2 r + e looks
 // for the beginning (e = 0) or the end (e = 1) of the share of round r: the warp's
@@ -269,6 +311,11 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
   int64_t* warp_len = scratch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool causal = p.causal != 0;
+  Lanes lanes{1, 0, gridDim.x, blockIdx.x};
+  if constexpr (kPrefix) {
+    lanes = find_lanes(p, reinterpret_cast<unsigned long long*>(tile_scratch + kWarps));
+    if (threadIdx.x == 0) sh->lanes = lanes;
+  }
   const int per_warp = (p.batch + kWarps - 1) / kWarps;
   int lo = min(p.batch, warp * per_warp), hi = min(p.batch, lo + per_warp);  // the run in hand
   int64_t before = 0, at = 0, sum = 0;
@@ -279,7 +326,7 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
     // the lanes' runs of [lo, hi)
     const int per = (hi - lo + 31) / 32;
     const int b0 = min(hi, lo + lane * per), b1 = min(hi, b0 + per);
-    sum = run_length<kPrefix>(p, b0, b1, &tiles);
+    sum = run_length<kPrefix>(p, lanes.count, b0, b1, &tiles);
     const int64_t upto = warp_scan(sum);
     if (level == 0) {
       if (blockIdx.x == 0) {
@@ -302,9 +349,9 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
       const int64_t len = warp_scan(lane < kWarps ? warp_len[lane] : 0);
       const int64_t items = static_cast<int64_t>(__reduce_add_sync(kAll, lane < kWarps ? tile_scratch[lane] : 0u)) * p.packs;
       const int64_t total = __shfl_sync(kAll, len, 31) * p.packs;
-      const ShareCut cut = share_cut(total, share_count(total, items, gridDim.x, p.rounds));
+      const ShareCut cut = share_cut(total, share_count(total, items, lanes.sets, p.rounds, kPrefix ? kPrefixShareShift : kLeastShareShift));
       if (threadIdx.x == 0) sh->cut = cut;
-      const uint32_t share = r * gridDim.x + blockIdx.x;
+      const uint32_t share = r * lanes.sets + lanes.set;
       if (r >= p.rounds || share >= cut.count) break;
       at = share_begin(cut, share + e);
       if (at == total) {
@@ -327,7 +374,7 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
     const int64_t len = __shfl_sync(kAll, sum, k);
     const int pack = small_quotient(at - before, len);
     before += pack * len;
-    const PackedSeq s = load_seq<kPrefix>(p, lo);
+    const PackedSeq s = load_seq<kPrefix>(p, lo, lanes.count);
     int tile = 0;
     int64_t stride = 1;
     while (stride * 32 < s.tiles) stride *= 32;
@@ -343,7 +390,7 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
     if (lane == 0) {
       const int64_t w = before + place;
       const int steps = kv_tiles(s, tile, p.pos_shift, causal);
-      const int step = cut_step(at - w, steps);
+      const int step = cut_step(at - w, steps, kPrefix ? kPrefixMinSteps : kMinSteps);
       if (e == 0)
         sh->start[r] = ShareStart{w, lo, pack, tile, step};
       else
@@ -397,14 +444,15 @@ struct Walk {
         fetch = false;
         OSS_ROLLED
         do {
-          s = load_seq<kPrefix>(p, ++seq);
+          s = load_seq<kPrefix>(p, ++seq, kPrefix ? sh.lanes.count : 1);
         } while (s.tiles == 0 && seq + 1 < p.batch);
       }
       const int steps = kv_tiles(s, tile, p.pos_shift, causal);
       const int s1 = w == end_w ? end_step : steps;
       const int from = s0;
-      if (from < s1) {
-        const int pos0 = tile << p.pos_shift;
+      const int pos0 = (kPrefix ? tile * sh.lanes.count + sh.lanes.lane : tile) << p.pos_shift;
+      const bool some = from < s1 && (!kPrefix || pos0 < s.q_len);  // (a lane may have no tile of a group)
+      if (some) {
         u.q_row = s.q_start + pos0;
         u.n_pos = min(1 << p.pos_shift, s.q_len - pos0);
         u.k_row = kPrefix ? seq : s.k_start;
@@ -416,10 +464,11 @@ struct Walk {
         u.s0 = from;
         u.s1 = s1;
         u.pack = pack;
-        u.share = round * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+        u.share = kPrefix ? static_cast<int>(sh.lanes.set) : round * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
         u.parts = 0;
         if (from == 0 && s1 < steps)
-          u.parts = static_cast<int>(last_boundary(sh.cut, w + kTileWeight + steps - kMinSteps)) - u.share + 1;
+          u.parts = static_cast<int>(last_boundary(sh.cut, w + kTileWeight + steps - (kPrefix ? kPrefixMinSteps : kMinSteps))) - u.share + 1;
+        if constexpr (kPrefix) u.share = u.share * sh.lanes.count + sh.lanes.lane;
         u.end = 0;
       }
       w += kTileWeight + steps;
@@ -431,7 +480,7 @@ struct Walk {
           fetch = true;
         }
       }
-      if (from < s1) return true;
+      if (some) return true;
     }
   }
 };
@@ -500,13 +549,13 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bars;
   __shared__ Shares shares;
-  __shared__ float2 row_ml[kBM];  // find_shares uses it first
+  __shared__ __align__(16) float2 row_ml[kBM];  // find_shares uses it first
   __shared__ Unit units[kUnits];
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag_s;
   __shared__ uint32_t bad_keys[kBadRing];  // of the steps' KV tiles (prefix)
   volatile int* abort_flag = &abort_flag_s;
-  let_next_kernel_start();
+  if constexpr (!kPrefix) let_next_kernel_start();
 
   const uint32_t sbase = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5;
@@ -549,6 +598,9 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     tc_fence_before();
   }
   wait_for_previous_kernel();
+  // (Prefix: the kernel behind this one reads nothing of it, and may begin once all that
+  // came before this one has ended. It waits for this one at its own end.)
+  if constexpr (kPrefix) let_next_kernel_start();
   if (!kPrefix && threadIdx.x < p.rounds) p.meta[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
   find_shares<kPrefix>(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
   tc_fence_after();
@@ -842,7 +894,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (kPrefix && u.s0 == 0) {
         // where the rows' states lie, for the kernel that joins them with the sequences' own tokens
         const int at = threadIdx.x - kEpiWarp * 32;
-        if (at < u.n_pos) p.prefix.where[static_cast<int64_t>(u.q_row + at) * p.packs + u.pack] = make_int4(u.share, u.parts, at << head_shift, 0);
+        if (at < u.n_pos) p.prefix.where[static_cast<int64_t>(u.q_row + at) * p.packs + u.pack] = make_int4(u.share, u.parts, at << head_shift, shares.lanes.count);
       }
       if (kPrefix && u.s0 == 0 && u.s1 == u.n_kv) {
         // The state as it is. 16 rows x 64 dims a load, of which 4 threads store the
@@ -1331,15 +1383,12 @@ cudaError_t launch_attn_packed(const PackedArgs& a, void* workspace, unsigned in
   return launch_kernel<false>(mq, mk, mv, p, a.D, a.f16, sms, stream);
 }
 
-PrefixPlan prefix_plan(int H, const os_paged_cache& c, int groups, int prefix_max_pages) {
+PrefixPlan prefix_plan(int H, const os_paged_cache& c) {
   PrefixPlan pl;
   const int heads = pack_heads(H / c.heads);
   pl.head_shift = 7 - tile_positions(heads);
   pl.packs = H / heads;
-  const int tiles = (c.batch + (kBM >> pl.head_shift) - 1) >> (7 - pl.head_shift);  // of the largest group at most
-  const int64_t tokens = static_cast<int64_t>(groups) * prefix_max_pages * c.page_size;
-  const int rounds = tiles <= 2 ? 1 : round_count(tokens, c.heads, c.head_dim);
-  pl.shares = device_sms() * rounds;
+  pl.shares = device_sms();
   int64_t at = 0;
   const auto take = [&](int64_t n) {
     const int64_t here = at;
@@ -1379,7 +1428,7 @@ cudaError_t launch_attn_prefix(const uint16_t* q, int64_t ld_q_batch, int64_t ld
   p.packs = pl.packs;
   p.packs_per_key_head = pl.packs / c.heads;
   p.pos_shift = 7 - pl.head_shift;
-  p.rounds = pl.shares / sms;
+  p.rounds = 1;
   p.C = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.err = err;
   p.wait_cycles = wait_limit(fault);

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float merge_m[kWarps][8], merge_l[kWarps][8];
   let_next_kernel_start();
-  wait_for_previous_kernel();
+  if (!p.behind_prefix) wait_for_previous_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane & 3, row8 = lane >> 2;
 
@@ -82,7 +82,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   ShareCut share;
   const bool has_share = find_share(p, &w, &share);
   if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (!has_share) return;
+  if (!has_share) {
+    if (p.behind_prefix) wait_for_previous_kernel();
+    return;
+  }
 
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
   float* merge = reinterpret_cast<float*>(smem + S::kRingBytes);
@@ -285,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
     go = w.next(p);
   }
   copy_wait<0>();
+  if (p.behind_prefix) wait_for_previous_kernel();
 }
 
 // The second kernel. With weights, its first CTAs add up: kAddKeys keys of one key

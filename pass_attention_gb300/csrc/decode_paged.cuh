@@ -53,6 +53,10 @@ struct DecodeParams {
   int4* meta;       // [N]: {sequence, key head and head block, parts, first slot}
   float* lse2;      // [batch][H], base 2: of items that were not cut (only with scores)
   int2* item_meta;  // [batch][heads * head_blocks]: {first share, parts}, or null
+  // of the decode behind shared prefixes: the kernel before this one writes nothing that this one
+  // reads, so it is waited for at the end
+  int32_t behind_prefix;
+  PrefixTables prefix;
   float* state_o;   // [batch][H][D]: O of whole items instead of o, or null
   float2* state_ml;  // [batch][H]: m, l
   float* scores;    // [batch][heads * head_blocks][capacity][score_heads], or null
@@ -284,6 +288,8 @@ __device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk& w
       parts = static_cast<int>(last_boundary(share, w.u + s.units - 1) - blockIdx.x) + 1;
       p.meta[blockIdx.x] = make_int4(s.b, s.j, parts, slot);
     }
+    // (behind prefixes, parts < 0: no group names the sequence)
+    if (p.behind_prefix && prefix_group(p.prefix, s.b) < 0) parts = -parts;
     if (p.item_meta) p.item_meta[static_cast<int64_t>(s.b) * p.c.heads * p.head_blocks + s.j] = make_int2(blockIdx.x, parts);
   }
   return slot;

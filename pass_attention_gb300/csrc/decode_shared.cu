@@ -22,12 +22,11 @@ namespace {
 
 using namespace decode;
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 // What the first kernel has left.
 struct PrefixStates {
-  PrefixTables tables;
   const int4* where;
   const float4* part_o;  // [2 shares][D / 4][128]
   const float2* part_ml;
@@ -43,27 +42,25 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
   constexpr int kDims = D / 32;
   __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
   let_next_kernel_start();
-  wait_for_previous_kernel();
-  const int64_t row = blockIdx.x;
-  const int b = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<int64_t>(b) * p.H);
+  const int h = blockIdx.x, b = blockIdx.y;
+  const int64_t row = static_cast<int64_t>(b) * p.H + h;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d0 = lane * kDims;
-
-  int first = 0, parts = 0, tile_row = 0;  // the prefix's; parts 0 and first -1: it was not cut
-  if (prefix_group(x.tables, b) >= 0) {
-    const int4 w = x.where[static_cast<int64_t>(b) * x.packs + (h >> x.head_shift)];
-    first = w.x;
-    parts = w.y;
-    tile_row = (w.z + (h & ((1 << x.head_shift) - 1))) & 127;
-    if (parts == 0) {
-      first = -1;
-      parts = 1;
-    } else if (static_cast<uint32_t>(first) >= static_cast<uint32_t>(x.shares) || parts < 0 || parts > x.shares - first) {
-      parts = 0;  // a launch that gave up on a wait has not written this
-    }
-  }
   const int g = h / p.group, in_group = h - g * p.group, hb = in_group / p.block_heads;
-  const int2 own = p.item_meta[(static_cast<int64_t>(b) * p.c.heads + g) * p.head_blocks + hb];
   const int in_block = in_group - hb * p.block_heads;
+  wait_for_previous_kernel();
+  int2 own = p.item_meta[(static_cast<int64_t>(b) * p.c.heads + g) * p.head_blocks + hb];
+  const int4 w = x.where[static_cast<int64_t>(b) * x.packs + (h >> x.head_shift)];
+  int parts = 0;  // of the prefix
+  const bool cut = w.y != 0;
+  const int tile_row = (w.z + (h & ((1 << x.head_shift) - 1))) & 127;
+  if (own.y > 0) {
+    parts = cut ? w.y : 1;
+    // (a launch that gave up on a wait has not written this)
+    if (cut && (parts < 0 || w.x < 0 || w.w < 1 || w.w > x.shares || w.x + (parts - 1) * static_cast<int64_t>(w.w) >= x.shares))
+      parts = 0;
+  } else {
+    own.y = -own.y;  // no group names the sequence
+  }
 
   float M = neg_inf(), L = 0.f, acc[kDims];
 #pragma unroll
@@ -82,11 +79,11 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
       if (i >= all) continue;
       const float* src;
       if (i < parts) {
-        if (first < 0) {
+        if (!cut) {
           ml[u] = x.state_ml[row];
           src = x.state_o + row * D + d0;
         } else {
-          const int64_t slot = part_slot(first, i);
+          const int64_t slot = 2 * (w.x + static_cast<int64_t>(i) * w.w) + (i == 0 ? 1 : 0);
           ml[u] = x.part_ml[slot * 128 + tile_row];
           // dims d0 .. of the vector of 4 that they lie in
           src = reinterpret_cast<const float*>(x.part_o + (slot * (D / 4) + d0 / 4) * 128 + tile_row) + d0 % 4;
@@ -157,9 +154,9 @@ struct SharedPlan {
   int64_t own_at, item_meta, state_o, state_ml, bytes;
 };
 
-bool make_shared_plan(int H, const os_paged_cache& c, int groups, int prefix_max_pages, SharedPlan* out) {
+bool make_shared_plan(int H, const os_paged_cache& c, SharedPlan* out) {
   if (!make_plan(H, c, kCtasPerSm, false, &out->own)) return false;
-  out->prefix = prefix_plan(H, c, groups, prefix_max_pages);
+  out->prefix = prefix_plan(H, c);
   const int64_t rows = static_cast<int64_t>(c.batch) * H;
   out->own_at = out->prefix.bytes;
   out->item_meta = out->own_at + out->own.bytes;
@@ -171,9 +168,9 @@ bool make_shared_plan(int H, const os_paged_cache& c, int groups, int prefix_max
 
 }  // namespace
 
-int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache, int groups, int prefix_max_pages) {
+int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache) {
   SharedPlan pl;
-  return make_shared_plan(H, cache, groups, prefix_max_pages, &pl) ? pl.bytes : -1;
+  return make_shared_plan(H, cache, &pl) ? pl.bytes : -1;
 }
 
 cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
@@ -181,9 +178,7 @@ cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t 
                                  float* lse, void* workspace, unsigned int* err, const AttnFault& fault,
                                  cudaStream_t stream) {
   SharedPlan pl;
-  if (!make_shared_plan(H, cache, prefix.groups, prefix.max_pages, &pl)) return cudaErrorInvalidDevice;
-  const int64_t rows = static_cast<int64_t>(cache.batch) * H;
-  if (rows > 0x7fffffff) return cudaErrorNotSupported;
+  if (!make_shared_plan(H, cache, &pl)) return cudaErrorInvalidDevice;
   char* ws = static_cast<char*>(workspace);
   cudaError_t e = launch_attn_prefix(q, ld_q_batch, ld_q_head, H, cache, prefix, scale, pl.prefix, ws, err, fault, stream);
   if (e != cudaSuccess) return e;
@@ -192,15 +187,16 @@ cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t 
   p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
   p.state_o = reinterpret_cast<float*>(ws + pl.state_o);
   p.state_ml = reinterpret_cast<float2*>(ws + pl.state_ml);
+  p.behind_prefix = 1;
+  p.prefix = prefix;
   if ((e = launch_states(p, f16, cache.head_dim, pl.own.shares, stream)) != cudaSuccess) return e;
-  const PrefixStates x{prefix,
-                       reinterpret_cast<const int4*>(ws + pl.prefix.where),
+  const PrefixStates x{reinterpret_cast<const int4*>(ws + pl.prefix.where),
                        reinterpret_cast<const float4*>(ws + pl.prefix.part_o),
                        reinterpret_cast<const float2*>(ws + pl.prefix.part_ml),
                        reinterpret_cast<const float*>(ws + pl.prefix.state_o),
                        reinterpret_cast<const float2*>(ws + pl.prefix.state_ml),
                        pl.prefix.shares, pl.prefix.packs, pl.prefix.head_shift};
-  const dim3 grid(static_cast<unsigned>(rows));
+  const dim3 grid(H, cache.batch);
   const auto join = [&](auto* kernel) { return launch_after(kernel, grid, kJoinThreads, 0, stream, p, x); };
   if (cache.head_dim == 128)
     return f16 ? join(decode_shared_join_kernel<true, 128>) : join(decode_shared_join_kernel<false, 128>);

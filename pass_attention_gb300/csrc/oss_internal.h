@@ -145,7 +145,7 @@ cudaError_t launch_decode_paged_fp8(const uint16_t* q, int64_t ld_q_batch, int64
 
 // Workspace of the decode behind shared prefixes on the current device (-1: it could not be
 // queried).
-int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache, int groups, int prefix_max_pages);
+int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache);
 
 cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
                                  const os_paged_cache& cache, const PrefixTables& prefix, float scale, uint16_t* o,
@@ -181,7 +181,7 @@ struct PrefixPlan {
   int64_t part_o, part_ml, where, state_o, state_ml, bytes;
 };
 
-PrefixPlan prefix_plan(int H, const os_paged_cache& cache, int groups, int prefix_max_pages);
+PrefixPlan prefix_plan(int H, const os_paged_cache& cache);
 
 // Attention of every sequence's token over its group's prefix, ending in states (m, l, O).
 cudaError_t launch_attn_prefix(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H, const os_paged_cache& cache,

@@ -20,6 +20,13 @@ namespace oss {
 
 constexpr int kTileWeight = 2;
 constexpr int kMinSteps = 3;
+constexpr int kLeastShareShift = 3;
+// The same for prefixes, whose states are joined in any case.
+#ifndef PREFIX_MIN
+#define PREFIX_MIN 1
+#define PREFIX_SHARE 2
+#endif
+constexpr int kPrefixMinSteps = PREFIX_MIN, kPrefixShareShift = PREFIX_SHARE;
 constexpr int kKeysPerTile = 128;
 constexpr int kTileShift = 7;
 
@@ -96,10 +103,10 @@ OSS_HD int32_t tile_at(const PackedSeq& s, int64_t at, int pos_shift, bool causa
 
 // Shares of a row of items for `ctas` CTAs that take up to `rounds` each: no
 // fewer than there are items where the CTAs reach; beyond that, a share holds at
-// least 8 units (6 KV steps), less is not worth a joined tile; and more than
+// least 2^least_shift units (8: 6 KV steps, less is not worth a joined tile); and more than
 // one round only as whole rounds, so that every CTA has the same number.
-OSS_HD int32_t share_count(int64_t total, int64_t items, int32_t ctas, int32_t rounds) {
-  int64_t want = total >> 3;
+OSS_HD int32_t share_count(int64_t total, int64_t items, int32_t ctas, int32_t rounds, int least_shift = kLeastShareShift) {
+  int64_t want = total >> least_shift;
   if (want < items) want = items;
   const int32_t most = ctas * rounds;
   int32_t n = want < most ? static_cast<int32_t>(want) : most;
@@ -152,10 +159,10 @@ OSS_HD int32_t small_quotient(int64_t x, int64_t y) {
 
 // KV step at which a boundary `into` units inside an item cuts it: 0 moves the
 // boundary to the item's start, `steps` to its end.
-OSS_HD int32_t cut_step(int64_t into, int32_t steps) {
+OSS_HD int32_t cut_step(int64_t into, int32_t steps, int32_t min_steps = kMinSteps) {
   const int64_t step = into - kTileWeight;
-  if (step < kMinSteps) return 0;
-  if (steps - step < kMinSteps) return steps;
+  if (step < min_steps) return 0;
+  if (steps - step < min_steps) return steps;
   return static_cast<int32_t>(step);
 }
 
