@@ -392,7 +392,8 @@ cudaError_t launch_decode_paged_fp8(const uint16_t* q, int64_t ld_q_batch, int64
                                     void* workspace, unsigned int* err, cudaStream_t stream) {
   Plan pl;
   if (!make_plan(H, cache.pages, ctas_of(H, cache.pages), false, &pl)) return cudaErrorInvalidDevice;
-  const DecodeParams p = decode_params(pl, paged_cache(cache.pages), q, ld_q_batch, ld_q_head, H, scale, o, lse, workspace, err);
+  DecodeParams p = decode_params(pl, paged_cache(cache.pages), q, ld_q_batch, ld_q_head, H, scale, o, lse, workspace, err);
+  p.item_weight = pl.whole ? 0 : kItemWeight;
   const Fp8Pools f = fp8_pools(cache);
   if (cache.pages.dtype == OS_DTYPE_F16)
     return cache.pages.head_dim == 128 ? launch_heads<true, 128>(p, f, pl.shares, stream)

@@ -33,6 +33,10 @@ constexpr int kCtasPerSm = 2;  // of the 16-bit decode
 constexpr int kWholeKeys = 384;
 constexpr int kWholeKeysMany = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
+// What an item costs beside its units of 64 keys, in units: its queries' way from memory
+// and the warps' merge. Without it, shares of many short items took twice as long as others.
+// RESULT
+constexpr int kItemWeight = 2;
 // The reference maximum moves only when a score exceeds it by more than
 // 2^kSlack: any reference gives the same quotient O / l, and weights up to 2^8 are
 // as exact in bf16 and fp16 as weights up to 1.
@@ -44,6 +48,7 @@ struct DecodeParams {
   int64_t ld_q_batch, ld_q_head;
   int32_t H, group, head_blocks, block_heads;  // block_heads: 8 or 16
   int32_t unit_tiles;                          // tiles of a unit: 4, or all of an item
+  int32_t item_weight;  // what an item costs beside its units, in units
   float scale2;                                // scale * log2(e)
   uint16_t* o;
   float* lse;
@@ -118,10 +123,12 @@ struct Segment {
   int b, j, len, units, r0, r1;
 };
 
-// The walk of one CTA over its share [u, end) of the units.
+// The walk of one CTA over its share of the row of items. An item takes
+// item_weight + units places of the row, and unit k of an item that begins at place `at`
+// lies at at + item_weight + k.
 struct Walk {
   Segment s;
-  int64_t u, end;
+  int64_t at, end;  // where the segment's item and the share's end lie
 
   // (an empty sequence has a unit, to be answered)
   __device__ __forceinline__ static int units_of(const DecodeParams& p, int len) {
@@ -129,23 +136,24 @@ struct Walk {
     const int n = (len + kTileKeys * kUnitTiles - 1) / (kTileKeys * kUnitTiles);
     return n > 0 ? n : 1;
   }
-  __device__ __forceinline__ void clip() {
-    const int64_t r1 = s.r0 + (end - u);
-    s.r1 = r1 < s.units ? static_cast<int>(r1) : s.units;
+  // The segment from unit r0 of the item at hand; false when the share ends before that.
+  __device__ __forceinline__ bool clip(const DecodeParams& p, int64_t r0) {
+    const int64_t r1 = end - at - p.item_weight;
+    s.r0 = static_cast<int>(r0);
+    s.r1 = r1 < s.units ? static_cast<int>(r1 > 0 ? r1 : 0) : s.units;
+    return s.r0 < s.r1;
   }
   // The next segment of the share; false when there is none.
   __device__ __forceinline__ bool next(const DecodeParams& p) {
-    u += s.r1 - s.r0;
-    if (u >= end) return false;
+    at += s.units + p.item_weight;
+    if (at + p.item_weight >= end) return false;
     if (++s.j == p.c.heads * p.head_blocks) {
       s.j = 0;
       ++s.b;
       s.len = paged_length(p.c.kv_len[s.b], p.c.max_pages, p.c.page_shift);
       s.units = units_of(p, s.len);
     }
-    s.r0 = 0;
-    clip();
-    return true;
+    return clip(p, 0);
   }
   // One past the last tile of the segment that holds a key.
   __device__ __forceinline__ int tile_end(const DecodeParams& p) const {
@@ -159,12 +167,13 @@ struct Walk {
 __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk* w, ShareCut* share) {
   __shared__ int64_t warp_sum[kWarps];
   __shared__ Walk found;
+  __shared__ bool some;  // a share may lie within an item's weight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.c.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.c.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.c.batch, b0 + per);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b)
-    mine += Walk::units_of(p, paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift));
+    mine += Walk::units_of(p, paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift)) + p.item_weight;
   int64_t upto = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -189,27 +198,26 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk* w, Share
     int64_t at = before * per_seq;
     for (int b = b0; b < b1; ++b) {
       const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
-      const int units = Walk::units_of(p, len);
-      if (first < at + static_cast<int64_t>(units) * per_seq) {
+      const int units = Walk::units_of(p, len), places = units + p.item_weight;
+      if (first < at + static_cast<int64_t>(places) * per_seq) {
         Walk f;
         f.s.b = b;
-        f.s.j = small_quotient(first - at, units);
+        f.s.j = small_quotient(first - at, places);
         f.s.len = len;
         f.s.units = units;
-        f.s.r0 = static_cast<int>((first - at) - static_cast<int64_t>(f.s.j) * units);
-        f.s.r1 = 0;
-        f.u = first;
+        f.at = at + static_cast<int64_t>(f.s.j) * places;
         f.end = last;
-        f.clip();
+        const int64_t into = first - f.at - p.item_weight;
+        some = f.clip(p, into > 0 ? into : 0) || f.next(p);
         found = f;
         break;
       }
-      at += static_cast<int64_t>(units) * per_seq;
+      at += static_cast<int64_t>(places) * per_seq;
     }
   }
   __syncthreads();
   *w = found;
-  return true;
+  return some;
 }
 
 // Rows of the warps' outputs in shared memory, in floats: conflict-free for the
@@ -285,7 +293,7 @@ __device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk& w
     int parts = 1;
     if (!whole) {
       // the item's last unit lies in the last of its shares
-      parts = static_cast<int>(last_boundary(share, w.u + s.units - 1) - blockIdx.x) + 1;
+      parts = static_cast<int>(last_boundary(share, w.at + p.item_weight + s.units - 1) - blockIdx.x) + 1;
       p.meta[blockIdx.x] = make_int4(s.b, s.j, parts, slot);
     }
     // (behind prefixes, parts < 0: no group names the sequence)

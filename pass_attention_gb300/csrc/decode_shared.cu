@@ -24,27 +24,34 @@ using namespace decode;
 
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
+// Rows (a sequence's query head) of a CTA. A tile's rows lie 16 bytes apart, 4 dims of each:
+// four neighbours make up two sectors. (One row a CTA took 14 us for 2048 rows of 11 parts,
+// every read half wasted and five dependent loads at the front; four rows RESULT.)
+constexpr int kJoinRows = 4;
 
 // What the first kernel has left.
 struct PrefixStates {
   const int4* where;
   const float4* part_o;  // [2 shares][D / 4][128]
   const float2* part_ml;
-  const float* state_o;
+  const float4* state_o;  // [batch][H][D / 4]
   const float2* state_ml;
   int32_t shares, packs, head_shift;
 };
 
-// CTA: one row (sequence, query head). Its warps take the parts in turn, first the
-// prefix's, then those of the own tokens; a lane holds D / 32 dims.
+// A warp takes every fourth part of its four rows, first the prefix's, then those of the
+// own tokens. Thread: row lane % 4, the vectors of 4 dims lane / 4, lane / 4 + 8, ...
 template <bool kF16, int D>
 __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const DecodeParams p, const PrefixStates x) {
-  constexpr int kDims = D / 32;
-  __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
+  constexpr int kVecs = D / 32;
+  __shared__ float2 sml[kJoinWarps][kJoinRows];
+  __shared__ float4 so[kJoinWarps][kJoinRows][D / 4 + 1];
   let_next_kernel_start();
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int64_t row = static_cast<int64_t>(b) * p.H + h;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d0 = lane * kDims;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v0 = lane >> 2;
+  const int64_t rows = static_cast<int64_t>(p.c.batch) * p.H;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinRows + (lane & 3);
+  const bool live = row < rows;
+  const int b = live ? static_cast<int>(row / p.H) : 0, h = live ? static_cast<int>(row - static_cast<int64_t>(b) * p.H) : 0;
   const int g = h / p.group, in_group = h - g * p.group, hb = in_group / p.block_heads;
   const int in_block = in_group - hb * p.block_heads;
   wait_for_previous_kernel();
@@ -61,88 +68,78 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
   } else {
     own.y = -own.y;  // no group names the sequence
   }
+  const int all = live ? parts + own.y : 0;
 
-  float M = neg_inf(), L = 0.f, acc[kDims];
+  float M = neg_inf(), L = 0.f;
+  float4 acc[kVecs];
 #pragma unroll
-  for (int k = 0; k < kDims; ++k) acc[k] = 0.f;
-  constexpr int kBatch = 4;
-  const int all = parts + own.y;
-  for (int i0 = warp; i0 < all; i0 += kJoinWarps * kBatch) {
-    float2 ml[kBatch];
-    float v[kBatch][kDims];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u * kJoinWarps;
-      ml[u] = make_float2(neg_inf(), 0.f);
-#pragma unroll
-      for (int k = 0; k < kDims; ++k) v[u][k] = 0.f;
-      if (i >= all) continue;
-      const float* src;
-      if (i < parts) {
-        if (!cut) {
-          ml[u] = x.state_ml[row];
-          src = x.state_o + row * D + d0;
-        } else {
-          const int64_t slot = 2 * (w.x + static_cast<int64_t>(i) * w.w) + (i == 0 ? 1 : 0);
-          ml[u] = x.part_ml[slot * 128 + tile_row];
-          // dims d0 .. of the vector of 4 that they lie in
-          src = reinterpret_cast<const float*>(x.part_o + (slot * (D / 4) + d0 / 4) * 128 + tile_row) + d0 % 4;
-        }
-      } else if (own.y == 1) {
-        ml[u] = p.state_ml[row];
-        src = p.state_o + row * D + d0;
+  for (int k = 0; k < kVecs; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = warp; i < all; i += kJoinWarps) {
+    float2 ml;
+    const float4* src;
+    int step = 8;  // vectors from one of this thread's to the next
+    if (i < parts) {
+      if (!cut) {
+        ml = x.state_ml[row];
+        src = x.state_o + row * (D / 4) + v0;
       } else {
-        const int64_t at = part_slot(own.x, i - parts) * p.block_heads + in_block;
-        ml[u] = p.part_ml[at];
-        src = p.part_o + at * D + d0;
+        const int64_t slot = 2 * (w.x + static_cast<int64_t>(i) * w.w) + (i == 0 ? 1 : 0);
+        ml = x.part_ml[slot * 128 + tile_row];
+        src = x.part_o + (slot * (D / 4) + v0) * 128 + tile_row;
+        step = 8 * 128;
       }
-      if constexpr (kDims == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src);
-        v[u][0] = y.x, v[u][1] = y.y, v[u][2] = y.z, v[u][3] = y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(src);
-        v[u][0] = y.x, v[u][1] = y.y;
-      }
+    } else if (own.y == 1) {
+      ml = p.state_ml[row];
+      src = reinterpret_cast<const float4*>(p.state_o) + row * (D / 4) + v0;
+    } else {
+      const int64_t at = part_slot(own.x, i - parts) * p.block_heads + in_block;
+      ml = p.part_ml[at];
+      src = reinterpret_cast<const float4*>(p.part_o) + at * (D / 4) + v0;
     }
-    float to = M;
+    float4 v[kVecs];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) to = fmaxf(to, ml[u].x);
-    const float ref = reference(to), corr = ex2(M - ref);
+    for (int k = 0; k < kVecs; ++k) v[k] = src[k * step];
+    const float to = fmaxf(M, ml.x), ref = reference(to), corr = ex2(M - ref), f = ex2(ml.x - ref);
     M = to;
-    L *= corr;
+    L = fmaf(ml.y, f, L * corr);
 #pragma unroll
-    for (int k = 0; k < kDims; ++k) acc[k] *= corr;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const float f = ex2(ml[u].x - ref);
-      L = fmaf(ml[u].y, f, L);
-#pragma unroll
-      for (int k = 0; k < kDims; ++k) acc[k] = fmaf(v[u][k], f, acc[k]);
+    for (int k = 0; k < kVecs; ++k) {
+      acc[k].x = fmaf(v[k].x, f, acc[k].x * corr);
+      acc[k].y = fmaf(v[k].y, f, acc[k].y * corr);
+      acc[k].z = fmaf(v[k].z, f, acc[k].z * corr);
+      acc[k].w = fmaf(v[k].w, f, acc[k].w * corr);
     }
   }
-  if (lane == 0) {
-    sm[warp] = M;
-    sl[warp] = L;
-  }
+  if (v0 == 0) sml[warp][lane & 3] = make_float2(M, L);
 #pragma unroll
-  for (int k = 0; k < kDims; ++k) so[warp][d0 + k] = acc[k];
+  for (int k = 0; k < kVecs; ++k) so[warp][lane & 3][v0 + 8 * k] = acc[k];
   __syncthreads();
-  if (threadIdx.x >= D / 2) return;
+  // warp: one of the rows; lane: D / 32 dims
+  const int64_t out = static_cast<int64_t>(blockIdx.x) * kJoinRows + warp;
+  if (out >= rows) return;
   M = neg_inf();
   L = 0.f;
-  float a = 0.f, c = 0.f;
+  float y[kVecs];
 #pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) M = fmaxf(M, sm[i]);
+  for (int k = 0; k < kVecs; ++k) y[k] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) M = fmaxf(M, sml[i][warp].x);
 #pragma unroll
   for (int i = 0; i < kJoinWarps; ++i) {
-    const float f = ex2(sm[i] - reference(M));
-    L = fmaf(sl[i], f, L);
-    a = fmaf(so[i][2 * threadIdx.x], f, a);
-    c = fmaf(so[i][2 * threadIdx.x + 1], f, c);
+    const float2 ml = sml[i][warp];
+    const float f = ex2(ml.x - reference(M)), *from = reinterpret_cast<const float*>(so[i][warp]) + lane * kVecs;
+    L = fmaf(ml.y, f, L);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) y[k] = fmaf(from[k], f, y[k]);
   }
   const float inv = L != 0.f ? 1.f / L : 0.f;
-  reinterpret_cast<uint32_t*>(p.o + row * D)[threadIdx.x] = pack2<kF16>(a * inv, c * inv);
-  if (threadIdx.x == 0 && p.lse) p.lse[row] = L != 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + out * D + lane * kVecs);
+  if constexpr (kVecs == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<kF16>(y[0] * inv, y[1] * inv), pack2<kF16>(y[2] * inv, y[3] * inv));
+  else
+    *dst = pack2<kF16>(y[0] * inv, y[1] * inv);
+  if (lane == 0 && p.lse) p.lse[out] = L != 0.f ? (M + log2f(L)) * kLn2 : neg_inf();
 }
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -187,16 +184,17 @@ cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t 
   p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
   p.state_o = reinterpret_cast<float*>(ws + pl.state_o);
   p.state_ml = reinterpret_cast<float2*>(ws + pl.state_ml);
+  p.item_weight = pl.own.whole ? 0 : kItemWeight;
   p.behind_prefix = 1;
   p.prefix = prefix;
   if ((e = launch_states(p, f16, cache.head_dim, pl.own.shares, stream)) != cudaSuccess) return e;
   const PrefixStates x{reinterpret_cast<const int4*>(ws + pl.prefix.where),
                        reinterpret_cast<const float4*>(ws + pl.prefix.part_o),
                        reinterpret_cast<const float2*>(ws + pl.prefix.part_ml),
-                       reinterpret_cast<const float*>(ws + pl.prefix.state_o),
+                       reinterpret_cast<const float4*>(ws + pl.prefix.state_o),
                        reinterpret_cast<const float2*>(ws + pl.prefix.state_ml),
                        pl.prefix.shares, pl.prefix.packs, pl.prefix.head_shift};
-  const dim3 grid(H, cache.batch);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(cache.batch) * H + kJoinRows - 1) / kJoinRows));
   const auto join = [&](auto* kernel) { return launch_after(kernel, grid, kJoinThreads, 0, stream, p, x); };
   if (cache.head_dim == 128)
     return f16 ? join(decode_shared_join_kernel<true, 128>) : join(decode_shared_join_kernel<false, 128>);
