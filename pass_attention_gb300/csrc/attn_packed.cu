@@ -225,6 +225,7 @@ struct Shares {
   ShareEnd end[kMaxRounds];
   ShareCut cut;
   Lanes lanes;
+  PackedSeq first;  // the sequence that the share begins in (prefix)
 };
 
 // (Prefix: sequence b is a group, its keys the group's prefix, and a tile one of every lane.)
@@ -272,6 +273,22 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x) {
 // idle in groups of fewer tiles; else 1. `sums` [3] is shared and cleared here.
 constexpr int kMaxLanes = 8;
 
+__device__ __forceinline__ int lane_count(int tiles) {
+  const int per = (tiles + kMaxLanes - 1) / kMaxLanes;
+  return (tiles + per - 1) / per;
+}
+
+// real, padded: steps of all tiles, and with the lanes' idle ones.
+__device__ __forceinline__ bool too_many_lanes(int lanes, int64_t real, int64_t padded) {
+  return lanes > static_cast<int>(gridDim.x) || padded * 4 > real * 5;
+}
+
+__device__ __forceinline__ void set_lane(Lanes* x) {
+  x->sets = gridDim.x / x->count;
+  x->set = blockIdx.x / x->count;
+  x->lane = static_cast<int>(blockIdx.x - x->set * x->count);
+}
+
 __device__ __forceinline__ Lanes find_lanes(const PackedParams& p, unsigned long long* sums) {
   Lanes x;
   if (threadIdx.x < 3) sums[threadIdx.x] = 0;
@@ -279,8 +296,7 @@ __device__ __forceinline__ Lanes find_lanes(const PackedParams& p, unsigned long
   OSS_ROLLED
   for (int b = threadIdx.x; b < p.batch; b += kThreads) atomicMax(&sums[0], static_cast<unsigned long long>(load_seq<true>(p, b, 1).tiles));
   __syncthreads();
-  const int most = max(1, static_cast<int>(sums[0])), per = (most + kMaxLanes - 1) / kMaxLanes;
-  x.count = (most + per - 1) / per;
+  x.count = lane_count(max(1, static_cast<int>(sums[0])));
   OSS_ROLLED
   for (int b = threadIdx.x; b < p.batch; b += kThreads) {
     const PackedSeq s = load_seq<true>(p, b, 1);
@@ -289,11 +305,69 @@ __device__ __forceinline__ Lanes find_lanes(const PackedParams& p, unsigned long
     atomicAdd(&sums[2], (s.tiles + x.count - 1) / x.count * x.count * steps);
   }
   __syncthreads();
-  if (x.count > static_cast<int>(gridDim.x) || sums[2] * 4 > sums[1] * 5) x.count = 1;
-  x.sets = gridDim.x / x.count;
-  x.set = blockIdx.x / x.count;
-  x.lane = static_cast<int>(blockIdx.x - x.set * x.count);
+  if (too_many_lanes(x.count, static_cast<int64_t>(sums[1]), static_cast<int64_t>(sums[2]))) x.count = 1;
+  set_lane(&x);
   return x;
+}
+
+// The same as find_shares, with the lanes, for up to 32 groups: a lane each, so one
+// way to memory and no CTA barrier until the end. Warp 0 looks for the share's beginning, warp
+// 1 for its end. (For one group, find_shares took 4.2 of the 16 us of a small launch.)
+__device__ __forceinline__ void find_prefix_share(const PackedParams& p, Shares* sh) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31, e = threadIdx.x >> 5;
+  if (e < 2) {
+    PackedSeq s = packed_seq(RowRange{0, 0, false}, RowRange{0, 0, false}, p.pos_shift);
+    if (lane < p.batch) s = load_seq<true>(p, lane, 1);
+    if (e == 0 && blockIdx.x == 0 && p.cu_q && lane < p.batch && row_range(p.cu_q[lane], p.cu_q[lane + 1], p.tokens_q).clamped)
+      report_error(p.err, kKernelPaged | (kSiteBadOffsets << 8));
+    const int places = kTileWeight + kv_tiles(s, 0, p.pos_shift, false);
+    const int32_t tiles = s.tiles;
+    Lanes x;
+    x.count = lane_count(max(1, __reduce_max_sync(kAll, tiles)));
+    s.tiles = (tiles + x.count - 1) / x.count;
+    const int64_t real = __shfl_sync(kAll, warp_scan(static_cast<int64_t>(tiles) * places), 31);
+    int64_t upto = warp_scan(static_cast<int64_t>(s.tiles) * places);
+    if (too_many_lanes(x.count, real, __shfl_sync(kAll, upto, 31) * x.count)) {
+      x.count = 1;
+      s.tiles = tiles;
+      upto = warp_scan(static_cast<int64_t>(tiles) * places);
+    }
+    set_lane(&x);
+    const int64_t mine = static_cast<int64_t>(s.tiles) * places, total = __shfl_sync(kAll, upto, 31) * p.packs;
+    const int64_t items = static_cast<int64_t>(__reduce_add_sync(kAll, static_cast<uint32_t>(s.tiles))) * p.packs;
+    const ShareCut cut = share_cut(total, share_count(total, items, x.sets, 1, kPrefixShareShift));
+    if (lane == 0 && e == 0) {
+      sh->cut = cut;
+      sh->lanes = x;
+    }
+    ShareStart start{0, 0, 0, 0, 0};
+    ShareEnd end{0, 0};
+    int k = 0;  // the group
+    if (x.set < cut.count) {
+      const int64_t at = share_begin(cut, x.set + e);
+      if (at == total) {
+        end = ShareEnd{total, 0};
+      } else {
+        k = __ffs(__ballot_sync(kAll, upto * p.packs > at)) - 1;
+        const int64_t len = __shfl_sync(kAll, mine, k), before = __shfl_sync(kAll, upto - mine, k) * p.packs;
+        const int each = __shfl_sync(kAll, places, k), steps = each - kTileWeight;
+        const int pack = small_quotient(at - before, len);
+        const int64_t in_pack = at - before - pack * len;
+        const int tile = small_quotient(in_pack, each);
+        const int64_t into = in_pack - static_cast<int64_t>(tile) * each, w = at - into;
+        const int step = cut_step(into, steps, kPrefixMinSteps);
+        start = ShareStart{w, k, pack, tile, step};
+        end = step == steps ? ShareEnd{w + each, 0} : ShareEnd{w, step};
+      }
+    }
+    if (e == 0 && lane == k) {
+      sh->start[0] = start;
+      sh->first = s;
+    }
+    if (e == 1 && lane == 0) sh->end[0] = end;
+  }
+  __syncthreads();
 }
 
 // Finds this CTA's shares. The sequences are cut into a run per warp, and each of
@@ -389,6 +463,7 @@ __device__ __forceinline__ void find_shares(const PackedParams& p, Shares* sh, i
     }
     if (lane == 0) {
       const int64_t w = before + place;
+      if (kPrefix && e == 0) sh->first = s;
       const int steps = kv_tiles(s, tile, p.pos_shift, causal);
       const int step = cut_step(at - w, steps, kPrefix ? kPrefixMinSteps : kMinSteps);
       if (e == 0)
@@ -431,13 +506,14 @@ struct Walk {
         if (++round >= p.rounds) return false;
         const ShareStart a = sh.start[round];
         w = a.w;
-        seq = a.seq - 1;
+        seq = kPrefix ? a.seq : a.seq - 1;
         pack = a.pack;
         tile = a.tile;
         s0 = a.step;
         end_w = sh.end[round].w;
         end_step = sh.end[round].step;
-        fetch = true;
+        fetch = !kPrefix;
+        if constexpr (kPrefix) s = sh.first;
         continue;
       }
       if (fetch) {
@@ -602,7 +678,10 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   // came before this one has ended. It waits for this one at its own end.)
   if constexpr (kPrefix) let_next_kernel_start();
   if (!kPrefix && threadIdx.x < p.rounds) p.meta[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
-  find_shares<kPrefix>(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
+  if (kPrefix && p.batch <= 32)
+    find_prefix_share(p, &shares);
+  else
+    find_shares<kPrefix>(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
   tc_fence_after();
   const uint32_t tbase = tmem_base_slot;
 
