@@ -226,15 +226,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
         for (int e = 0; e < 4; ++e) od[nt][i][e] = 0.f;
     }
     const int t_end = w.tile_end(p);
-    for (int t = s.r0 * p.unit_tiles + warp; t < t_end; t += kUnitTiles) {
-      copy_wait<kStages - 1>();
-      __syncwarp();
-      const uint32_t kt = ring + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes;
-      // lanes 0 .. 15: the keys' scales, 16 .. 31: the values' exponents
-      const uint32_t byte = scale_ring[stage * S::kScaleBytes + lane];
-      const float ev = byte == kFp8ScaleNan ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | byte) - 8388735.f;
-      const float sv = lane < 16 ? fp8_scale_value(byte) : ev;
-      float sc[NT][2][4];  // two sums: even and odd dims' chunks
+    // scores of the tile in a stage, before their factors; two sums: even and odd dims' chunks
+    auto products = [&](int st, float (&sc)[NT][2][4]) {
+      const uint32_t kt = ring + st * 2 * S::kTileBytes;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -251,6 +245,27 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
           for (int nt = 0; nt < NT; ++nt) mma16816<true>(sc[nt][half], a, qf[nt][2 * c + half][0], qf[nt][2 * c + half][1]);
         }
       }
+    };
+    float sc[NT][2][4];
+    int t = s.r0 * p.unit_tiles + warp;
+    if (t < t_end) {
+      copy_wait<kStages - 1>();
+      __syncwarp();
+      products(stage, sc);
+    }
+    for (; t < t_end; t += kUnitTiles) {
+      // the next tile's products beside this one's softmax (behind the segment's last
+      // tile: of whatever lies in the next stage, for nothing)
+      const int next_stage = stage + 1 == kStages ? 0 : stage + 1;
+      float ahead[NT][2][4];
+      copy_wait<kStages - 2>();
+      __syncwarp();
+      products(next_stage, ahead);
+      const uint32_t vt = ring + stage * 2 * S::kTileBytes + S::kTileBytes;
+      // lanes 0 .. 15: the keys' scales, 16 .. 31: the values' exponents
+      const uint32_t byte = scale_ring[stage * S::kScaleBytes + lane];
+      const float ev = byte == kFp8ScaleNan ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | byte) - 8388735.f;
+      const float sv = lane < 16 ? fp8_scale_value(byte) : ev;
       const float ka = __shfl_sync(0xffffffffu, sv, row8), kb = __shfl_sync(0xffffffffu, sv, row8 + 8);
       const float va = __shfl_sync(0xffffffffu, sv, row8 + 16), vb = __shfl_sync(0xffffffffu, sv, row8 + 24);
       float x[NT][4], y[NT][4];  // scores in base 2, and with the value's exponent
@@ -326,7 +341,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
       }
       __syncwarp();
       load(stage);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      stage = next_stage;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[nt][0][e] = ahead[nt][0][e];
+          sc[nt][1][e] = ahead[nt][1][e];
+        }
     }
     // ---- the four warps' states, 8 heads at a time
     const bool whole = s.r0 == 0 && s.r1 == s.units;
