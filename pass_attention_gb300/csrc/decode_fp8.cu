@@ -37,20 +37,17 @@ namespace {
 
 using namespace decode;
 
-#ifndef FP8_CTAS
-#define FP8_CTAS 3
-#endif
-#ifndef FP8_STAGES
-#define FP8_STAGES (kCtas == 3 ? 3 : 5)
-#endif
-constexpr int ctas_per_sm(int NT) { return NT == 1 ? FP8_CTAS : 2; }
+constexpr int ctas_per_sm(int NT) { return NT == 1 ? 3 : 2; }
 
 template <int D, int NT>
 struct Shape {
   static constexpr int kCtas = ctas_per_sm(NT);
-  static constexpr int kStages = FP8_STAGES * (128 / D);
-  static constexpr int kTileBytes = kTileKeys * D;   // K or V
-  static constexpr int kScaleBytes = 2 * kTileKeys;  // K's, then V's
+  static constexpr int kSub = 128 / D;               // blocks of 16 keys in a tile: 4 KB of K and V either way
+  static constexpr int kKeys = 16 * kSub;
+  static constexpr int kStages = kCtas == 2 ? 5 : 2 + kSub;  // what fits beside the merge buffer
+  static constexpr int kBlockBytes = 16 * D;         // 16 rows of K or V
+  static constexpr int kTileBytes = kKeys * D;       // K or V of a tile
+  static constexpr int kScaleBytes = 2 * kKeys;      // K's, then V's
   static constexpr int kRingBytes = kWarps * kStages * 2 * kTileBytes;
   static constexpr int kScaleRing = kWarps * kStages * kScaleBytes;
   static constexpr int kSmemBytes = kRingBytes + kScaleRing + kMergeBytes<D>;
@@ -73,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
   using S = Shape<D, NT>;
   constexpr int kChunks = D / 16;             // 16-byte chunks of a row
   constexpr int kRowsPerCopy = 32 / kChunks;  // rows a warp's copy instruction covers
-  constexpr int kStages = S::kStages;
+  constexpr int kStages = S::kStages, kSub = S::kSub;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float merge_m[kWarps][8], merge_l[kWarps][8];
   let_next_kernel_start();
@@ -81,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane & 3, row8 = lane >> 2;
 
-  Walk w;
+  Walk<S::kKeys> w;
   ShareCut share;
   const bool has_share = find_share(p, &w, &share);
   if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -94,10 +91,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
 
   // ---- the loads' cursor: the tile to be loaded next and its page, and what of its
   // address the segment decides
-  Walk lw = w;
+  Walk<S::kKeys> lw = w;
   int lt, lt_end;
   bool more = true;
-  int page = 0;
+  int page[kSub];
   const int32_t* row;
   int64_t head_at, scale_at;
   const int64_t lane_at = copy_row * p.c.ld_slot + copy_chunk * 16, copy_step = kRowsPerCopy * p.c.ld_slot;
@@ -115,45 +112,55 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
       if (!(more = lw.next(p))) return;
       enter();
     }
-    page = row[(lt * kTileKeys) >> p.c.page_shift];
+#pragma unroll
+    for (int b = 0; b < kSub; ++b) {
+      const int key = lt * S::kKeys + 16 * b;
+      page[b] = b == 0 || key < lw.s.len ? row[key >> p.c.page_shift] : 0;
+    }
   };
-  uint32_t bad = 0;  // stages whose tile has a page outside the pool
+  uint32_t bad = 0;  // a bit for every block of every stage: its page is outside the pool
   auto load = [&](int stage) {
     if (more) {
-      const int key0 = lt * kTileKeys, slot0 = key0 & slot_mask;
-      const int rows = lw.s.len - key0;  // rows of the tile that hold a token
-      const uint32_t dst = ring + stage * 2 * S::kTileBytes + chunk_at<D>(copy_row, copy_chunk);
-      const uint32_t sc = smem_u32(scale_ring) + stage * S::kScaleBytes + lane * kTileKeys;
-      // (rows kRowsPerCopy apart have the same swizzle but in D 128's second four of eight)
-      auto at_copy = [&](int i) { return D == 128 && (i & 1) ? (dst ^ 64) + i * kRowsPerCopy * D : dst + i * kRowsPerCopy * D; };
-      bad &= ~(1u << stage);
-      if (page_ok(page, p.c.num_pages)) {
-        const int64_t at = static_cast<int64_t>(page) * p.c.ld_page + head_at + slot0 * p.c.ld_slot;
-        const uint8_t *k = f.k + at, *v = f.v + at;
-        if (rows >= kTileKeys) {
 #pragma unroll
-          for (int i = 0; i < kTileKeys / kRowsPerCopy; ++i, k += copy_step, v += copy_step) {
-            copy16(at_copy(i), k);
-            copy16(at_copy(i) + S::kTileBytes, v);
+      for (int b = 0; b < kSub; ++b) {
+        const int key0 = lt * S::kKeys + 16 * b, slot0 = key0 & slot_mask;
+        const int rows = lw.s.len - key0;  // rows of the block that hold a token
+        const uint32_t dst = ring + stage * 2 * S::kTileBytes + b * S::kBlockBytes + chunk_at<D>(copy_row, copy_chunk);
+        const uint32_t sc = smem_u32(scale_ring) + stage * S::kScaleBytes + lane * S::kKeys + 16 * b;
+        const uint32_t bit = 1u << (stage * kSub + b);
+        // (rows kRowsPerCopy apart have the same swizzle but in D 128's second four of eight)
+        auto at_copy = [&](int i) { return D == 128 && (i & 1) ? (dst ^ 64) + i * kRowsPerCopy * D : dst + i * kRowsPerCopy * D; };
+        bad &= ~bit;
+        if (page_ok(page[b], p.c.num_pages) && rows > 0) {
+          const int64_t at = static_cast<int64_t>(page[b]) * p.c.ld_page + head_at + slot0 * p.c.ld_slot;
+          const uint8_t *k = f.k + at, *v = f.v + at;
+          if (rows >= 16) {
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsPerCopy; ++i, k += copy_step, v += copy_step) {
+              copy16(at_copy(i), k);
+              copy16(at_copy(i) + S::kTileBytes, v);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsPerCopy; ++i) {
+              const bool there = i * kRowsPerCopy + copy_row < rows;
+              copy16(at_copy(i), there ? k + i * copy_step : f.k, there);
+              copy16(at_copy(i) + S::kTileBytes, there ? v + i * copy_step : f.v, there);
+            }
           }
+          if (lane < 2) copy16(sc, (lane ? f.v_scales : f.k_scales) + page[b] * f.ld_page + scale_at + slot0);
         } else {
-#pragma unroll
-          for (int i = 0; i < kTileKeys / kRowsPerCopy; ++i) {
-            const bool there = i * kRowsPerCopy + copy_row < rows;
-            copy16(at_copy(i), there ? k + i * copy_step : f.k, there);
-            copy16(at_copy(i) + S::kTileBytes, there ? v + i * copy_step : f.v, there);
+          if (rows > 0) {
+            report_error(p.err, kKernelPaged | (kSiteBadPage << 8));
+            bad |= bit;
           }
-        }
-        if (lane < 2) copy16(sc, (lane ? f.v_scales : f.k_scales) + page * f.ld_page + scale_at + slot0);
-      } else {
-        report_error(p.err, kKernelPaged | (kSiteBadPage << 8));
-        bad |= 1u << stage;
 #pragma unroll
-        for (int i = 0; i < kTileKeys / kRowsPerCopy; ++i) {
-          copy16(at_copy(i), f.k, false);
-          copy16(at_copy(i) + S::kTileBytes, f.v, false);
+          for (int i = 0; i < 16 / kRowsPerCopy; ++i) {
+            copy16(at_copy(i), f.k, false);
+            copy16(at_copy(i) + S::kTileBytes, f.v, false);
+          }
+          if (lane < 2) copy16(sc, f.k_scales, false);
         }
-        if (lane < 2) copy16(sc, f.k_scales, false);
       }
       lt += kUnitTiles;
       settle();
@@ -227,26 +234,31 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
     }
     const int t_end = w.tile_end(p);
     // scores of the tile in a stage, before their factors; two sums: even and odd dims' chunks
-    auto products = [&](int st, float (&sc)[NT][2][4]) {
+    using Sums = float[kSub][NT][2][4];
+    auto products = [&](int st, Sums& sc) {
       const uint32_t kt = ring + st * 2 * S::kTileBytes;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int b = 0; b < kSub; ++b) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[4];
-        ldmatrix4(x, kt + chunk_at<D>(lane & 15, 2 * c + (lane >> 4)));
+          for (int e = 0; e < 4; ++e) sc[b][nt][0][e] = sc[b][nt][1][e] = 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t a[4] = {from_e4m3x2(x[2 * half]), from_e4m3x2(x[2 * half + 1]), from_e4m3x2(x[2 * half] >> 16),
-                                 from_e4m3x2(x[2 * half + 1] >> 16)};
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[4];
+          ldmatrix4(x, kt + b * S::kBlockBytes + chunk_at<D>(lane & 15, 2 * c + (lane >> 4)));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<true>(sc[nt][half], a, qf[nt][2 * c + half][0], qf[nt][2 * c + half][1]);
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t a[4] = {from_e4m3x2(x[2 * half]), from_e4m3x2(x[2 * half + 1]), from_e4m3x2(x[2 * half] >> 16),
+                                   from_e4m3x2(x[2 * half + 1] >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<true>(sc[b][nt][half], a, qf[nt][2 * c + half][0], qf[nt][2 * c + half][1]);
+          }
         }
       }
     };
-    float sc[NT][2][4];
+    Sums sc;
     int t = s.r0 * p.unit_tiles + warp;
     if (t < t_end) {
       copy_wait<kStages - 1>();
@@ -257,56 +269,78 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
       // the next tile's products beside this one's softmax (behind the segment's last
       // tile: of whatever lies in the next stage, for nothing)
       const int next_stage = stage + 1 == kStages ? 0 : stage + 1;
-      float ahead[NT][2][4];
+      Sums ahead;
       copy_wait<kStages - 2>();
       __syncwarp();
       products(next_stage, ahead);
       const uint32_t vt = ring + stage * 2 * S::kTileBytes + S::kTileBytes;
-      // lanes 0 .. 15: the keys' scales, 16 .. 31: the values' exponents
-      const uint32_t byte = scale_ring[stage * S::kScaleBytes + lane];
-      const float ev = byte == kFp8ScaleNan ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | byte) - 8388735.f;
-      const float sv = lane < 16 ? fp8_scale_value(byte) : ev;
-      const float ka = __shfl_sync(0xffffffffu, sv, row8), kb = __shfl_sync(0xffffffffu, sv, row8 + 8);
-      const float va = __shfl_sync(0xffffffffu, sv, row8 + 16), vb = __shfl_sync(0xffffffffu, sv, row8 + 24);
-      float x[NT][4], y[NT][4];  // scores in base 2, and with the value's exponent
+      // the keys' scales and the values' exponents, one to a lane: lanes 0 .. 15 and 16 .. 31
+      // have those of one block, or all lanes both of two
+      const uint8_t* bytes = scale_ring + stage * S::kScaleBytes + lane;
+      const float ks = fp8_scale_value(bytes[0]);
+      const uint32_t vb = bytes[kSub == 1 ? 0 : 32];
+      const float ev = vb == kFp8ScaleNan ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | vb) - 8388735.f;
+      float x[kSub][NT][4], y[kSub][NT][4];  // scores in base 2, and with the value's exponent
+      const int left = s.len - t * S::kKeys;  // keys from the tile's first one on
+#pragma unroll
+      for (int b = 0; b < kSub; ++b) {
+        float kf[2], vf[2];  // of keys row8 and row8 + 8
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          kf[r] = __shfl_sync(0xffffffffu, ks, 16 * b + 8 * r + row8);
+          vf[r] = __shfl_sync(0xffffffffu, ev, (kSub == 1 ? 16 : 16 * b) + 8 * r + row8);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[b][nt][e] = (sc[b][nt][0][e] + sc[b][nt][1][e]) * qs[nt][e & 1] * kf[e >> 1];
+            y[b][nt][e] = x[b][nt][e] + vf[e >> 1];
+          }
+      }
+      if (left < S::kKeys || bad) {  // some tile has a bad page, perhaps this one
+#pragma unroll
+        for (int b = 0; b < kSub; ++b) {
+          const int live = (bad >> (stage * kSub + b)) & 1u ? 0 : left - 16 * b;  // the block's rows that hold a token
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (row8 + (e < 2 ? 0 : 8) >= live) x[b][nt][e] = y[b][nt][e] = neg_inf();
+        }
+      }
+      float mx[NT][2], my[NT][2];  // this thread's largest
       bool rise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[nt][e] = (sc[nt][0][e] + sc[nt][1][e]) * qs[nt][e & 1] * (e < 2 ? ka : kb);
-          y[nt][e] = x[nt][e] + (e < 2 ? va : vb);
+        for (int e = 0; e < 2; ++e) {
+          mx[nt][e] = fmaxf(x[0][nt][e], x[0][nt][e + 2]);
+          my[nt][e] = fmaxf(y[0][nt][e], y[0][nt][e + 2]);
+#pragma unroll
+          for (int b = 1; b < kSub; ++b) {
+            mx[nt][e] = fmaxf(mx[nt][e], fmaxf(x[b][nt][e], x[b][nt][e + 2]));
+            my[nt][e] = fmaxf(my[nt][e], fmaxf(y[b][nt][e], y[b][nt][e + 2]));
+          }
+          rise |= mx[nt][e] > m[nt][e] + kSlack || my[nt][e] > mo[nt][e] + kSlack;
         }
-      if (t * kTileKeys + kTileKeys > s.len || bad) {  // some tile has a bad page, perhaps this one
-        const int live = (bad >> stage) & 1u ? 0 : s.len - t * kTileKeys;  // its rows that hold a token
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (row8 + (e < 2 ? 0 : 8) >= live) x[nt][e] = y[nt][e] = neg_inf();
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) rise |= x[nt][e] > m[nt][e & 1] + kSlack || y[nt][e] > mo[nt][e & 1] + kSlack;
       if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float corr[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(x[nt][e], x[nt][e + 2]), my = fmaxf(y[nt][e], y[nt][e + 2]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-              my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, off));
+              mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
+              my[nt][e] = fmaxf(my[nt][e], __shfl_xor_sync(0xffffffffu, my[nt][e], off));
             }
-            mx = fmaxf(mx, m[nt][e]);
-            my = fmaxf(my, mo[nt][e]);
-            l[nt][e] *= ex2(m[nt][e] - mx);
-            corr[e] = ex2(mo[nt][e] - my);
-            m[nt][e] = mx;
-            mo[nt][e] = my;
+            mx[nt][e] = fmaxf(mx[nt][e], m[nt][e]);
+            my[nt][e] = fmaxf(my[nt][e], mo[nt][e]);
+            l[nt][e] *= ex2(m[nt][e] - mx[nt][e]);
+            corr[e] = ex2(mo[nt][e] - my[nt][e]);
+            m[nt][e] = mx[nt][e];
+            mo[nt][e] = my[nt][e];
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
@@ -314,41 +348,47 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
             for (int e = 0; e < 4; ++e) od[nt][i][e] *= corr[e & 1];
         }
       }
-      uint32_t pf[NT][2];
+      uint32_t pf[kSub][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pe[4];
+      for (int b = 0; b < kSub; ++b)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          l[nt][e & 1] += ex2(x[nt][e] - m[nt][e & 1]);
-          pe[e] = ex2(y[nt][e] - mo[nt][e & 1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          float pe[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l[nt][e & 1] += ex2(x[b][nt][e] - m[nt][e & 1]);
+            pe[e] = ex2(y[b][nt][e] - mo[nt][e & 1]);
+          }
+          pf[b][nt][0] = transpose8x8(pack2<true>(pe[0], pe[1]));
+          pf[b][nt][1] = transpose8x8(pack2<true>(pe[2], pe[3]));
         }
-        pf[nt][0] = transpose8x8(pack2<true>(pe[0], pe[1]));
-        pf[nt][1] = transpose8x8(pack2<true>(pe[2], pe[3]));
-      }
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[4];
-        ldmatrix4_trans(v, vt + chunk_at<D>(lane & 15, 2 * c + (lane >> 4)));
+      for (int b = 0; b < kSub; ++b)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          // bytes {key, dim}: 00 01 10 11 -> 00 10 01 11
-          const uint32_t lo = __byte_perm(v[2 * half], 0, 0x3120), hi = __byte_perm(v[2 * half + 1], 0, 0x3120);
-          const uint32_t a[4] = {from_e4m3x2(lo), from_e4m3x2(lo >> 16), from_e4m3x2(hi), from_e4m3x2(hi >> 16)};
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[4];
+          ldmatrix4_trans(v, vt + b * S::kBlockBytes + chunk_at<D>(lane & 15, 2 * c + (lane >> 4)));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<true>(od[nt][2 * c + half], a, pf[nt][0], pf[nt][1]);
+          for (int half = 0; half < 2; ++half) {
+            // bytes {key, dim}: 00 01 10 11 -> 00 10 01 11
+            const uint32_t lo = __byte_perm(v[2 * half], 0, 0x3120), hi = __byte_perm(v[2 * half + 1], 0, 0x3120);
+            const uint32_t a[4] = {from_e4m3x2(lo), from_e4m3x2(lo >> 16), from_e4m3x2(hi), from_e4m3x2(hi >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<true>(od[nt][2 * c + half], a, pf[b][nt][0], pf[b][nt][1]);
+          }
         }
-      }
       __syncwarp();
       load(stage);
       stage = next_stage;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int b = 0; b < kSub; ++b)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[nt][0][e] = ahead[nt][0][e];
-          sc[nt][1][e] = ahead[nt][1][e];
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc[b][nt][0][e] = ahead[b][nt][0][e];
+            sc[b][nt][1][e] = ahead[b][nt][1][e];
+          }
     }
     // ---- the four warps' states, 8 heads at a time
     const bool whole = s.r0 == 0 && s.r1 == s.units;
@@ -416,6 +456,7 @@ cudaError_t launch_decode_paged_fp8(const uint16_t* q, int64_t ld_q_batch, int64
   if (!make_plan(H, cache.pages, ctas_of(H, cache.pages), false, &pl)) return cudaErrorInvalidDevice;
   DecodeParams p = decode_params(pl, paged_cache(cache.pages), q, ld_q_batch, ld_q_head, H, scale, o, lse, workspace, err);
   p.item_weight = pl.whole ? 0 : kItemWeight;
+  if (pl.whole) p.unit_tiles = kWholeKeysMany / (16 * 128 / cache.pages.head_dim);
   const Fp8Pools f = fp8_pools(cache);
   if (cache.pages.dtype == OS_DTYPE_F16)
     return cache.pages.head_dim == 128 ? launch_heads<true, 128>(p, f, pl.shares, stream)

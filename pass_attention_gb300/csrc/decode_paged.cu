@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane & 3, row8 = lane >> 2;
 
-  Walk w;
+  Walk<kTileKeys> w;
   ShareCut share;
   const bool has_share = find_share(p, &w, &share);
   if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   const int copy_row = lane / kChunks, copy_chunk = lane % kChunks;
 
   // ---- the loads' cursor: the tile to be loaded next, and its page
-  Walk lw = w;
+  Walk<kTileKeys> lw = w;
   int lt = lw.s.r0 * p.unit_tiles + warp;
   bool more = true;
   int page = 0;

@@ -126,6 +126,8 @@ struct Segment {
 // The walk of one CTA over its share of the row of items. An item takes
 // item_weight + units places of the row, and unit k of an item that begins at place `at`
 // lies at at + item_weight + k.
+// kKeys: keys of a tile.
+template <int kKeys>
 struct Walk {
   Segment s;
   int64_t at, end;  // where the segment's item and the share's end lie
@@ -133,7 +135,7 @@ struct Walk {
   // (an empty sequence has a unit, to be answered)
   __device__ __forceinline__ static int units_of(const DecodeParams& p, int len) {
     if (p.unit_tiles != kUnitTiles) return 1;
-    const int n = (len + kTileKeys * kUnitTiles - 1) / (kTileKeys * kUnitTiles);
+    const int n = (len + kKeys * kUnitTiles - 1) / (kKeys * kUnitTiles);
     return n > 0 ? n : 1;
   }
   // The segment from unit r0 of the item at hand; false when the share ends before that.
@@ -157,14 +159,16 @@ struct Walk {
   }
   // One past the last tile of the segment that holds a key.
   __device__ __forceinline__ int tile_end(const DecodeParams& p) const {
-    return min(s.r1 * p.unit_tiles, (s.len + kTileKeys - 1) / kTileKeys);
+    return min(s.r1 * p.unit_tiles, (s.len + kKeys - 1) / kKeys);
   }
 };
 
 // This CTA's share, from the lengths: every thread sums a run of sequences, a
 // block scan places the runs, and the thread whose run holds the first unit
 // finds the sequence in it. False when the CTA has no share.
-__device__ __forceinline__ bool find_share(const DecodeParams& p, Walk* w, ShareCut* share) {
+template <int kKeys>
+__device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys>* w, ShareCut* share) {
+  using Walk = decode::Walk<kKeys>;
   __shared__ int64_t warp_sum[kWarps];
   __shared__ Walk found;
   __shared__ bool some;  // a share may lie within an item's weight
@@ -286,7 +290,8 @@ __device__ __forceinline__ void merge_warps(const DecodeParams& p, const Segment
 // The part of an item that begins in this CTA's share: 2 blockIdx.x + 1, of others 2
 // blockIdx.x. Where the item begins and is cut, thread 0 leaves its number of
 // parts behind, for the join.
-__device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk& w, const ShareCut& share, bool whole) {
+template <int kKeys>
+__device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk<kKeys>& w, const ShareCut& share, bool whole) {
   const Segment& s = w.s;
   const int slot = 2 * blockIdx.x + (s.r0 == 0 ? 1 : 0);
   if (s.r0 == 0 && threadIdx.x == 0) {
