@@ -440,23 +440,23 @@ cudaError_t launch_heads(const DecodeParams& p, const Fp8Pools& f, int shares, c
   return e != cudaSuccess ? e : launch_join(p, kF16, D, shares, stream);
 }
 
-int ctas_of(int H, const os_paged_cache& c) { return ctas_per_sm(heads_of_block(H / c.heads) / 8); }
+bool fp8_plan(int H, const os_paged_cache& c, Plan* out) {
+  return make_plan(H, c, ctas_per_sm(heads_of_block(H / c.heads) / 8), 16 * 128 / c.head_dim, kItemWeight, false, out);
+}
 
 }  // namespace
 
 int64_t decode_paged_fp8_workspace_bytes(int H, const os_paged_cache& pages) {
   Plan pl;
-  return make_plan(H, pages, ctas_of(H, pages), false, &pl) ? pl.bytes : -1;
+  return fp8_plan(H, pages, &pl) ? pl.bytes : -1;
 }
 
 cudaError_t launch_decode_paged_fp8(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
                                     const os_paged_cache_fp8& cache, float scale, uint16_t* o, float* lse,
                                     void* workspace, unsigned int* err, cudaStream_t stream) {
   Plan pl;
-  if (!make_plan(H, cache.pages, ctas_of(H, cache.pages), false, &pl)) return cudaErrorInvalidDevice;
-  DecodeParams p = decode_params(pl, paged_cache(cache.pages), q, ld_q_batch, ld_q_head, H, scale, o, lse, workspace, err);
-  p.item_weight = pl.whole ? 0 : kItemWeight;
-  if (pl.whole) p.unit_tiles = kWholeKeysMany / (16 * 128 / cache.pages.head_dim);
+  if (!fp8_plan(H, cache.pages, &pl)) return cudaErrorInvalidDevice;
+  const DecodeParams p = decode_params(pl, paged_cache(cache.pages), q, ld_q_batch, ld_q_head, H, scale, o, lse, workspace, err);
   const Fp8Pools f = fp8_pools(cache);
   if (cache.pages.dtype == OS_DTYPE_F16)
     return cache.pages.head_dim == 128 ? launch_heads<true, 128>(p, f, pl.shares, stream)

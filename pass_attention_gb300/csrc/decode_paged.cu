@@ -497,18 +497,24 @@ cudaError_t launch_decode(const DecodeParams& p, bool f16, int D, int shares, fl
 
 namespace decode {
 
-bool make_plan(int H, const os_paged_cache& c, int ctas_per_sm, bool weights, Plan* out) {
+bool make_plan(int H, const os_paged_cache& c, int ctas, int tile_keys, int item_weight, bool weights, Plan* out) {
   const int sms = device_sms();
   if (sms < 1) return false;
   const int group = H / c.heads;
   Plan pl;
-  pl.shares = sms * ctas_per_sm;
   pl.block_heads = heads_of_block(group);
   pl.head_blocks = (group + pl.block_heads - 1) / pl.block_heads;
   pl.score_heads = pl.head_blocks > 1 ? pl.block_heads : (group + 3) / 4 * 4;
   const int64_t capacity = static_cast<int64_t>(c.max_pages) * c.page_size;
   const int64_t items = static_cast<int64_t>(c.batch) * c.heads * pl.head_blocks;
+  pl.shares = sms * ctas;
   pl.whole = capacity <= kWholeKeys || (capacity <= kWholeKeysMany && items >= pl.shares);
+  pl.unit_tiles = pl.whole ? kWholeKeysMany / tile_keys : kUnitTiles;
+  pl.item_weight = pl.whole ? 0 : item_weight;
+  // no more than there are places in the row of items, if every sequence fills its pages
+  const int64_t unit = static_cast<int64_t>(tile_keys) * pl.unit_tiles;
+  const int64_t places = items * ((capacity + unit - 1) / unit + pl.item_weight);
+  if (pl.shares > places) pl.shares = static_cast<int>(places);
   int64_t at = 0;
   auto take = [&](int64_t n) {
     const int64_t here = at;
@@ -542,7 +548,8 @@ DecodeParams decode_params(const Plan& pl, const PagedCache& c, const uint16_t* 
   p.group = H / c.heads;
   p.head_blocks = pl.head_blocks;
   p.block_heads = pl.block_heads;
-  p.unit_tiles = pl.whole ? kWholeKeysMany / kTileKeys : kUnitTiles;
+  p.unit_tiles = pl.unit_tiles;
+  p.item_weight = pl.item_weight;
   p.score_heads = pl.score_heads;
   p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.o = o;
@@ -568,7 +575,7 @@ cudaError_t launch_join(const DecodeParams& p, bool f16, int D, int shares, cuda
 
 int64_t decode_paged_workspace_bytes(int H, const os_paged_cache& cache, bool weights) {
   Plan pl;
-  return make_plan(H, cache, kCtasPerSm, weights, &pl) ? pl.bytes : -1;
+  return make_plan(H, cache, kCtasPerSm, kTileKeys, 0, weights, &pl) ? pl.bytes : -1;
 }
 
 cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
@@ -576,7 +583,7 @@ cudaError_t launch_decode_paged(const uint16_t* q, int64_t ld_q_batch, int64_t l
                                 float* weights, int64_t ld_w_batch, int64_t ld_w_head,
                                 void* workspace, unsigned int* err, cudaStream_t stream) {
   Plan pl;
-  if (!make_plan(H, cache, kCtasPerSm, weights != nullptr, &pl)) return cudaErrorInvalidDevice;
+  if (!make_plan(H, cache, kCtasPerSm, kTileKeys, 0, weights != nullptr, &pl)) return cudaErrorInvalidDevice;
   DecodeParams p = decode_params(pl, paged_cache(cache), q, ld_q_batch, ld_q_head, H, scale, o, lse, workspace, err);
   if (weights) {
     char* ws = static_cast<char*>(workspace);

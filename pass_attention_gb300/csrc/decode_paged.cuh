@@ -315,7 +315,7 @@ __device__ __forceinline__ int64_t part_slot(int c, int i) {
 
 // Layout of the workspace, the same for its size and its use.
 struct Plan {
-  int shares, block_heads, head_blocks, score_heads;
+  int shares, block_heads, head_blocks, score_heads, unit_tiles, item_weight;
   bool whole;  // items are not cut
   int64_t part_o, part_ml, meta, lse2, item_meta, scores, bytes;  // offsets, then the size
 };
@@ -325,7 +325,9 @@ inline int heads_of_block(int group) { return group <= 8 ? 8 : kMaxHeadBlock; }
 
 // What the plan adds to the cache's tables: the parts of cut items, and optionally the scores
 // and what else the weights' sums need.
-bool make_plan(int H, const os_paged_cache& c, int ctas_per_sm, bool weights, Plan* out);
+// (ctas: of an SM; tile_keys: of the kernel's Walk; item_weight: as in DecodeParams, of items
+// that may be cut.)
+bool make_plan(int H, const os_paged_cache& c, int ctas, int tile_keys, int item_weight, bool weights, Plan* out);
 
 // The parameters of a launch that writes o and lse, without weights and states.
 DecodeParams decode_params(const Plan& pl, const PagedCache& c, const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head,

@@ -152,7 +152,7 @@ struct SharedPlan {
 };
 
 bool make_shared_plan(int H, const os_paged_cache& c, SharedPlan* out) {
-  if (!make_plan(H, c, kCtasPerSm, false, &out->own)) return false;
+  if (!make_plan(H, c, kCtasPerSm, kTileKeys, kItemWeight, false, &out->own)) return false;
   out->prefix = prefix_plan(H, c);
   const int64_t rows = static_cast<int64_t>(c.batch) * H;
   out->own_at = out->prefix.bytes;
@@ -184,7 +184,6 @@ cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t 
   p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
   p.state_o = reinterpret_cast<float*>(ws + pl.state_o);
   p.state_ml = reinterpret_cast<float2*>(ws + pl.state_ml);
-  p.item_weight = pl.own.whole ? 0 : kItemWeight;
   p.behind_prefix = 1;
   p.prefix = prefix;
   if ((e = launch_states(p, f16, cache.head_dim, pl.own.shares, stream)) != cudaSuccess) return e;
