@@ -56,6 +56,7 @@
 #include "launch.cuh"
 #include "oss_internal.h"
 #include "packed_plan.h"
+#include "prefix_split.cuh"
 #include "tcgen05.cuh"
 
 namespace oss {
@@ -98,8 +99,10 @@ struct Smem {
 // What the prefix kernels read and write beside the others' parameters: KV tiles come
 // from pages, and states go to a join with the sequences' own tokens.
 struct PrefixOut {
-  PrefixTables tables;
-  int32_t num_pages, page_shift, box_shift;  // a TMA box: 2^box_shift slots of a page
+  PrefixLaunch launch;
+  const int32_t* kv_len;  // of the sequences' own tokens
+  int32_t own_max_pages;
+  int32_t num_pages, box_shift;  // a TMA box: 2^box_shift slots of a page
   int4* where;      // [tokens_q][packs]: {first slot / 2, parts (0: not cut), row of the first head in the tile, lanes}
   float* state_o;   // [tokens_q][Hq][D]: unnormalised O of items that are not cut
   float2* state_ml;  // [tokens_q][Hq]
@@ -200,16 +203,6 @@ struct Barriers {
   uint64_t drain[2];
 };
 
-// Lanes (prefix; others: 1 of 1). With several query tiles on one prefix, `count` CTAs take the
-// same shares, each with a tile of its own (tile number at * count + lane), and so
-// read the same K and V at the same time, which then come from HBM once. As items of their
-// own the tiles were half a share apart: 64 sequences, 4 heads a key head, behind 65536
-// tokens read the prefix's 268 MB twice (87 us, the kernel alone).
-struct Lanes {
-  int32_t count, lane;
-  uint32_t sets, set;  // sets of `count` CTAs, and this CTA's
-};
-
 // Where a share begins and ends: the item at place w of the row of items, and
 // the KV step inside it.
 struct ShareStart {
@@ -232,9 +225,8 @@ struct Shares {
 template <bool kPrefix>
 __device__ __forceinline__ PackedSeq load_seq(const PackedParams& p, int b, int lanes) {
   if constexpr (kPrefix) {
-    const PrefixTables& t = p.prefix.tables;
-    const RowRange q = p.cu_q ? row_range(p.cu_q[b], p.cu_q[b + 1], p.tokens_q) : RowRange{0, p.tokens_q, false};
-    PackedSeq s = packed_seq(q, RowRange{0, paged_length(t.len[b], t.max_pages, p.prefix.page_shift), false}, p.pos_shift);
+    const PrefixLaunch& x = p.prefix.launch;
+    PackedSeq s = prefix_seq(x.tables, b, x.batch, x.page_shift, x.pos_shift);
     s.tiles = (s.tiles + lanes - 1) / lanes;
     return s;
   }
@@ -257,101 +249,64 @@ __device__ __forceinline__ int64_t run_length(const PackedParams& p, int lanes, 
   return sum;
 }
 
-// Inclusive scan over a warp.
-__device__ __forceinline__ int64_t warp_scan(int64_t x) {
-  const int lane = threadIdx.x & 31;
-  OSS_ROLLED
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
-  }
-  return x;
-}
-
-// The lanes of a prefix launch: as many as the group with the most tiles has, up to 8 (beyond
-// that in equal shares of its tiles), if that leaves at most a fifth of the CTAs' time
-// idle in groups of fewer tiles; else 1. `sums` [3] is shared and cleared here.
-constexpr int kMaxLanes = 8;
-
-__device__ __forceinline__ int lane_count(int tiles) {
-  const int per = (tiles + kMaxLanes - 1) / kMaxLanes;
-  return (tiles + per - 1) / per;
-}
-
-// real, padded: steps of all tiles, and with the lanes' idle ones.
-__device__ __forceinline__ bool too_many_lanes(int lanes, int64_t real, int64_t padded) {
-  return lanes > static_cast<int>(gridDim.x) || padded * 4 > real * 5;
-}
-
-__device__ __forceinline__ void set_lane(Lanes* x) {
-  x->sets = gridDim.x / x->count;
-  x->set = blockIdx.x / x->count;
-  x->lane = static_cast<int>(blockIdx.x - x->set * x->count);
-}
-
+// The lanes where a warp does not hold the groups. `sums` [3] is shared and cleared here.
 __device__ __forceinline__ Lanes find_lanes(const PackedParams& p, unsigned long long* sums) {
-  Lanes x;
   if (threadIdx.x < 3) sums[threadIdx.x] = 0;
   __syncthreads();
   OSS_ROLLED
   for (int b = threadIdx.x; b < p.batch; b += kThreads) atomicMax(&sums[0], static_cast<unsigned long long>(load_seq<true>(p, b, 1).tiles));
   __syncthreads();
-  x.count = lane_count(max(1, static_cast<int>(sums[0])));
+  int count = lane_count(max(1, static_cast<int>(sums[0])));
   OSS_ROLLED
   for (int b = threadIdx.x; b < p.batch; b += kThreads) {
     const PackedSeq s = load_seq<true>(p, b, 1);
     const unsigned long long steps = kTileWeight + kv_tiles(s, 0, p.pos_shift, false);
     atomicAdd(&sums[1], s.tiles * steps);
-    atomicAdd(&sums[2], (s.tiles + x.count - 1) / x.count * x.count * steps);
+    atomicAdd(&sums[2], (s.tiles + count - 1) / count * count * steps);
   }
   __syncthreads();
-  if (too_many_lanes(x.count, static_cast<int64_t>(sums[1]), static_cast<int64_t>(sums[2]))) x.count = 1;
-  set_lane(&x);
-  return x;
+  if (too_many_lanes(count, gridDim.x, static_cast<int64_t>(sums[1]), static_cast<int64_t>(sums[2]))) count = 1;
+  return this_lane(count, gridDim.x / count);
 }
 
-// The same as find_shares, with the lanes, for up to 32 groups: a lane each, so one
-// way to memory and no CTA barrier until the end. Warp 0 looks for the share's beginning, warp
-// 1 for its end. (For one group, find_shares took 4.2 of the 16 us of a small launch.)
-__device__ __forceinline__ void find_prefix_share(const PackedParams& p, Shares* sh) {
+// The same as find_shares, for up to kWarpGroups groups: one way to memory and two CTA
+// barriers. Warp 0 looks for the share's beginning, warp 1 for its end. (find_shares took
+// 4.2 of the 16 us of a small launch of one group.) `scratch` [kThreads / 32].
+__device__ __forceinline__ void find_prefix_share(const PackedParams& p, Shares* sh, int64_t* scratch) {
   constexpr uint32_t kAll = 0xffffffffu;
-  const int lane = threadIdx.x & 31, e = threadIdx.x >> 5;
-  if (e < 2) {
-    PackedSeq s = packed_seq(RowRange{0, 0, false}, RowRange{0, 0, false}, p.pos_shift);
-    if (lane < p.batch) s = load_seq<true>(p, lane, 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = warp;
+  const PrefixLaunch& x = p.prefix.launch;
+  PackedSeq s = packed_seq(RowRange{0, 0, false}, RowRange{0, 0, false}, p.pos_shift);
+  if (warp < 2 && lane < p.batch) s = prefix_seq(x.tables, lane, x.batch, x.page_shift, x.pos_shift);
+  int64_t own = 0;
+  OSS_ROLLED
+  for (int b = threadIdx.x; x.bytes_cost > 0 && b < x.batch; b += kThreads)
+    own += own_units(paged_length(p.prefix.kv_len[b], p.prefix.own_max_pages, x.page_shift));
+  own = warp_scan(own);
+  if (lane == 31) scratch[warp] = own;
+  __syncthreads();
+  if (warp < 2) {
+    own = __shfl_sync(kAll, warp_scan(lane < kThreads / 32 ? scratch[lane] : 0), 31) * x.per_seq;
     if (e == 0 && blockIdx.x == 0 && p.cu_q && lane < p.batch && row_range(p.cu_q[lane], p.cu_q[lane + 1], p.tokens_q).clamped)
       report_error(p.err, kKernelPaged | (kSiteBadOffsets << 8));
-    const int places = kTileWeight + kv_tiles(s, 0, p.pos_shift, false);
-    const int32_t tiles = s.tiles;
-    Lanes x;
-    x.count = lane_count(max(1, __reduce_max_sync(kAll, tiles)));
-    s.tiles = (tiles + x.count - 1) / x.count;
-    const int64_t real = __shfl_sync(kAll, warp_scan(static_cast<int64_t>(tiles) * places), 31);
-    int64_t upto = warp_scan(static_cast<int64_t>(s.tiles) * places);
-    if (too_many_lanes(x.count, real, __shfl_sync(kAll, upto, 31) * x.count)) {
-      x.count = 1;
-      s.tiles = tiles;
-      upto = warp_scan(static_cast<int64_t>(tiles) * places);
-    }
-    set_lane(&x);
-    const int64_t mine = static_cast<int64_t>(s.tiles) * places, total = __shfl_sync(kAll, upto, 31) * p.packs;
-    const int64_t items = static_cast<int64_t>(__reduce_add_sync(kAll, static_cast<uint32_t>(s.tiles))) * p.packs;
-    const ShareCut cut = share_cut(total, share_count(total, items, x.sets, 1, kPrefixShareShift));
+    const PrefixDivision d = divide_prefix(x, s, own);
+    const Lanes lanes = this_lane(d.count, d.sets);
     if (lane == 0 && e == 0) {
-      sh->cut = cut;
-      sh->lanes = x;
+      sh->cut = d.cut;
+      sh->lanes = lanes;
     }
     ShareStart start{0, 0, 0, 0, 0};
     ShareEnd end{0, 0};
     int k = 0;  // the group
-    if (x.set < cut.count) {
-      const int64_t at = share_begin(cut, x.set + e);
-      if (at == total) {
-        end = ShareEnd{total, 0};
+    if (lanes.set < d.cut.count) {
+      const int64_t at = share_begin(d.cut, lanes.set + e);
+      if (at == d.total) {
+        end = ShareEnd{d.total, 0};
       } else {
-        k = __ffs(__ballot_sync(kAll, upto * p.packs > at)) - 1;
-        const int64_t len = __shfl_sync(kAll, mine, k), before = __shfl_sync(kAll, upto - mine, k) * p.packs;
-        const int each = __shfl_sync(kAll, places, k), steps = each - kTileWeight;
+        k = __ffs(__ballot_sync(kAll, d.upto * p.packs > at)) - 1;
+        const int64_t mine = static_cast<int64_t>(d.s.tiles) * d.places;
+        const int64_t len = __shfl_sync(kAll, mine, k), before = __shfl_sync(kAll, d.upto - mine, k) * p.packs;
+        const int each = __shfl_sync(kAll, d.places, k), steps = each - kTileWeight;
         const int pack = small_quotient(at - before, len);
         const int64_t in_pack = at - before - pack * len;
         const int tile = small_quotient(in_pack, each);
@@ -363,7 +318,7 @@ __device__ __forceinline__ void find_prefix_share(const PackedParams& p, Shares*
     }
     if (e == 0 && lane == k) {
       sh->start[0] = start;
-      sh->first = s;
+      sh->first = d.s;
     }
     if (e == 1 && lane == 0) sh->end[0] = end;
   }
@@ -591,7 +546,7 @@ constexpr int kBadRing = 8;  // steps whose masks of bad pages are kept: no read
 __device__ __forceinline__ int piece_page(const PrefixOut& x, int group, int tile, int k_len, uint32_t* bad) {
   const int lane = threadIdx.x & 31, key = tile * kBN + (lane << x.box_shift);
   const bool mine = lane < (kBN >> x.box_shift) && key < k_len;
-  const int page = mine ? x.tables.table[group * x.tables.ld_table + (key >> x.page_shift)] : x.num_pages;
+  const int page = mine ? x.launch.tables.table[group * x.launch.tables.ld_table + (key >> x.launch.page_shift)] : x.num_pages;
   const bool ok = page_ok(page, x.num_pages);
   const uint32_t pieces = __ballot_sync(0xffffffffu, mine && !ok);
   *bad = __ballot_sync(0xffffffffu, lane < kBN / 16 && ((pieces >> (lane >> (x.box_shift - 4))) & 1u));
@@ -607,7 +562,7 @@ __device__ __forceinline__ void load_piece(const PrefixOut& x, const CUtensorMap
   if (lane == 0) mbar_expect_tx(bar, (D / 64) * kHalf);
   __syncwarp();
   if (lane < (kBN >> x.box_shift)) {
-    const int slot = (tile * kBN) & ((1 << x.page_shift) - 1);  // 0 for pages of a tile or less
+    const int slot = (tile * kBN) & ((1 << x.launch.page_shift) - 1);  // 0 for pages of a tile or less
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) tma_load_4d(dst + h * kHalf + (lane << (x.box_shift + 7)), map, bar, h * 64, slot, head, page);
   }
@@ -678,8 +633,8 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   // came before this one has ended. It waits for this one at its own end.)
   if constexpr (kPrefix) let_next_kernel_start();
   if (!kPrefix && threadIdx.x < p.rounds) p.meta[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (kPrefix && p.batch <= 32)
-    find_prefix_share(p, &shares);
+  if (kPrefix && p.batch <= kWarpGroups)
+    find_prefix_share(p, &shares, reinterpret_cast<int64_t*>(row_ml));
   else
     find_shares<kPrefix>(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
   tc_fence_after();
@@ -1485,7 +1440,7 @@ PrefixPlan prefix_plan(int H, const os_paged_cache& c) {
 }
 
 cudaError_t launch_attn_prefix(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H, const os_paged_cache& c,
-                               const PrefixTables& tables, float scale, const PrefixPlan& pl, void* workspace,
+                               const PrefixLaunch& x, float scale, const PrefixPlan& pl, void* workspace,
                                unsigned int* err, const AttnFault& fault, cudaStream_t stream) {
   const int sms = device_sms();
   if (sms < 1) return cudaErrorInvalidDevice;
@@ -1500,8 +1455,8 @@ cudaError_t launch_attn_prefix(const uint16_t* q, int64_t ld_q_batch, int64_t ld
     return cudaErrorInvalidValue;
   char* ws = static_cast<char*>(workspace);
   PackedParams p = {};
-  p.cu_q = tables.cu;
-  p.batch = tables.groups;
+  p.cu_q = x.tables.cu;
+  p.batch = x.tables.groups;
   p.tokens_q = c.batch;
   p.Hq = H;
   p.packs = pl.packs;
@@ -1514,9 +1469,10 @@ cudaError_t launch_attn_prefix(const uint16_t* q, int64_t ld_q_batch, int64_t ld
   p.skip_v_step = fault.skip_v_step;
   p.part_o = reinterpret_cast<float4*>(ws + pl.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
-  p.prefix.tables = tables;
+  p.prefix.launch = x;
+  p.prefix.kv_len = c.kv_len;
+  p.prefix.own_max_pages = c.max_pages;
   p.prefix.num_pages = c.num_pages;
-  while ((1 << p.prefix.page_shift) < c.page_size) ++p.prefix.page_shift;
   while ((1 << p.prefix.box_shift) < box_rows) ++p.prefix.box_shift;
   p.prefix.where = reinterpret_cast<int4*>(ws + pl.where);
   p.prefix.state_o = reinterpret_cast<float*>(ws + pl.state_o);

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   const bool has_share = find_share(p, &w, &share);
   if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (!has_share) {
-    if (p.behind_prefix) wait_for_previous_kernel();
+    if (p.behind_prefix && blockIdx.x == 0) wait_for_previous_kernel();
     return;
   }
 
@@ -288,7 +288,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
     go = w.next(p);
   }
   copy_wait<0>();
-  if (p.behind_prefix) wait_for_previous_kernel();
+  // (behind prefixes: this kernel ends when its first CTA has seen the one before it end. The
+  // others leave, so that CTAs without a share do not wait for a place on an SM.)
+  if (p.behind_prefix && blockIdx.x == 0) wait_for_previous_kernel();
 }
 
 // The second kernel. With weights, its first CTAs add up: kAddKeys keys of one key

@@ -11,6 +11,7 @@
 #include "oss_internal.h"
 #include "packed_plan.h"
 #include "paged.h"
+#include "prefix_split.cuh"
 
 namespace oss {
 namespace decode {
@@ -59,9 +60,9 @@ struct DecodeParams {
   float* lse2;      // [batch][H], base 2: of items that were not cut (only with scores)
   int2* item_meta;  // [batch][heads * head_blocks]: {first share, parts}, or null
   // of the decode behind shared prefixes: the kernel before this one writes nothing that this one
-  // reads, so it is waited for at the end
+  // reads, so it is waited for at the end, by the first CTA
   int32_t behind_prefix;
-  PrefixTables prefix;
+  PrefixLaunch prefix;
   float* state_o;   // [batch][H][D]: O of whole items instead of o, or null
   float2* state_ml;  // [batch][H]: m, l
   float* scores;    // [batch][heads * head_blocks][capacity][score_heads], or null
@@ -175,9 +176,16 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys>* w
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.c.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.c.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.c.batch, b0 + per);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b)
-    mine += Walk::units_of(p, paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift)) + p.item_weight;
+  int64_t mine = 0, own = 0;
+  PackedSeq group = packed_seq(RowRange{0, 0, false}, RowRange{0, 0, false}, 0);
+  const bool split = p.behind_prefix && p.prefix.bytes_cost > 0 && p.prefix.tables.groups <= kWarpGroups;  // SMs are left to the prefixes
+  if (split && threadIdx.x < p.prefix.tables.groups)
+    group = prefix_seq(p.prefix.tables, threadIdx.x, p.prefix.batch, p.prefix.page_shift, p.prefix.pos_shift);
+  for (int b = b0; b < b1; ++b) {
+    const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
+    mine += Walk::units_of(p, len) + p.item_weight;
+    own += own_units(len);
+  }
   int64_t upto = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -194,7 +202,25 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys>* w
   }
   const int per_seq = p.c.heads * p.head_blocks;
   const int64_t W = all * per_seq;
-  const ShareCut cut = share_cut(W, W < gridDim.x ? static_cast<int>(W) : static_cast<int>(gridDim.x));
+  int ctas = gridDim.x;
+  if (split) {
+    __shared__ int64_t warp_own[kWarps];
+    __shared__ int left;
+    own = warp_scan(own);
+    if (lane == 31) warp_own[warp] = own;
+    __syncthreads();
+    if (warp == 0) {
+      own = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) own += warp_own[i];
+      const PrefixDivision d = divide_prefix(p.prefix, group, own * p.prefix.per_seq);
+      if (lane == 0) left = d.split ? p.prefix.sms - static_cast<int>(d.cut.count) * d.count : 0;
+    }
+    __syncthreads();
+    // (0: the own tokens come behind the prefixes, on every SM)
+    if (left > 0) ctas = min(ctas, kCtasPerSm * left);
+  }
+  const ShareCut cut = share_cut(W, W < ctas ? static_cast<int>(W) : ctas);
   *share = cut;
   if (blockIdx.x >= cut.count) return false;
   const int64_t first = share_begin(cut, blockIdx.x), last = share_begin(cut, blockIdx.x + 1);
@@ -302,7 +328,7 @@ __device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk<kK
       p.meta[blockIdx.x] = make_int4(s.b, s.j, parts, slot);
     }
     // (behind prefixes, parts < 0: no group names the sequence)
-    if (p.behind_prefix && prefix_group(p.prefix, s.b) < 0) parts = -parts;
+    if (p.behind_prefix && prefix_group(p.prefix.tables, s.b) < 0) parts = -parts;
     if (p.item_meta) p.item_meta[static_cast<int64_t>(s.b) * p.c.heads * p.head_blocks + s.j] = make_int2(blockIdx.x, parts);
   }
   return slot;

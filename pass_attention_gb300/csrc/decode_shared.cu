@@ -177,24 +177,30 @@ cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t 
   SharedPlan pl;
   if (!make_shared_plan(H, cache, &pl)) return cudaErrorInvalidDevice;
   char* ws = static_cast<char*>(workspace);
-  cudaError_t e = launch_attn_prefix(q, ld_q_batch, ld_q_head, H, cache, prefix, scale, pl.prefix, ws, err, fault, stream);
+  const PagedCache c = paged_cache(cache);
+  const PrefixLaunch x{prefix, cache.batch, c.page_shift, 7 - pl.prefix.head_shift, pl.prefix.packs, device_sms(),
+                       cache.heads * pl.own.head_blocks,
+                       cache.head_dim == 128 ? kStepCost : kStepCost64,
+                       pl.own.block_heads > 8 ? kWideUnitCost : cache.head_dim == 128 ? kUnitCost : kUnitCost64,
+                       pl.own.whole ? 0 : kUnitBytesCost * cache.head_dim / 128};
+  cudaError_t e = launch_attn_prefix(q, ld_q_batch, ld_q_head, H, cache, x, scale, pl.prefix, ws, err, fault, stream);
   if (e != cudaSuccess) return e;
   const bool f16 = cache.dtype == OS_DTYPE_F16;
-  DecodeParams p = decode_params(pl.own, paged_cache(cache), q, ld_q_batch, ld_q_head, H, scale, o, lse, ws + pl.own_at, err);
+  DecodeParams p = decode_params(pl.own, c, q, ld_q_batch, ld_q_head, H, scale, o, lse, ws + pl.own_at, err);
   p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
   p.state_o = reinterpret_cast<float*>(ws + pl.state_o);
   p.state_ml = reinterpret_cast<float2*>(ws + pl.state_ml);
   p.behind_prefix = 1;
-  p.prefix = prefix;
+  p.prefix = x;
   if ((e = launch_states(p, f16, cache.head_dim, pl.own.shares, stream)) != cudaSuccess) return e;
-  const PrefixStates x{reinterpret_cast<const int4*>(ws + pl.prefix.where),
+  const PrefixStates states{reinterpret_cast<const int4*>(ws + pl.prefix.where),
                        reinterpret_cast<const float4*>(ws + pl.prefix.part_o),
                        reinterpret_cast<const float2*>(ws + pl.prefix.part_ml),
                        reinterpret_cast<const float4*>(ws + pl.prefix.state_o),
                        reinterpret_cast<const float2*>(ws + pl.prefix.state_ml),
                        pl.prefix.shares, pl.prefix.packs, pl.prefix.head_shift};
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(cache.batch) * H + kJoinRows - 1) / kJoinRows));
-  const auto join = [&](auto* kernel) { return launch_after(kernel, grid, kJoinThreads, 0, stream, p, x); };
+  const auto join = [&](auto* kernel) { return launch_after(kernel, grid, kJoinThreads, 0, stream, p, states); };
   if (cache.head_dim == 128)
     return f16 ? join(decode_shared_join_kernel<true, 128>) : join(decode_shared_join_kernel<false, 128>);
   return f16 ? join(decode_shared_join_kernel<true, 64>) : join(decode_shared_join_kernel<false, 64>);

@@ -183,9 +183,11 @@ struct PrefixPlan {
 
 PrefixPlan prefix_plan(int H, const os_paged_cache& cache);
 
+struct PrefixLaunch;
+
 // Attention of every sequence's token over its group's prefix, ending in states (m, l, O).
 cudaError_t launch_attn_prefix(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H, const os_paged_cache& cache,
-                               const PrefixTables& tables, float scale, const PrefixPlan& plan, void* workspace,
+                               const PrefixLaunch& launch, float scale, const PrefixPlan& plan, void* workspace,
                                unsigned int* err, const AttnFault& fault, cudaStream_t stream);
 
 // log2(e) split into a float and the float nearest to the remainder, so that
