@@ -35,8 +35,10 @@ constexpr int kWholeKeys = 384;
 constexpr int kWholeKeysMany = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 // What an item costs beside its units of 64 keys, in units: its queries' way from memory
-// and the warps' merge. Without it, shares of many short items took twice as long as others.
-// RESULT
+// and the warps' merge. Without it, shares of many short items took twice as long as others:
+// 8-bit decode of 64 sequences of up to 8192 tokens 111.9 us with 0, 107.6 with 1, 106.6 with 2,
+// 107.0 with 4; 64 of up to 1000 behind a prefix 68.8, 61.9, 58.2 and (3) 58.1. (The 16-bit
+// decode keeps 0.)
 constexpr int kItemWeight = 2;
 // The reference maximum moves only when a score exceeds it by more than
 // 2^kSlack: any reference gives the same quotient O / l, and weights up to 2^8 are

@@ -22,11 +22,9 @@ constexpr int kTileWeight = 2;
 constexpr int kMinSteps = 3;
 constexpr int kLeastShareShift = 3;
 // The same for prefixes, whose states are joined in any case.
-#ifndef PREFIX_MIN
-#define PREFIX_MIN 1
-#define PREFIX_SHARE 2
-#endif
-constexpr int kPrefixMinSteps = PREFIX_MIN, kPrefixShareShift = PREFIX_SHARE;
+// (4 sequences behind 1000 tokens: 17.0 us with shares of 4 units and cuts after one step, 20.6 with the
+// values above; 64 behind 8192: 68.4 and 66.0.)
+constexpr int kPrefixMinSteps = 1, kPrefixShareShift = 2;
 constexpr int kKeysPerTile = 128;
 constexpr int kTileShift = 7;
 
