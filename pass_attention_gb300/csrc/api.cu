@@ -521,7 +521,7 @@ int64_t os_attention_decode_shared_workspace_bytes(int32_t H, const os_paged_cac
   if (!cache || !sized_cache(H, *cache) || groups <= 0 || groups > 65535 || prefix_max_pages <= 0 ||
       static_cast<int64_t>(prefix_max_pages) * cache->page_size > (int64_t(1) << 30))
     return 0;
-  return oss::decode_shared_workspace_bytes(H, *cache);
+  return oss::decode_shared_workspace_bytes(H, *cache, groups, prefix_max_pages);
 }
 
 os_status os_attention_decode_shared(const void* q, int64_t ld_q_batch, int64_t ld_q_head, int32_t H,
@@ -544,7 +544,7 @@ os_status os_attention_decode_shared(const void* q, int64_t ld_q_batch, int64_t 
     return OS_ERR_MISALIGNED;
   if (H > 65535 || groups > 65535 || static_cast<int64_t>(prefix_max_pages) * cache->page_size > (int64_t(1) << 30))
     return OS_ERR_UNSUPPORTED;
-  const int64_t need = oss::decode_shared_workspace_bytes(H, *cache);
+  const int64_t need = oss::decode_shared_workspace_bytes(H, *cache, groups, prefix_max_pages);
   if (need < 0) return OS_ERR_CUDA;
   if (workspace_bytes < need) return OS_ERR_INVALID_ARGUMENT;
   unsigned int* err = error_word();

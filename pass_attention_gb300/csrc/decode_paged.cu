@@ -64,8 +64,8 @@ struct Shape {
   static constexpr int kSmemBytes = kRingBytes + kMergeBytes<D>;
 };
 
-// NT: blocks of 8 query heads.
-template <bool kF16, int D, int NT>
+// NT: blocks of 8 query heads. kPairs: see seq_count.
+template <bool kF16, int D, int NT, bool kPairs>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(const DecodeParams p) {
   using S = Shape<D>;
   constexpr int kChunks = D / 8;              // 16-byte chunks of a row
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane & 3, row8 = lane >> 2;
 
-  Walk<kTileKeys> w;
+  Walk<kTileKeys, kPairs> w;
   ShareCut share;
   const bool has_share = find_share(p, &w, &share);
   if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -92,16 +92,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   const int copy_row = lane / kChunks, copy_chunk = lane % kChunks;
 
   // ---- the loads' cursor: the tile to be loaded next, and its page
-  Walk<kTileKeys> lw = w;
+  Walk<kTileKeys, kPairs> lw = w;
   int lt = lw.s.r0 * p.unit_tiles + warp;
   bool more = true;
   int page = 0;
+  const int32_t* row = seq_table<kPairs>(p, lw.s.b);
   auto settle = [&]() {  // move to the next tile that exists, fetch its page number
     while (lt >= lw.tile_end(p)) {
       if (!(more = lw.next(p))) return;
       lt = lw.s.r0 * p.unit_tiles + warp;
+      row = seq_table<kPairs>(p, lw.s.b);
     }
-    page = p.c.table[static_cast<int64_t>(lw.s.b) * p.c.ld_table + ((lt * kTileKeys) >> p.c.page_shift)];
+    page = row[(lt * kTileKeys) >> p.c.page_shift];
   };
   uint32_t bad = 0;  // stages whose tile has a page outside the pool
   auto load = [&](int stage) {
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
     for (int nt = 0; nt < NT; ++nt) {
       const bool live = nt * 8 + row8 < heads;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          p.q + s.b * p.ld_q_batch + static_cast<int64_t>(live ? head0 + nt * 8 + row8 : 0) * p.ld_q_head);
+          p.q + (kPairs ? s.b >> 1 : s.b) * p.ld_q_batch + static_cast<int64_t>(live ? head0 + nt * 8 + row8 : 0) * p.ld_q_head);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         qf[nt][kk][0] = live ? src[8 * kk + quad] : 0u;
@@ -470,13 +472,13 @@ cudaError_t launch_finish(const DecodeParams& p, int shares, float* weights, int
                       static_cast<int>(adds), static_cast<int>(chunks), weights, ld_w_batch, ld_w_head);
 }
 
-template <bool kF16, int D, int NT>
+template <bool kF16, int D, int NT, bool kPairs = false>
 cudaError_t launch_shape(const DecodeParams& p, int shares, cudaStream_t stream) {
   constexpr int smem = Shape<D>::kSmemBytes;
   static std::atomic<bool> smem_set[kMaxDevices];
-  const cudaError_t e = raise_smem(decode_paged_kernel<kF16, D, NT>, smem, smem_set);
+  const cudaError_t e = raise_smem(decode_paged_kernel<kF16, D, NT, kPairs>, smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_after(decode_paged_kernel<kF16, D, NT>, dim3(shares), kThreads, smem, stream, p);
+  return launch_after(decode_paged_kernel<kF16, D, NT, kPairs>, dim3(shares), kThreads, smem, stream, p);
 }
 
 template <bool kF16, int D>
@@ -563,7 +565,15 @@ DecodeParams decode_params(const Plan& pl, const PagedCache& c, const uint16_t* 
   return p;
 }
 
-cudaError_t launch_states(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream) {
+cudaError_t launch_states(const DecodeParams& p, bool f16, int D, int shares, bool pairs, cudaStream_t stream) {
+  if (pairs) {
+    if (p.block_heads == 8) {
+      if (D == 128) return f16 ? launch_shape<true, 128, 1, true>(p, shares, stream) : launch_shape<false, 128, 1, true>(p, shares, stream);
+      return f16 ? launch_shape<true, 64, 1, true>(p, shares, stream) : launch_shape<false, 64, 1, true>(p, shares, stream);
+    }
+    if (D == 128) return f16 ? launch_shape<true, 128, 2, true>(p, shares, stream) : launch_shape<false, 128, 2, true>(p, shares, stream);
+    return f16 ? launch_shape<true, 64, 2, true>(p, shares, stream) : launch_shape<false, 64, 2, true>(p, shares, stream);
+  }
   return launch_decode(p, f16, D, shares, nullptr, 0, 0, stream);
 }
 

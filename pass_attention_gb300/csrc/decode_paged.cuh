@@ -121,6 +121,37 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // maximum shows) adds NaN instead of nothing.
 __device__ __forceinline__ float reference(float m) { return m == neg_inf() ? 0.f : m; }
 
+// The sequences that a launch walks. With kPairs there are two for each of the batch: 2 b is the
+// prefix of b's group, 2 b + 1 its own tokens.
+template <bool kPairs>
+__device__ __forceinline__ int seq_count(const DecodeParams& p) {
+  return kPairs ? 2 * p.c.batch : p.c.batch;
+}
+
+template <bool kPairs>
+__device__ __forceinline__ int seq_len(const DecodeParams& p, int v) {
+  if constexpr (kPairs) {
+    const PrefixTables& t = p.prefix.tables;
+    if ((v & 1) == 0) {
+      const int g = prefix_group(t, v >> 1);
+      return g < 0 ? 0 : paged_length(t.len[g], t.max_pages, p.c.page_shift);
+    }
+    v >>= 1;
+  }
+  return paged_length(p.c.kv_len[v], p.c.max_pages, p.c.page_shift);
+}
+
+// The sequence's row of its page table (of a sequence with tokens).
+template <bool kPairs>
+__device__ __forceinline__ const int32_t* seq_table(const DecodeParams& p, int v) {
+  if constexpr (kPairs) {
+    const PrefixTables& t = p.prefix.tables;
+    if ((v & 1) == 0) return t.table + max(prefix_group(t, v >> 1), 0) * t.ld_table;
+    v >>= 1;
+  }
+  return p.c.table + v * p.c.ld_table;
+}
+
 // Units [r0, r1) of an item: sequence b, key head and head block j.
 struct Segment {
   int b, j, len, units, r0, r1;
@@ -130,7 +161,7 @@ struct Segment {
 // item_weight + units places of the row, and unit k of an item that begins at place `at`
 // lies at at + item_weight + k.
 // kKeys: keys of a tile.
-template <int kKeys>
+template <int kKeys, bool kPairs = false>
 struct Walk {
   Segment s;
   int64_t at, end;  // where the segment's item and the share's end lie
@@ -155,7 +186,7 @@ struct Walk {
     if (++s.j == p.c.heads * p.head_blocks) {
       s.j = 0;
       ++s.b;
-      s.len = paged_length(p.c.kv_len[s.b], p.c.max_pages, p.c.page_shift);
+      s.len = seq_len<kPairs>(p, s.b);
       s.units = units_of(p, s.len);
     }
     return clip(p, 0);
@@ -169,22 +200,27 @@ struct Walk {
 // This CTA's share, from the lengths: every thread sums a run of sequences, a
 // block scan places the runs, and the thread whose run holds the first unit
 // finds the sequence in it. False when the CTA has no share.
-template <int kKeys>
-__device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys>* w, ShareCut* share) {
-  using Walk = decode::Walk<kKeys>;
+template <int kKeys, bool kPairs>
+__device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys, kPairs>* w, ShareCut* share) {
+  using Walk = decode::Walk<kKeys, kPairs>;
   __shared__ int64_t warp_sum[kWarps];
   __shared__ Walk found;
   __shared__ bool some;  // a share may lie within an item's weight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (p.c.batch + kThreads - 1) / kThreads;
-  const int b0 = min(p.c.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.c.batch, b0 + per);
+  const int count = seq_count<kPairs>(p), per = (count + kThreads - 1) / kThreads;
+  const int b0 = min(count, static_cast<int>(threadIdx.x) * per), b1 = min(count, b0 + per);
   int64_t mine = 0, own = 0;
   PackedSeq group = packed_seq(RowRange{0, 0, false}, RowRange{0, 0, false}, 0);
-  const bool split = p.behind_prefix && p.prefix.bytes_cost > 0 && p.prefix.tables.groups <= kWarpGroups;  // SMs are left to the prefixes
+  const bool split = !kPairs && p.behind_prefix && p.prefix.bytes_cost > 0 && p.prefix.tables.groups <= kWarpGroups;  // SMs are left to the prefixes
   if (split && threadIdx.x < p.prefix.tables.groups)
     group = prefix_seq(p.prefix.tables, threadIdx.x, p.prefix.batch, p.prefix.page_shift, p.prefix.pos_shift);
+  if constexpr (kPairs) {
+    const PrefixTables& t = p.prefix.tables;
+    for (int g = threadIdx.x; t.cu && blockIdx.x == 0 && g < t.groups; g += kThreads)
+      if (row_range(t.cu[g], t.cu[g + 1], p.c.batch).clamped) report_error(p.err, kKernelPaged | (kSiteBadOffsets << 8));
+  }
   for (int b = b0; b < b1; ++b) {
-    const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
+    const int len = seq_len<kPairs>(p, b);
     mine += Walk::units_of(p, len) + p.item_weight;
     own += own_units(len);
   }
@@ -229,7 +265,7 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys>* w
   if (first >= before * per_seq && first < (before + mine) * per_seq) {
     int64_t at = before * per_seq;
     for (int b = b0; b < b1; ++b) {
-      const int len = paged_length(p.c.kv_len[b], p.c.max_pages, p.c.page_shift);
+      const int len = seq_len<kPairs>(p, b);
       const int units = Walk::units_of(p, len), places = units + p.item_weight;
       if (first < at + static_cast<int64_t>(places) * per_seq) {
         Walk f;
@@ -318,8 +354,8 @@ __device__ __forceinline__ void merge_warps(const DecodeParams& p, const Segment
 // The part of an item that begins in this CTA's share: 2 blockIdx.x + 1, of others 2
 // blockIdx.x. Where the item begins and is cut, thread 0 leaves its number of
 // parts behind, for the join.
-template <int kKeys>
-__device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk<kKeys>& w, const ShareCut& share, bool whole) {
+template <int kKeys, bool kPairs>
+__device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk<kKeys, kPairs>& w, const ShareCut& share, bool whole) {
   const Segment& s = w.s;
   const int slot = 2 * blockIdx.x + (s.r0 == 0 ? 1 : 0);
   if (s.r0 == 0 && threadIdx.x == 0) {
@@ -362,7 +398,8 @@ DecodeParams decode_params(const Plan& pl, const PagedCache& c, const uint16_t* 
                            int H, float scale, uint16_t* o, float* lse, void* workspace, unsigned int* err);
 
 // The first kernel alone, ending in states (p.state_o) and the parts of cut items.
-cudaError_t launch_states(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream);
+// (pairs: over prefixes and own tokens, two sequences for each.)
+cudaError_t launch_states(const DecodeParams& p, bool f16, int D, int shares, bool pairs, cudaStream_t stream);
 
 // The second kernel of a launch that cuts items: their join.
 cudaError_t launch_join(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream);

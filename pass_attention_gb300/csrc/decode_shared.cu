@@ -52,7 +52,8 @@ struct PrefixStates {
 
 // A warp takes every eighth part of the four rows, first the prefix's, then those of the
 // own tokens. Thread: row lane % 4, the vectors of 4 dims lane / 4, lane / 4 + 8, ...
-template <bool kF16, int D>
+// kPairs: the prefix's parts and states are those of sequence 2 b of the decode's kernel.
+template <bool kF16, int D, bool kPairs>
 __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const DecodeParams p, const PrefixStates x) {
   constexpr int kVecs = D / 32;
   __shared__ float2 sml[kJoinWarps][kJoinRows];
@@ -66,19 +67,30 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
   const int g = h / p.group, in_group = h - g * p.group, hb = in_group / p.block_heads;
   const int in_block = in_group - hb * p.block_heads;
   wait_for_previous_kernel();
-  int2 own = p.item_meta[(static_cast<int64_t>(b) * p.c.heads + g) * p.head_blocks + hb];
-  const int4 w = x.where[static_cast<int64_t>(b) * x.packs + (h >> x.head_shift)];
+  const int per_seq = p.c.heads * p.head_blocks, item = g * p.head_blocks + hb;
+  int2 own, pre = make_int2(0, 0);  // kPairs: {first share, parts} of the prefix
+  int4 w = make_int4(0, 0, 0, 0);
   int parts = 0;  // of the prefix
-  const bool cut = w.y != 0;
-  const int tile_row = (w.z + (h & ((1 << x.head_shift) - 1))) & 127;
-  if (own.y > 0) {
-    parts = cut ? w.y : 1;
-    // (a launch that gave up on a wait has not written this)
-    if (cut && (parts < 0 || w.x < 0 || w.w < 1 || w.w > x.shares || w.x + (parts - 1) * static_cast<int64_t>(w.w) >= x.shares))
-      parts = 0;
+  int64_t pre_row = row, own_row = row;
+  if constexpr (kPairs) {
+    pre = p.item_meta[static_cast<int64_t>(2 * b) * per_seq + item];
+    own = p.item_meta[static_cast<int64_t>(2 * b + 1) * per_seq + item];
+    parts = pre.y;
+    pre_row = static_cast<int64_t>(2 * b) * p.H + h;
+    own_row = pre_row + p.H;
   } else {
-    own.y = -own.y;  // no group names the sequence
+    own = p.item_meta[static_cast<int64_t>(b) * per_seq + item];
+    w = x.where[static_cast<int64_t>(b) * x.packs + (h >> x.head_shift)];
+    if (own.y > 0) {
+      parts = w.y != 0 ? w.y : 1;
+      // (a launch that gave up on a wait has not written this)
+      if (w.y != 0 && (parts < 0 || w.x < 0 || w.w < 1 || w.w > x.shares || w.x + (parts - 1) * static_cast<int64_t>(w.w) >= x.shares))
+        parts = 0;
+    } else {
+      own.y = -own.y;  // no group names the sequence
+    }
   }
+  const int tile_row = (w.z + (h & ((1 << x.head_shift) - 1))) & 127;
   const int all = live ? parts + own.y : 0;
 
   float M = neg_inf(), L = 0.f;
@@ -90,8 +102,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
     float2 ml;
     const float4* src;
     int step = 8;  // vectors from one of this thread's to the next
-    if (i < parts) {
-      if (!cut) {
+    if (!kPairs && i < parts) {
+      if (w.y == 0) {
         ml = x.state_ml[row];
         src = x.state_o + row * (D / 4) + v0;
       } else {
@@ -100,13 +112,18 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
         src = x.part_o + (slot * (D / 4) + v0) * 128 + tile_row;
         step = 8 * 128;
       }
-    } else if (own.y == 1) {
-      ml = p.state_ml[row];
-      src = reinterpret_cast<const float4*>(p.state_o) + row * (D / 4) + v0;
     } else {
-      const int64_t at = part_slot(own.x, i - parts) * p.block_heads + in_block;
-      ml = p.part_ml[at];
-      src = reinterpret_cast<const float4*>(p.part_o) + at * (D / 4) + v0;
+      const bool first = i < parts;  // kPairs
+      const int2 it = first ? pre : own;
+      const int64_t of = first ? pre_row : own_row;
+      if (it.y == 1) {
+        ml = p.state_ml[of];
+        src = reinterpret_cast<const float4*>(p.state_o) + of * (D / 4) + v0;
+      } else {
+        const int64_t at = part_slot(it.x, first ? i : i - parts) * p.block_heads + in_block;
+        ml = p.part_ml[at];
+        src = reinterpret_cast<const float4*>(p.part_o) + at * (D / 4) + v0;
+      }
     }
     float4 v[kVecs];
 #pragma unroll
@@ -156,30 +173,59 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Layout of the workspace: the prefixes' part, the decode's, and its states.
+// Prefixes that cost little to read again are read by every sequence: the paged decode's
+// kernel, over two sequences for each of the batch, and the join, two launches for three. The
+// rule goes by the bytes that are read again if every prefix fills its row of the table.
+// 4 sequences, 32 heads over 8, behind 1000 tokens (12 MB): RESULT
+constexpr int64_t kReadAgain = int64_t(40) << 20;
+constexpr int kPairGroups = 64;  // (every sequence looks its group up)
+
+bool in_pairs(const os_paged_cache& c, int groups, int prefix_max_pages) {
+  const int64_t again = c.batch > groups ? c.batch - groups : 0;
+  return groups <= kPairGroups &&
+         again * prefix_max_pages * c.page_size <= kReadAgain / (4 * static_cast<int64_t>(c.heads) * c.head_dim);
+}
+
+// Layout of the workspace: the prefixes' part (not in pairs), the decode's, and its states.
 struct SharedPlan {
+  bool pairs;
   PrefixPlan prefix;
   Plan own;
   int64_t own_at, item_meta, state_o, state_ml, bytes;
 };
 
-bool make_shared_plan(int H, const os_paged_cache& c, SharedPlan* out) {
-  if (!make_plan(H, c, kCtasPerSm, kTileKeys, kItemWeight, false, &out->own)) return false;
+bool make_shared_plan(int H, const os_paged_cache& c, int groups, int prefix_max_pages, SharedPlan* out) {
+  out->pairs = in_pairs(c, groups, prefix_max_pages);
+  os_paged_cache walked = c;  // the sequences of the decode's kernel
+  if (out->pairs) {
+    walked.batch = 2 * c.batch;
+    if (prefix_max_pages > c.max_pages) walked.max_pages = prefix_max_pages;
+  }
+  if (!make_plan(H, walked, kCtasPerSm, kTileKeys, kItemWeight, false, &out->own)) return false;
   out->prefix = prefix_plan(H, c);
-  const int64_t rows = static_cast<int64_t>(c.batch) * H;
-  out->own_at = out->prefix.bytes;
+  const int64_t rows = static_cast<int64_t>(walked.batch) * H;
+  out->own_at = out->pairs ? 0 : out->prefix.bytes;
   out->item_meta = out->own_at + out->own.bytes;
-  out->state_o = out->item_meta + round256(static_cast<int64_t>(c.batch) * c.heads * out->own.head_blocks * 8);
+  out->state_o = out->item_meta + round256(static_cast<int64_t>(walked.batch) * c.heads * out->own.head_blocks * 8);
   out->state_ml = out->state_o + round256(rows * c.head_dim * 4);
   out->bytes = out->state_ml + round256(rows * 8);
   return true;
 }
 
+template <bool kPairs>
+cudaError_t launch_join(const DecodeParams& p, const PrefixStates& x, bool f16, int D, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.c.batch) * p.H;
+  const dim3 grid(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
+  const auto join = [&](auto* kernel) { return launch_after(kernel, grid, kJoinThreads, 0, stream, p, x); };
+  if (D == 128) return f16 ? join(decode_shared_join_kernel<true, 128, kPairs>) : join(decode_shared_join_kernel<false, 128, kPairs>);
+  return f16 ? join(decode_shared_join_kernel<true, 64, kPairs>) : join(decode_shared_join_kernel<false, 64, kPairs>);
+}
+
 }  // namespace
 
-int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache) {
+int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache, int groups, int prefix_max_pages) {
   SharedPlan pl;
-  return make_shared_plan(H, cache, &pl) ? pl.bytes : -1;
+  return make_shared_plan(H, cache, groups, prefix_max_pages, &pl) ? pl.bytes : -1;
 }
 
 cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
@@ -187,35 +233,33 @@ cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t 
                                  float* lse, void* workspace, unsigned int* err, const AttnFault& fault,
                                  cudaStream_t stream) {
   SharedPlan pl;
-  if (!make_shared_plan(H, cache, &pl)) return cudaErrorInvalidDevice;
+  if (!make_shared_plan(H, cache, prefix.groups, prefix.max_pages, &pl)) return cudaErrorInvalidDevice;
   char* ws = static_cast<char*>(workspace);
+  const bool f16 = cache.dtype == OS_DTYPE_F16;
+  const int D = cache.head_dim;
   const PagedCache c = paged_cache(cache);
   const PrefixLaunch x{prefix, cache.batch, c.page_shift, 7 - pl.prefix.head_shift, pl.prefix.packs, device_sms(),
-                       cache.heads * pl.own.head_blocks,
-                       cache.head_dim == 128 ? kStepCost : kStepCost64,
-                       pl.own.block_heads > 8 ? kWideUnitCost : cache.head_dim == 128 ? kUnitCost : kUnitCost64,
-                       pl.own.whole ? 0 : kUnitBytesCost * cache.head_dim / 128};
-  cudaError_t e = launch_attn_prefix(q, ld_q_batch, ld_q_head, H, cache, x, scale, pl.prefix, ws, err, fault, stream);
-  if (e != cudaSuccess) return e;
-  const bool f16 = cache.dtype == OS_DTYPE_F16;
+                       cache.heads * pl.own.head_blocks, D == 128 ? kStepCost : kStepCost64,
+                       pl.own.block_heads > 8 ? kWideUnitCost : D == 128 ? kUnitCost : kUnitCost64,
+                       pl.own.whole ? 0 : kUnitBytesCost * D / 128};
+  cudaError_t e;
+  if (!pl.pairs && (e = launch_attn_prefix(q, ld_q_batch, ld_q_head, H, cache, x, scale, pl.prefix, ws, err, fault, stream)) != cudaSuccess)
+    return e;
   DecodeParams p = decode_params(pl.own, c, q, ld_q_batch, ld_q_head, H, scale, o, lse, ws + pl.own_at, err);
   p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
   p.state_o = reinterpret_cast<float*>(ws + pl.state_o);
   p.state_ml = reinterpret_cast<float2*>(ws + pl.state_ml);
-  p.behind_prefix = 1;
+  p.behind_prefix = pl.pairs ? 0 : 1;
   p.prefix = x;
-  if ((e = launch_states(p, f16, cache.head_dim, pl.own.shares, stream)) != cudaSuccess) return e;
+  if ((e = launch_states(p, f16, D, pl.own.shares, pl.pairs, stream)) != cudaSuccess) return e;
+  if (pl.pairs) return launch_join<true>(p, PrefixStates{}, f16, D, stream);
   const PrefixStates states{reinterpret_cast<const int4*>(ws + pl.prefix.where),
-                       reinterpret_cast<const float4*>(ws + pl.prefix.part_o),
-                       reinterpret_cast<const float2*>(ws + pl.prefix.part_ml),
-                       reinterpret_cast<const float4*>(ws + pl.prefix.state_o),
-                       reinterpret_cast<const float2*>(ws + pl.prefix.state_ml),
-                       pl.prefix.shares, pl.prefix.packs, pl.prefix.head_shift};
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(cache.batch) * H + kJoinRows - 1) / kJoinRows));
-  const auto join = [&](auto* kernel) { return launch_after(kernel, grid, kJoinThreads, 0, stream, p, states); };
-  if (cache.head_dim == 128)
-    return f16 ? join(decode_shared_join_kernel<true, 128>) : join(decode_shared_join_kernel<false, 128>);
-  return f16 ? join(decode_shared_join_kernel<true, 64>) : join(decode_shared_join_kernel<false, 64>);
+                            reinterpret_cast<const float4*>(ws + pl.prefix.part_o),
+                            reinterpret_cast<const float2*>(ws + pl.prefix.part_ml),
+                            reinterpret_cast<const float4*>(ws + pl.prefix.state_o),
+                            reinterpret_cast<const float2*>(ws + pl.prefix.state_ml),
+                            pl.prefix.shares, pl.prefix.packs, pl.prefix.head_shift};
+  return launch_join<false>(p, states, f16, D, stream);
 }
 
 }  // namespace oss

@@ -145,7 +145,7 @@ cudaError_t launch_decode_paged_fp8(const uint16_t* q, int64_t ld_q_batch, int64
 
 // Workspace of the decode behind shared prefixes on the current device (-1: it could not be
 // queried).
-int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache);
+int64_t decode_shared_workspace_bytes(int H, const os_paged_cache& cache, int groups, int prefix_max_pages);
 
 cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head, int H,
                                  const os_paged_cache& cache, const PrefixTables& prefix, float scale, uint16_t* o,

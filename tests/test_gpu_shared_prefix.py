@@ -19,6 +19,21 @@ def ints(values):
     return torch.tensor(values, dtype=torch.int32, device="cuda")
 
 
+# Prefixes that cost little to read again are read by every sequence, by what the table has
+# room for: every test runs over tables of the prefixes' own width, and over wide ones, which send
+# the prefixes to the tensor cores.
+WIDE = False
+READ_AGAIN = 40 << 20
+
+
+@pytest.fixture(params=[False, True], ids=["narrow", "wide"], autouse=True)
+def wide(request):
+    global WIDE
+    WIDE = request.param
+    yield
+    WIDE = False
+
+
 class Case:
     """Pools whose pages are in random order, with NaN in every slot that no token has, and -1 behind
     each sequence's and prefix's last page."""
@@ -42,6 +57,9 @@ class Case:
         else:
             self.kp, self.vp = r(pages, hkv, page, d), r(pages, hkv, page, d)
         order = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+        again = (batch - len(sizes)) * hkv * page * 4 * d  # bytes of a page, for each sequence that reads it again
+        if WIDE and prefix_columns is None and again > 0:
+            prefix_columns = max(READ_AGAIN // again + 1, max(need0))
         at = 0
         free = torch.ones((pages, page), dtype=torch.bool, device="cuda")
         tables = []
@@ -201,6 +219,7 @@ def test_bad_pages_are_left_out(page):
         assert oss.check_device_error() == 0
         c.prefix_table, c.prefixes = torch.cat([full[:, :1], full[:, 2:]], 1), [2 * page]
         c.check(o, lse)
+        c.prefix_table = full
         c.prefixes = [prefix]
     c.prefix_table = torch.full_like(full, -5)
     o, lse = c.run()
@@ -211,10 +230,14 @@ def test_bad_pages_are_left_out(page):
 
 
 def test_lengths_outside_the_tables_are_clamped():
-    c = Case([2, 2], [64, 40], [32, 30, 0, 5], 4, 1, seed=9)
+    c = Case([2, 2], [64, 40], [32, 30, 0, 5], 4, 1, seed=9, prefix_columns=4)
     c.prefix_len, c.kv_len = ints([65, -3]), ints([33, 30, -1, 5])
     c.prefixes = [64, 0]
     c.go()
+    # 12 sequences over a table of 1024 tokens, on the tensor cores
+    c = Case([12], [1024], [32] + [7] * 11, 16, 8, seed=9, prefix_columns=64)
+    c.prefix_len, c.kv_len = ints([2 ** 31 - 1]), ints([33] + [7] * 11)
+    c.go(rows=[0, 11])
 
 
 @pytest.mark.parametrize("cu", [[0, 3, 2], [0, 2, 9], [-1, 2, 4]])
@@ -231,7 +254,7 @@ def test_as_the_paged_decode_over_the_same_tokens():
     # a prefix of whole pages: the same tokens by one table for each sequence
     c = Case([6], [640], [0, 1, 33, 100, 64, 7], 8, 2, page=32, seed=11)
     o, lse = c.run()
-    table = torch.cat([c.prefix_table.expand(6, -1), c.table], 1).contiguous()
+    table = torch.cat([c.prefix_table[:, :20].expand(6, -1), c.table], 1).contiguous()
     ro, rl = oss.attention_decode_paged(c.q, c.kp, c.vp, table, c.kv_len + 640)
     u = torch.finfo(c.q.dtype).eps / 2
     # both round o once and the weights once: 2 (u |o| + u sum p |v|), |v| <= 6
@@ -302,10 +325,11 @@ def test_a_prompt_then_steps_of_its_samples():
     gen.manual_seed(33)
     hq, hkv, d, page, dtype, batch, prompt, steps = 8, 2, 128, 16, torch.bfloat16, 5, 173, 6
     r = lambda *s: torch.randn(s, generator=gen, device="cuda").to(dtype)  # noqa: E731
-    pages = 11 + batch
+    pages, room = 11 + batch, 400 if WIDE else 11  # (11: 4 sequences read it again, 1.4 MB; 400: 52 MB)
     kp, vp = (torch.full((pages, hkv, page, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
     order = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
-    prefix_table, table = order[None, :11].contiguous(), order[11:, None].contiguous()
+    prefix_table, table = torch.full((1, room), -1, dtype=torch.int32, device="cuda"), order[11:, None].contiguous()
+    prefix_table[0, :11] = order[:11]
     prefix_len, cu = ints([prompt]), ints([0, prompt])
     q, k, v = r(prompt, hq, d), r(prompt, hkv, d), r(prompt, hkv, d)
     oss.attention_fwd_packed(q, k, v, cu)
@@ -371,3 +395,40 @@ def test_two_graphs_with_other_lengths_side_by_side():
         for c, out in zip(cases, outs):
             c.check(*out)
     assert oss.check_device_error() == 0
+
+
+def test_a_wait_that_gives_up_is_reported(wide):
+    # a V tile that never arrives: the launch ends, and the next one works
+    c = Case([12], [1000], [20] * 12, 16, 8, seed=17, prefix_columns=64)
+    oss.debug_inject_fault(1, 0, 20_000_000)
+    c.run()
+    with pytest.raises(oss.OssError, match="OS_ERR_TIMEOUT"):
+        oss.check_device_error()
+    assert oss.check_device_error() == 0
+    c.go(rows=[0, 11])
+
+
+@pytest.mark.slow
+def test_offsets_beyond_32_bits():
+    # pools of more than 2^32 bytes and 2^31 elements each: the last pages are used
+    page, heads, d = 64, 8, 128
+    pages = (2 ** 31 + 2 ** 26) // (page * heads * d)
+    kp = torch.empty((pages, heads, page, d), dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    prefix_table = torch.full((1, 700 if WIDE else 3), -1, dtype=torch.int32, device="cuda")
+    prefix_table[0, :3] = ints([pages - 1, 0, pages - 2])
+    table = ints([[pages - 3], [pages - 4], [1]])
+    k, v = (torch.randn((150 + 3 * 20, heads, d), device="cuda").to(torch.bfloat16) for _ in range(2))
+    own = ints([20, 20, 20])
+    oss.kv_cache_append(k[:150], v[:150], kp, vp, prefix_table, ints([150]), ints([0, 150]))
+    oss.kv_cache_append(k[150:], v[150:], kp, vp, table, own, ints([0, 20, 40, 60]))
+    q = torch.randn((3, 16, d), device="cuda").to(torch.bfloat16)
+    o, lse = oss.attention_decode_shared(q, kp, vp, prefix_table, ints([150]), table, own)
+    assert oss.check_device_error() == 0
+
+    def rows(x):
+        def get(b, g):
+            return f64(torch.cat([x[:150, g], x[150 + 20 * b:170 + 20 * b, g]]))
+        get.heads = heads
+        return get
+    check_shared(o, lse, q, rows(k), rows(v), 1 / math.sqrt(d))
