@@ -678,9 +678,11 @@ OSS_API os_status os_kv_cache_evict(const os_paged_cache* cache, const float* we
  * prefix_len[g] tokens of the group's prefix and then the sequence's own
  * kv_len tokens, all of them in pages of the same pools:
  *     s_t = scale * q . k_t;  lse = ln sum_t exp(s_t);  o = sum_t exp(s_t - lse) v_t
- * The prefix is read once for the whole group, on the tensor cores, and not
- * once a sequence; the two parts' states (m, l, O) are joined in fp32 with the
- * merge identity, in a fixed order, so every run gives the same bits. A sequence
+ * A prefix is read once for 128 rows (queries of its group times query heads of a key
+ * head), on the tensor cores, and not once a sequence, unless reading it again costs
+ * little: up to 80 MB of it in all, by what prefix_table has room for, and up to
+ * 64 groups. The two parts' states (m, l, O) are joined in fp32 with the merge
+ * identity, in a fixed order, so every run gives the same bits. A sequence
  * that no group names has its own tokens only; one without any key gives o = 0,
  * lse = -inf. Rounding and NaN as in os_attention_decode_paged; k and v of a prefix
  * are finite.
@@ -803,7 +805,8 @@ OSS_API int64_t os_attention_decode_paged_fp8_workspace_bytes(int32_t H, const o
  * forward (see os_debug_inject_fault); 2 | (1 << 8) is a row softmax whose
  * wait for its row's bulk copies into shared memory gave up, 2 | (2 << 8) one
  * whose wait for the (max, sum) states of the other CTAs of its cluster gave
- * up; kernel 4 is os_attention_fwd_packed (sites as kernel 1). Kernel 3 is
+ * up; kernel 4 is os_attention_fwd_packed, or the prefixes' part of
+ * os_attention_decode_shared (sites as kernel 1). Kernel 3 is
  * not a wait: a call on a paged cache or on packed sequences met an index
  * outside them and left that row out (site 1: a page number; site 2: a position
  * without a page; site 3: sequence offsets that run backwards or past the
@@ -824,7 +827,9 @@ OSS_API os_status os_check_device_error(void* stream, int32_t* code);
  * the next call of the kind's entry point made by the calling host thread
  * (that call disarms it):
  *   kind 0: disarm.
- *   kind 1: (os_attention_fwd, its variants and os_attention_fwd_packed) the
+ *   kind 1: (os_attention_fwd, its variants, os_attention_fwd_packed, and
+ *           os_attention_decode_shared where it reads prefixes on the tensor
+ *           cores) the
  *           kernel's load warp skips the V tile of KV step `step` (counted
  *           in the order each CTA visits its KV tiles), so the thread that
  *           issues P V waits on a phase that never completes. After
@@ -834,8 +839,9 @@ OSS_API os_status os_check_device_error(void* stream, int32_t* code);
  *           the recorded error and stop too). os_check_device_error then
  *           returns OS_ERR_TIMEOUT with code & 0xFFFF = 1 | (3 << 8) (kernel
  *           1, wait site 3: V tile full); bits 16..31 hold the launch's tag.
- *           os_attention_fwd_packed reports 4 | (site << 8), the site of one
- *           of the waits that ran out, and no tag.
+ *           os_attention_fwd_packed and os_attention_decode_shared report
+ *           4 | (site << 8), the site of one of the waits that ran out, and no
+ *           tag.
  *           The CUDA context stays usable; the outputs of that call are
  *           undefined.
  *   kind 2: the next os_softmax_rows or os_softmax_rows_16bit call. If it

@@ -74,7 +74,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_paged_kernel(cons
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float merge_m[kWarps][8], merge_l[kWarps][8];
   let_next_kernel_start();
-  if (!p.behind_prefix) wait_for_previous_kernel();
+  if (p.behind_prefix)
+    begin_behind_waiting_kernel();
+  else
+    wait_for_previous_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane & 3, row8 = lane >> 2;
 

@@ -16,9 +16,10 @@
 // that came before the first has ended, and waits for the first at its own end.
 //
 // Measured, 32 heads over 8 of 128: 64 sequences of up to 1000 tokens behind 8192: 46 us (183 MB:
-// 27 us of HBM's time); of up to 2500 behind 65536: 110 us (566 MB: 85 us); 4 of up to 77
-// behind 1000: 15.6 us, of which the way to the first product is 5 and the join with its two
-// hand-overs 6. One table a sequence, every one with the prefix's pages, instead: RESULT
+// 27 us of HBM's time); of up to 2500 behind 65536: 110 us (566 MB: 85 us). With one table a
+// sequence, every one of them with the prefix's pages in front, the paged decode takes 193
+// and 1455 us. Of a launch, 5 us are the way to the first product, and 6 the join with its two
+// hand-overs.
 
 #include <cstdint>
 
@@ -176,8 +177,12 @@ int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 // Prefixes that cost little to read again are read by every sequence: the paged decode's
 // kernel, over two sequences for each of the batch, and the join, two launches for three. The
 // rule goes by the bytes that are read again if every prefix fills its row of the table.
-// 4 sequences, 32 heads over 8, behind 1000 tokens (12 MB): RESULT
-constexpr int64_t kReadAgain = int64_t(40) << 20;
+// From a graph, read again / on the tensor cores (sequences, heads, prefix): 4, 32 / 8, 1000 (12 MB):
+// 10.5 / 15.6 us; 16, 8 / 1, 4000 (31): 13.1 / 16.8; 4, 32 / 8, 4000 (49): 14.8 / 17.2; 16, 32 / 8, 1000
+// (61): 15.3 / 16.8; 37 in 5 groups, 16 / 2 of 64, 5001 (82): 19.9 / 16.6; 4, 32 / 8, 8000 (98): 20.9 / 20.8;
+// 32, 32 / 8, 1000 (127): 22.2 / 17.4. Launched one by one, 24 us of the host against 30:
+// on the GPU the two meet at 65 MB or so, with the host at twice that.
+constexpr int64_t kReadAgain = int64_t(80) << 20;
 constexpr int kPairGroups = 64;  // (every sequence looks its group up)
 
 bool in_pairs(const os_paged_cache& c, int groups, int prefix_max_pages) {

@@ -107,10 +107,11 @@ struct Piece {
   int head, part;
   __device__ __forceinline__ Piece(int64_t i, int heads) {
     const int groups = (heads + kHeads - 1) / kHeads;
-    part = static_cast<int>(i % kLanes);
-    const int64_t g = i / kLanes;
-    token = static_cast<int32_t>(g / groups);
-    head = static_cast<int>(g - static_cast<int64_t>(token) * groups) * kHeads;
+    part = static_cast<int>(threadIdx.x % kLanes);
+    const uint64_t g = static_cast<uint64_t>(i) / kLanes;
+    // (a 64-bit division is a hundred instructions)
+    token = static_cast<int32_t>(g >> 32 ? g / groups : static_cast<uint32_t>(g) / static_cast<uint32_t>(groups));
+    head = static_cast<int>(g - static_cast<uint64_t>(token) * groups) * kHeads;
   }
   __device__ __forceinline__ static int64_t count(int64_t tokens, int heads) {
     return tokens * ((heads + kHeads - 1) / kHeads) * kLanes;
@@ -219,9 +220,9 @@ kv_read_fp8_kernel(PagedCache c, Fp8Pools f, const int32_t* __restrict__ cu, int
 
 // Heads of a thread, and CTAs (at most 64 an SM, whose threads go on). With two heads a
 // thread looks its token's place up once for both and has two rows on their way: 37 k
-// tokens, 8 heads of 128, read in 38.0 us against 45.4 with one head (and 38.3 with four), written in 39.7
-// against 40.2 (four: 42.4, by their registers). With rows for less than the GPU's threads one head
-// a thread is as fast (64 rows of 8 heads: 3.2 us).
+// tokens, 8 heads of 128, read in 37.7 us against 40.6 with one head and 38.4 with four, written in
+// 39.4 against 43.0 and 41.8 (four take its registers). With rows for less than the GPU's
+// threads, one head a thread is as fast (64 rows of 8 heads: 3.3 us).
 constexpr int kManyHeads = 2;
 
 bool many_rows(int64_t rows, int lanes, int sms) { return rows * lanes > static_cast<int64_t>(sms) * 2048; }

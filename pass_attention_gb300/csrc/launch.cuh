@@ -3,7 +3,7 @@
 // ones run, and call wait_for_previous_kernel() before they touch anything that it
 // reads or writes. Every CTA calls it, also one that has nothing to do: a kernel
 // that ended without waiting would let the next one start before the one
-// before it has ended.
+// before it has ended. (begin_behind_waiting_kernel() is the exception.)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -13,6 +13,13 @@ namespace oss {
 // Returns when every kernel before this one on the stream has ended and its
 // writes are visible.
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// For a kernel that reads nothing of the one before it, where every CTA of that one calls
+// wait_for_previous_kernel() before let_next_kernel_start(): all that came earlier has
+// ended when this one starts. (The fence keeps what an SM's L1 holds of older launches out.) A
+// CTA of it still waits for the kernel before, at its end: the kernel behind this one
+// waits for this one only.
+__device__ __forceinline__ void begin_behind_waiting_kernel() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
 // The next kernel on the stream may be scheduled (it waits as above).
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

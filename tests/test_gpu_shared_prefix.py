@@ -23,7 +23,7 @@ def ints(values):
 # room for: every test runs over tables of the prefixes' own width, and over wide ones, which send
 # the prefixes to the tensor cores.
 WIDE = False
-READ_AGAIN = 40 << 20
+READ_AGAIN = 80 << 20
 
 
 @pytest.fixture(params=[False, True], ids=["narrow", "wide"], autouse=True)
@@ -135,11 +135,20 @@ def test_pages_and_layouts(page, layout):
     ([0, 4, 0, 3, 0], [50, 700, 0, 129, 9]),  # groups of none
     ([33, 1, 40, 2], [128, 1000, 17, 2000]),  # tiles that begin inside a group's rows of q
     ([2] * 60, [64 + 3 * i for i in range(60)]),
+    ([1] * 70, [5 * i for i in range(70)]),  # more groups than are looked up by every sequence
 ])
 def test_groups_of_sequences(sizes, prefixes):
     own = [(37 * i) % 90 for i in range(sum(sizes))]
     Case(sizes, prefixes, own, 4, 1, seed=len(sizes)).go()
     Case(sizes, prefixes, own, 6, 2, d=64, dtype="f16", seed=len(sizes)).go()
+
+
+@pytest.mark.parametrize("sizes,prefixes", [([20], [700]), ([17, 3], [300, 900]), ([9, 9], [129, 1])])
+def test_many_tiles_of_rows(sizes, prefixes):
+    # 128 heads of a key head fill a tile each: a tile or two for every sequence, more than eight a group
+    n = sum(sizes)
+    Case(sizes, prefixes, [(13 * i) % 40 for i in range(n)], 256, 1, d=64, seed=n).go(rows=[0, n // 2, n - 1])
+    Case(sizes, prefixes, [(13 * i) % 40 for i in range(n)], 128, 1, seed=n).go(rows=[0, n // 2, n - 1])
 
 
 def test_sequences_outside_every_group():
@@ -234,10 +243,10 @@ def test_lengths_outside_the_tables_are_clamped():
     c.prefix_len, c.kv_len = ints([65, -3]), ints([33, 30, -1, 5])
     c.prefixes = [64, 0]
     c.go()
-    # 12 sequences over a table of 1024 tokens, on the tensor cores
-    c = Case([12], [1024], [32] + [7] * 11, 16, 8, seed=9, prefix_columns=64)
-    c.prefix_len, c.kv_len = ints([2 ** 31 - 1]), ints([33] + [7] * 11)
-    c.go(rows=[0, 11])
+    # 24 sequences over a table of 1024 tokens, on the tensor cores
+    c = Case([24], [1024], [32] + [7] * 23, 16, 8, seed=9, prefix_columns=64)
+    c.prefix_len, c.kv_len = ints([2 ** 31 - 1]), ints([33] + [7] * 23)
+    c.go(rows=[0, 23])
 
 
 @pytest.mark.parametrize("cu", [[0, 3, 2], [0, 2, 9], [-1, 2, 4]])
@@ -325,7 +334,7 @@ def test_a_prompt_then_steps_of_its_samples():
     gen.manual_seed(33)
     hq, hkv, d, page, dtype, batch, prompt, steps = 8, 2, 128, 16, torch.bfloat16, 5, 173, 6
     r = lambda *s: torch.randn(s, generator=gen, device="cuda").to(dtype)  # noqa: E731
-    pages, room = 11 + batch, 400 if WIDE else 11  # (11: 4 sequences read it again, 1.4 MB; 400: 52 MB)
+    pages, room = 11 + batch, 1300 if WIDE else 11  # (11: 4 sequences read it again, 1.4 MB; 1300: 85 MB)
     kp, vp = (torch.full((pages, hkv, page, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
     order = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
     prefix_table, table = torch.full((1, room), -1, dtype=torch.int32, device="cuda"), order[11:, None].contiguous()
@@ -399,13 +408,13 @@ def test_two_graphs_with_other_lengths_side_by_side():
 
 def test_a_wait_that_gives_up_is_reported(wide):
     # a V tile that never arrives: the launch ends, and the next one works
-    c = Case([12], [1000], [20] * 12, 16, 8, seed=17, prefix_columns=64)
+    c = Case([24], [1000], [20] * 24, 16, 8, seed=17, prefix_columns=64)
     oss.debug_inject_fault(1, 0, 20_000_000)
     c.run()
     with pytest.raises(oss.OssError, match="OS_ERR_TIMEOUT"):
         oss.check_device_error()
     assert oss.check_device_error() == 0
-    c.go(rows=[0, 11])
+    c.go(rows=[0, 23])
 
 
 @pytest.mark.slow
@@ -415,7 +424,7 @@ def test_offsets_beyond_32_bits():
     pages = (2 ** 31 + 2 ** 26) // (page * heads * d)
     kp = torch.empty((pages, heads, page, d), dtype=torch.bfloat16, device="cuda")
     vp = torch.empty_like(kp)
-    prefix_table = torch.full((1, 700 if WIDE else 3), -1, dtype=torch.int32, device="cuda")
+    prefix_table = torch.full((1, 400 if WIDE else 3), -1, dtype=torch.int32, device="cuda")
     prefix_table[0, :3] = ints([pages - 1, 0, pages - 2])
     table = ints([[pages - 3], [pages - 4], [1]])
     k, v = (torch.randn((150 + 3 * 20, heads, d), device="cuda").to(torch.bfloat16) for _ in range(2))
