@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane & 3, row8 = lane >> 2;
 
-  Walk<S::kKeys> w;
+  Walk<S::kKeys, kWeighed> w;
   ShareCut share;
   const bool has_share = find_share(p, &w, &share);
   if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
 
   // ---- the loads' cursor: the tile to be loaded next and its page, and what of its
   // address the segment decides
-  Walk<S::kKeys> lw = w;
+  Walk<S::kKeys, kWeighed> lw = w;
   int lt, lt_end;
   bool more = true;
   int page[kSub];
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
         }
       }
       __syncthreads();
-      merge_warps<kF16, D>(p, s, whole, slot, head0, nt * 8, heads, merge, merge_m, merge_l);
+      merge_warps<kF16, D, kWeighed>(p, s, whole, slot, head0, nt * 8, heads, merge, merge_m, merge_l);
       __syncthreads();
     }
     go = w.next(p);

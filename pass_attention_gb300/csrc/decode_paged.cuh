@@ -34,7 +34,7 @@ constexpr int kCtasPerSm = 2;  // of the 16-bit decode
 constexpr int kWholeKeys = 384;
 constexpr int kWholeKeysMany = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
-// What an item costs beside its units of 64 keys, in units: its queries' way from memory
+// kMode other than kPlain: what an item costs beside its units, in units: its queries' way from memory
 // and the warps' merge. Without it, shares of many short items took twice as long as others:
 // 8-bit decode of 64 sequences of up to 8192 tokens 111.9 us with 0, 107.6 with 1, 106.6 with 2,
 // 107.0 with 4; 64 of up to 1000 behind a prefix 68.8, 61.9, 58.2 and (3) 58.1. (The 16-bit
@@ -61,12 +61,10 @@ struct DecodeParams {
   int4* meta;       // [N]: {sequence, key head and head block, parts, first slot}
   float* lse2;      // [batch][H], base 2: of items that were not cut (only with scores)
   int2* item_meta;  // [batch][heads * head_blocks]: {first share, parts}, or null
-  // of the decode behind shared prefixes: the kernel before this one writes nothing that this one
-  // reads, so it is waited for at the end, by the first CTA
-  int32_t behind_prefix;
+  // of the decode behind shared prefixes
   PrefixLaunch prefix;
-  float* state_o;   // [batch][H][D]: O of whole items instead of o, or null
-  float2* state_ml;  // [batch][H]: m, l
+  float* state_o;   // [sequences][H][D]: O of whole items (kPairs, kBehind)
+  float2* state_ml;  // [sequences][H]: m, l
   float* scores;    // [batch][heads * head_blocks][capacity][score_heads], or null
   int32_t score_heads;
   unsigned int* err;
@@ -121,16 +119,30 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // maximum shows) adds NaN instead of nothing.
 __device__ __forceinline__ float reference(float m) { return m == neg_inf() ? 0.f : m; }
 
-// The sequences that a launch walks. With kPairs there are two for each of the batch: 2 b is the
-// prefix of b's group, 2 b + 1 its own tokens.
-template <bool kPairs>
-__device__ __forceinline__ int seq_count(const DecodeParams& p) {
-  return kPairs ? 2 * p.c.batch : p.c.batch;
+// What a launch of the decode is.
+enum Mode {
+  kPlain,   // the 16-bit decode: items have no weight, and end in o and lse
+  kWeighed,  // the 8-bit decode: items have one
+  // of the decode behind shared prefixes, ending in states:
+  kPairs,   // two sequences for each of the batch: 2 b is the prefix of b's group, 2 b + 1 its own tokens
+  kBehind,  // the own tokens, beside or behind the prefixes' kernel
+};
+
+// What an item costs beside its units, in units.
+template <Mode kMode>
+__device__ __forceinline__ int item_weight(const DecodeParams& p) {
+  return kMode == kPlain ? 0 : p.item_weight;
 }
 
-template <bool kPairs>
+// The sequences that a launch walks.
+template <Mode kMode>
+__device__ __forceinline__ int seq_count(const DecodeParams& p) {
+  return kMode == kPairs ? 2 * p.c.batch : p.c.batch;
+}
+
+template <Mode kMode>
 __device__ __forceinline__ int seq_len(const DecodeParams& p, int v) {
-  if constexpr (kPairs) {
+  if constexpr (kMode == kPairs) {
     const PrefixTables& t = p.prefix.tables;
     if ((v & 1) == 0) {
       const int g = prefix_group(t, v >> 1);
@@ -142,9 +154,9 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int v) {
 }
 
 // The sequence's row of its page table (of a sequence with tokens).
-template <bool kPairs>
+template <Mode kMode>
 __device__ __forceinline__ const int32_t* seq_table(const DecodeParams& p, int v) {
-  if constexpr (kPairs) {
+  if constexpr (kMode == kPairs) {
     const PrefixTables& t = p.prefix.tables;
     if ((v & 1) == 0) return t.table + max(prefix_group(t, v >> 1), 0) * t.ld_table;
     v >>= 1;
@@ -161,7 +173,7 @@ struct Segment {
 // item_weight + units places of the row, and unit k of an item that begins at place `at`
 // lies at at + item_weight + k.
 // kKeys: keys of a tile.
-template <int kKeys, bool kPairs = false>
+template <int kKeys, Mode kMode>
 struct Walk {
   Segment s;
   int64_t at, end;  // where the segment's item and the share's end lie
@@ -174,19 +186,19 @@ struct Walk {
   }
   // The segment from unit r0 of the item at hand; false when the share ends before that.
   __device__ __forceinline__ bool clip(const DecodeParams& p, int64_t r0) {
-    const int64_t r1 = end - at - p.item_weight;
+    const int64_t r1 = end - at - item_weight<kMode>(p);
     s.r0 = static_cast<int>(r0);
     s.r1 = r1 < s.units ? static_cast<int>(r1 > 0 ? r1 : 0) : s.units;
     return s.r0 < s.r1;
   }
   // The next segment of the share; false when there is none.
   __device__ __forceinline__ bool next(const DecodeParams& p) {
-    at += s.units + p.item_weight;
-    if (at + p.item_weight >= end) return false;
+    at += s.units + item_weight<kMode>(p);
+    if (at + item_weight<kMode>(p) >= end) return false;
     if (++s.j == p.c.heads * p.head_blocks) {
       s.j = 0;
       ++s.b;
-      s.len = seq_len<kPairs>(p, s.b);
+      s.len = seq_len<kMode>(p, s.b);
       s.units = units_of(p, s.len);
     }
     return clip(p, 0);
@@ -200,28 +212,28 @@ struct Walk {
 // This CTA's share, from the lengths: every thread sums a run of sequences, a
 // block scan places the runs, and the thread whose run holds the first unit
 // finds the sequence in it. False when the CTA has no share.
-template <int kKeys, bool kPairs>
-__device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys, kPairs>* w, ShareCut* share) {
-  using Walk = decode::Walk<kKeys, kPairs>;
+template <int kKeys, Mode kMode>
+__device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys, kMode>* w, ShareCut* share) {
+  using Walk = decode::Walk<kKeys, kMode>;
   __shared__ int64_t warp_sum[kWarps];
   __shared__ Walk found;
   __shared__ bool some;  // a share may lie within an item's weight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int count = seq_count<kPairs>(p), per = (count + kThreads - 1) / kThreads;
+  const int count = seq_count<kMode>(p), per = (count + kThreads - 1) / kThreads;
   const int b0 = min(count, static_cast<int>(threadIdx.x) * per), b1 = min(count, b0 + per);
   int64_t mine = 0, own = 0;
   PackedSeq group = packed_seq(RowRange{0, 0, false}, RowRange{0, 0, false}, 0);
-  const bool split = !kPairs && p.behind_prefix && p.prefix.bytes_cost > 0 && p.prefix.tables.groups <= kWarpGroups;  // SMs are left to the prefixes
+  const bool split = kMode == kBehind && p.prefix.bytes_cost > 0 && p.prefix.tables.groups <= kWarpGroups;  // SMs are left to the prefixes
   if (split && threadIdx.x < p.prefix.tables.groups)
     group = prefix_seq(p.prefix.tables, threadIdx.x, p.prefix.batch, p.prefix.page_shift, p.prefix.pos_shift);
-  if constexpr (kPairs) {
+  if constexpr (kMode == kPairs) {
     const PrefixTables& t = p.prefix.tables;
     for (int g = threadIdx.x; t.cu && blockIdx.x == 0 && g < t.groups; g += kThreads)
       if (row_range(t.cu[g], t.cu[g + 1], p.c.batch).clamped) report_error(p.err, kKernelPaged | (kSiteBadOffsets << 8));
   }
   for (int b = b0; b < b1; ++b) {
-    const int len = seq_len<kPairs>(p, b);
-    mine += Walk::units_of(p, len) + p.item_weight;
+    const int len = seq_len<kMode>(p, b);
+    mine += Walk::units_of(p, len) + item_weight<kMode>(p);
     own += own_units(len);
   }
   int64_t upto = mine;
@@ -265,8 +277,8 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys, kP
   if (first >= before * per_seq && first < (before + mine) * per_seq) {
     int64_t at = before * per_seq;
     for (int b = b0; b < b1; ++b) {
-      const int len = seq_len<kPairs>(p, b);
-      const int units = Walk::units_of(p, len), places = units + p.item_weight;
+      const int len = seq_len<kMode>(p, b);
+      const int units = Walk::units_of(p, len), places = units + item_weight<kMode>(p);
       if (first < at + static_cast<int64_t>(places) * per_seq) {
         Walk f;
         f.s.b = b;
@@ -275,7 +287,7 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys, kP
         f.s.units = units;
         f.at = at + static_cast<int64_t>(f.s.j) * places;
         f.end = last;
-        const int64_t into = first - f.at - p.item_weight;
+        const int64_t into = first - f.at - item_weight<kMode>(p);
         some = f.clip(p, into > 0 ? into : 0) || f.next(p);
         found = f;
         break;
@@ -297,8 +309,8 @@ constexpr int kMergeBytes = kWarps * 8 * kMergeLd<D> * 4;
 
 // The four warps' states of 8 query heads, from head0 on (`heads` of them are live), as they
 // lie in `merge` [warp][8][kMergeLd], m and l: the answer of an item that one CTA has
-// seen whole, else its part in `slot` (or, with p.state_o, a whole item's state).
-template <bool kF16, int D>
+// seen whole (kPairs, kBehind: its state), else its part in `slot`.
+template <bool kF16, int D, Mode kMode>
 __device__ __forceinline__ void merge_warps(const DecodeParams& p, const Segment& s, bool whole, int slot, int head0,
                                             int in_block, int heads, const float* merge, const float (*merge_m)[8],
                                             const float (*merge_l)[8]) {
@@ -326,7 +338,8 @@ __device__ __forceinline__ void merge_warps(const DecodeParams& p, const Segment
     }
   }
   const int64_t row = static_cast<int64_t>(s.b) * p.H + head0 + in_block + hh;
-  if (whole && !p.state_o) {
+  constexpr bool kStates = kMode == kPairs || kMode == kBehind;
+  if (whole && !kStates) {
     const float inv = L != 0.f ? 1.f / L : 0.f;
     uint32_t out[kDims / 2];
 #pragma unroll
@@ -354,19 +367,19 @@ __device__ __forceinline__ void merge_warps(const DecodeParams& p, const Segment
 // The part of an item that begins in this CTA's share: 2 blockIdx.x + 1, of others 2
 // blockIdx.x. Where the item begins and is cut, thread 0 leaves its number of
 // parts behind, for the join.
-template <int kKeys, bool kPairs>
-__device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk<kKeys, kPairs>& w, const ShareCut& share, bool whole) {
+template <int kKeys, Mode kMode>
+__device__ __forceinline__ int open_segment(const DecodeParams& p, const Walk<kKeys, kMode>& w, const ShareCut& share, bool whole) {
   const Segment& s = w.s;
   const int slot = 2 * blockIdx.x + (s.r0 == 0 ? 1 : 0);
   if (s.r0 == 0 && threadIdx.x == 0) {
     int parts = 1;
     if (!whole) {
       // the item's last unit lies in the last of its shares
-      parts = static_cast<int>(last_boundary(share, w.at + p.item_weight + s.units - 1) - blockIdx.x) + 1;
+      parts = static_cast<int>(last_boundary(share, w.at + item_weight<kMode>(p) + s.units - 1) - blockIdx.x) + 1;
       p.meta[blockIdx.x] = make_int4(s.b, s.j, parts, slot);
     }
     // (behind prefixes, parts < 0: no group names the sequence)
-    if (p.behind_prefix && prefix_group(p.prefix.tables, s.b) < 0) parts = -parts;
+    if (kMode == kBehind && prefix_group(p.prefix.tables, s.b) < 0) parts = -parts;
     if (p.item_meta) p.item_meta[static_cast<int64_t>(s.b) * p.c.heads * p.head_blocks + s.j] = make_int2(blockIdx.x, parts);
   }
   return slot;
@@ -396,10 +409,6 @@ bool make_plan(int H, const os_paged_cache& c, int ctas, int tile_keys, int item
 // The parameters of a launch that writes o and lse, without weights and states.
 DecodeParams decode_params(const Plan& pl, const PagedCache& c, const uint16_t* q, int64_t ld_q_batch, int64_t ld_q_head,
                            int H, float scale, uint16_t* o, float* lse, void* workspace, unsigned int* err);
-
-// The first kernel alone, ending in states (p.state_o) and the parts of cut items.
-// (pairs: over prefixes and own tokens, two sequences for each.)
-cudaError_t launch_states(const DecodeParams& p, bool f16, int D, int shares, bool pairs, cudaStream_t stream);
 
 // The second kernel of a launch that cuts items: their join.
 cudaError_t launch_join(const DecodeParams& p, bool f16, int D, int shares, cudaStream_t stream);

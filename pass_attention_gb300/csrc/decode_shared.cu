@@ -23,7 +23,7 @@
 
 #include <cstdint>
 
-#include "decode_paged.cuh"
+#include "decode_paged_kernel.cuh"
 #include "device_common.cuh"
 #include "launch.cuh"
 #include "oss_internal.h"
@@ -53,8 +53,8 @@ struct PrefixStates {
 
 // A warp takes every eighth part of the four rows, first the prefix's, then those of the
 // own tokens. Thread: row lane % 4, the vectors of 4 dims lane / 4, lane / 4 + 8, ...
-// kPairs: the prefix's parts and states are those of sequence 2 b of the decode's kernel.
-template <bool kF16, int D, bool kPairs>
+// kInPairs: the prefix's parts and states are those of sequence 2 b of the decode's kernel.
+template <bool kF16, int D, bool kInPairs>
 __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const DecodeParams p, const PrefixStates x) {
   constexpr int kVecs = D / 32;
   __shared__ float2 sml[kJoinWarps][kJoinRows];
@@ -69,11 +69,11 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
   const int in_block = in_group - hb * p.block_heads;
   wait_for_previous_kernel();
   const int per_seq = p.c.heads * p.head_blocks, item = g * p.head_blocks + hb;
-  int2 own, pre = make_int2(0, 0);  // kPairs: {first share, parts} of the prefix
+  int2 own, pre = make_int2(0, 0);  // kInPairs: {first share, parts} of the prefix
   int4 w = make_int4(0, 0, 0, 0);
   int parts = 0;  // of the prefix
   int64_t pre_row = row, own_row = row;
-  if constexpr (kPairs) {
+  if constexpr (kInPairs) {
     pre = p.item_meta[static_cast<int64_t>(2 * b) * per_seq + item];
     own = p.item_meta[static_cast<int64_t>(2 * b + 1) * per_seq + item];
     parts = pre.y;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
     float2 ml;
     const float4* src;
     int step = 8;  // vectors from one of this thread's to the next
-    if (!kPairs && i < parts) {
+    if (!kInPairs && i < parts) {
       if (w.y == 0) {
         ml = x.state_ml[row];
         src = x.state_o + row * (D / 4) + v0;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
         step = 8 * 128;
       }
     } else {
-      const bool first = i < parts;  // kPairs
+      const bool first = i < parts;  // kInPairs
       const int2 it = first ? pre : own;
       const int64_t of = first ? pre_row : own_row;
       if (it.y == 1) {
@@ -217,13 +217,13 @@ bool make_shared_plan(int H, const os_paged_cache& c, int groups, int prefix_max
   return true;
 }
 
-template <bool kPairs>
+template <bool kInPairs>
 cudaError_t launch_join(const DecodeParams& p, const PrefixStates& x, bool f16, int D, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.H;
   const dim3 grid(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
   const auto join = [&](auto* kernel) { return launch_after(kernel, grid, kJoinThreads, 0, stream, p, x); };
-  if (D == 128) return f16 ? join(decode_shared_join_kernel<true, 128, kPairs>) : join(decode_shared_join_kernel<false, 128, kPairs>);
-  return f16 ? join(decode_shared_join_kernel<true, 64, kPairs>) : join(decode_shared_join_kernel<false, 64, kPairs>);
+  if (D == 128) return f16 ? join(decode_shared_join_kernel<true, 128, kInPairs>) : join(decode_shared_join_kernel<false, 128, kInPairs>);
+  return f16 ? join(decode_shared_join_kernel<true, 64, kInPairs>) : join(decode_shared_join_kernel<false, 64, kInPairs>);
 }
 
 }  // namespace
@@ -254,9 +254,9 @@ cudaError_t launch_decode_shared(const uint16_t* q, int64_t ld_q_batch, int64_t 
   p.item_meta = reinterpret_cast<int2*>(ws + pl.item_meta);
   p.state_o = reinterpret_cast<float*>(ws + pl.state_o);
   p.state_ml = reinterpret_cast<float2*>(ws + pl.state_ml);
-  p.behind_prefix = pl.pairs ? 0 : 1;
   p.prefix = x;
-  if ((e = launch_states(p, f16, D, pl.own.shares, pl.pairs, stream)) != cudaSuccess) return e;
+  e = pl.pairs ? launch_kernel<kPairs>(p, f16, D, pl.own.shares, stream) : launch_kernel<kBehind>(p, f16, D, pl.own.shares, stream);
+  if (e != cudaSuccess) return e;
   if (pl.pairs) return launch_join<true>(p, PrefixStates{}, f16, D, stream);
   const PrefixStates states{reinterpret_cast<const int4*>(ws + pl.prefix.where),
                             reinterpret_cast<const float4*>(ws + pl.prefix.part_o),
