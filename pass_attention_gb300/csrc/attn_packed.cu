@@ -41,6 +41,11 @@
 // round are neighbours, so the K and V that the CTAs read at one time stay in L2
 // (rounds in launch_attn_packed).
 //
+// Prefixes. The same kernel reads prefixes that groups of sequences share (decode_shared.cu):
+// a group's queries are one sequence, its keys are in pages, and items end in states for
+// another kernel's join (kPrefix; lanes and the division of the SMs: prefix_split.cuh). 64 sequences, 4
+// heads a key head, behind 65536 tokens of 8 key heads: 54 KV steps a CTA at 0.93 us, 62 us.
+//
 // Foreign rows. The last KV tile of a sequence reaches into the next sequence's
 // rows, or into rows that nobody wrote. Their scores are replaced by -inf; their V
 // rows are set to zero in shared memory, since a weight of 0 times NaN or
