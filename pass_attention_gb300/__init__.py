@@ -981,11 +981,14 @@ def attention_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
 
 # -- the cache in 8 bits ---------------------------------------------------------------------
 
+_F8, _E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
 def _scale_strides(t: torch.Tensor, name: str, shape, device: torch.device):
     """Strides of the scales [pages, heads, page_size] of a pool."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float8_e8m0fnu or t.dim() != 3 or t.device != device \
+    if not isinstance(t, torch.Tensor) or t.dtype is not _E8 or t.dim() != 3 or t.device != device \
             or t.stride(2) != 1:
-        _refuse(t, name, 3, torch.float8_e8m0fnu, device)
+        _refuse(t, name, 3, _E8, device)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, a scale for each row of the pages")
     st = t.stride()
@@ -998,16 +1001,52 @@ def _scale_strides(t: torch.Tensor, name: str, shape, device: torch.device):
 def _cache_fp8(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype):
     """``(os_paged_cache_fp8, device, batch, heads, head_dim)`` of these tensors, for
     calls whose 16-bit tensors are of ``dtype``."""
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype is not torch.float8_e4m3fn:
+    try:
+        st, ss, shape, index = k_pages.stride(), k_scales.stride(), k_pages.shape, k_pages.get_device()
+        plain = (k_pages.dtype is _F8 and v_pages.dtype is _F8 and k_scales.dtype is _E8 and v_scales.dtype is _E8
+                 and page_table.dtype is torch.int32 and kv_len.dtype is torch.int32 and dtype in _DTYPE_CODES
+                 and 0 <= index == v_pages.get_device() == k_scales.get_device() == v_scales.get_device()
+                 == page_table.get_device() == kv_len.get_device()
+                 and len(shape) == 4 and v_pages.shape == shape and v_pages.stride() == st and v_scales.stride() == ss
+                 and k_scales.shape == v_scales.shape == shape[:3] and st[3] == ss[2] == 1
+                 and not (st[0] | st[1] | st[2] | ss[0] | ss[1]) & 15)
+    except (AttributeError, RuntimeError):
+        plain = False
+    if plain:
+        dev, rows, lens = k_pages.device, page_table.shape, kv_len.shape
+        ld_table = page_table.stride()
+        plain = len(rows) == 2 and len(lens) == 1 and ld_table[1] == 1 and kv_len.stride() == (1,)
+    if not plain:
+        dev, st, ss = _cache_fp8_checked(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype)
+        shape, rows, lens, ld_table = k_pages.shape, page_table.shape, kv_len.shape, page_table.stride()
+    pages, heads, page_size, d = shape
+    batch, max_pages = rows
+    if lens[0] != batch:
+        raise ValueError("kv_len must have one entry for each row of page_table")
+    try:
+        packed = _PAGED_CACHE_FP8.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
+                                       page_table.data_ptr(), ld_table[0], kv_len.data_ptr(), pages, heads,
+                                       page_size, d, _DTYPE_CODES[dtype], batch, max_pages, k_scales.data_ptr(),
+                                       v_scales.data_ptr(), ss[0], ss[1])
+    except struct.error:
+        raise ValueError("more pages than 32 bits count") from None
+    return packed, dev, batch, heads, d
+
+
+def _cache_fp8_checked(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype):
+    """The device and strides of a cache that the quick check has not passed: a view
+    off the common path, or what is wrong with it is raised."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype is not _F8:
         raise TypeError("k_pages must be a float8_e4m3fn torch.Tensor")
     if not k_pages.is_cuda:
         raise ValueError("k_pages must be a CUDA tensor (liboss has no CPU path)")
     if dtype not in _DTYPE_CODES:
         raise TypeError(f"{dtype} is neither bfloat16 nor float16")
     dev = k_pages.device
-    st = _pair(k_pages, v_pages, ("k_pages", "v_pages"), 4, torch.float8_e4m3fn, dev)
+    st = _pair(k_pages, v_pages, ("k_pages", "v_pages"), 4, _F8, dev)
     shape = k_pages.shape
     if (st[0] | st[1] | st[2]) & 15:
+        # a stride off the grid matters only where it is walked
         st = tuple(0 if n == 1 and x & 15 else x for n, x in zip(shape, st))
     ss = _scale_strides(k_scales, "k_scales", shape[:3], dev)
     sv = _scale_strides(v_scales, "v_scales", shape[:3], dev)
@@ -1015,18 +1054,7 @@ def _cache_fp8(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype):
         raise ValueError("k_scales and v_scales must have the same strides")
     _ints(page_table, "page_table", 2, dev)
     _ints(kv_len, "kv_len", 1, dev)
-    pages, heads, page_size, d = shape
-    batch, max_pages = page_table.shape
-    if kv_len.shape[0] != batch:
-        raise ValueError("kv_len must have one entry for each row of page_table")
-    try:
-        packed = _PAGED_CACHE_FP8.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2],
-                                       page_table.data_ptr(), page_table.stride(0), kv_len.data_ptr(), pages, heads,
-                                       page_size, d, _DTYPE_CODES[dtype], batch, max_pages, k_scales.data_ptr(),
-                                       v_scales.data_ptr(), ss[0], ss[1])
-    except struct.error:
-        raise ValueError("more pages than 32 bits count") from None
-    return packed, dev, batch, heads, d
+    return dev, st, ss
 
 
 def _seqlens(cu_seqlens: torch.Tensor, batch: int, dev: torch.device) -> int:
