@@ -277,21 +277,24 @@ __device__ __forceinline__ Lanes find_lanes(const PackedParams& p, unsigned long
 // The same as find_shares, for up to kWarpGroups groups: one way to memory and two CTA
 // barriers. Warp 0 looks for the share's beginning, warp 1 for its end. (find_shares took
 // 4.2 of the 16 us of a small launch of one group.) `scratch` [kThreads / 32].
-__device__ __forceinline__ void find_prefix_share(const PackedParams& p, Shares* sh, int64_t* scratch) {
+__device__ __forceinline__ void find_prefix_share(const PackedParams& p, Shares* sh, float* scratch) {
   constexpr uint32_t kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = warp;
   const PrefixLaunch& x = p.prefix.launch;
   PackedSeq s = packed_seq(RowRange{0, 0, false}, RowRange{0, 0, false}, p.pos_shift);
-  if (warp < 2 && lane < p.batch) s = prefix_seq(x.tables, lane, x.batch, x.page_shift, x.pos_shift);
-  int64_t own = 0;
-  OSS_ROLLED
-  for (int b = threadIdx.x; x.bytes_cost > 0 && b < x.batch; b += kThreads)
-    own += own_units(paged_length(p.prefix.kv_len[b], p.prefix.own_max_pages, x.page_shift));
-  own = warp_scan(own);
-  if (lane == 31) scratch[warp] = own;
-  __syncthreads();
+  const int mine = p.batch == 1 ? 0 : lane;
+  if (warp < 2 && mine < p.batch) s = prefix_seq(x.tables, mine, x.batch, x.page_shift, x.pos_shift);
+  float own = 0.f;
+  if (x.bytes_cost > 0) {
+    OSS_ROLLED
+    for (int b = threadIdx.x; b < x.batch; b += kThreads)
+      own += static_cast<float>(own_units(paged_length(p.prefix.kv_len[b], p.prefix.own_max_pages, x.page_shift)));
+    own = sum_of_warp(own);
+    if (lane == 0) scratch[warp] = own;
+    __syncthreads();
+    own = sum_of_warp(lane < kThreads / 32 ? scratch[lane] : 0.f) * static_cast<float>(x.per_seq);
+  }
   if (warp < 2) {
-    own = __shfl_sync(kAll, warp_scan(lane < kThreads / 32 ? scratch[lane] : 0), 31) * x.per_seq;
     if (e == 0 && blockIdx.x == 0 && p.cu_q && lane < p.batch && row_range(p.cu_q[lane], p.cu_q[lane + 1], p.tokens_q).clamped)
       report_error(p.err, kKernelPaged | (kSiteBadOffsets << 8));
     const PrefixDivision d = divide_prefix(x, s, own);
@@ -308,10 +311,15 @@ __device__ __forceinline__ void find_prefix_share(const PackedParams& p, Shares*
       if (at == d.total) {
         end = ShareEnd{d.total, 0};
       } else {
-        k = __ffs(__ballot_sync(kAll, d.upto * p.packs > at)) - 1;
-        const int64_t mine = static_cast<int64_t>(d.s.tiles) * d.places;
-        const int64_t len = __shfl_sync(kAll, mine, k), before = __shfl_sync(kAll, d.upto - mine, k) * p.packs;
-        const int each = __shfl_sync(kAll, d.places, k), steps = each - kTileWeight;
+        int64_t len = static_cast<int64_t>(d.s.tiles) * d.places, before = (d.upto - len) * p.packs;
+        int each = d.places;
+        if (p.batch > 1) {
+          k = __ffs(__ballot_sync(kAll, d.upto * p.packs > at)) - 1;
+          len = __shfl_sync(kAll, len, k);
+          before = __shfl_sync(kAll, before, k);
+          each = __shfl_sync(kAll, each, k);
+        }
+        const int steps = each - kTileWeight;
         const int pack = small_quotient(at - before, len);
         const int64_t in_pack = at - before - pack * len;
         const int tile = small_quotient(in_pack, each);
@@ -639,7 +647,7 @@ attn_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if constexpr (kPrefix) let_next_kernel_start();
   if (!kPrefix && threadIdx.x < p.rounds) p.meta[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
   if (kPrefix && p.batch <= kWarpGroups)
-    find_prefix_share(p, &shares, reinterpret_cast<int64_t*>(row_ml));
+    find_prefix_share(p, &shares, reinterpret_cast<float*>(row_ml));
   else
     find_shares<kPrefix>(p, &shares, reinterpret_cast<int64_t*>(row_ml), reinterpret_cast<uint32_t*>(row_ml + 2 * kThreads / 32));  // its barriers publish the set-up above
   tc_fence_after();

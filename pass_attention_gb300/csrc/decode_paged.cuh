@@ -221,11 +221,13 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys, kM
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = seq_count<kMode>(p), per = (count + kThreads - 1) / kThreads;
   const int b0 = min(count, static_cast<int>(threadIdx.x) * per), b1 = min(count, b0 + per);
-  int64_t mine = 0, own = 0;
+  int64_t mine = 0;
+  float own = 0.f;
   PackedSeq group = packed_seq(RowRange{0, 0, false}, RowRange{0, 0, false}, 0);
   const bool split = kMode == kBehind && p.prefix.bytes_cost > 0 && p.prefix.tables.groups <= kWarpGroups;  // SMs are left to the prefixes
-  if (split && threadIdx.x < p.prefix.tables.groups)
-    group = prefix_seq(p.prefix.tables, threadIdx.x, p.prefix.batch, p.prefix.page_shift, p.prefix.pos_shift);
+  const int g = p.prefix.tables.groups == 1 ? 0 : threadIdx.x;
+  if (split && warp == 0 && g < p.prefix.tables.groups)
+    group = prefix_seq(p.prefix.tables, g, p.prefix.batch, p.prefix.page_shift, p.prefix.pos_shift);
   if constexpr (kMode == kPairs) {
     const PrefixTables& t = p.prefix.tables;
     for (int g = threadIdx.x; t.cu && blockIdx.x == 0 && g < t.groups; g += kThreads)
@@ -234,7 +236,7 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys, kM
   for (int b = b0; b < b1; ++b) {
     const int len = seq_len<kMode>(p, b);
     mine += Walk::units_of(p, len) + item_weight<kMode>(p);
-    own += own_units(len);
+    if (split) own += static_cast<float>(own_units(len));
   }
   int64_t upto = mine;
 #pragma unroll
@@ -254,16 +256,16 @@ __device__ __forceinline__ bool find_share(const DecodeParams& p, Walk<kKeys, kM
   const int64_t W = all * per_seq;
   int ctas = gridDim.x;
   if (split) {
-    __shared__ int64_t warp_own[kWarps];
+    __shared__ float warp_own[kWarps];
     __shared__ int left;
-    own = warp_scan(own);
-    if (lane == 31) warp_own[warp] = own;
+    own = sum_of_warp(own);
+    if (lane == 0) warp_own[warp] = own;
     __syncthreads();
     if (warp == 0) {
-      own = 0;
+      own = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) own += warp_own[i];
-      const PrefixDivision d = divide_prefix(p.prefix, group, own * p.prefix.per_seq);
+      const PrefixDivision d = divide_prefix(p.prefix, group, own * static_cast<float>(p.prefix.per_seq));
       if (lane == 0) left = d.split ? p.prefix.sms - static_cast<int>(d.cut.count) * d.count : 0;
     }
     __syncthreads();

@@ -16,7 +16,7 @@
 // that came before the first has ended, and waits for the first at its own end.
 //
 // Measured, 32 heads over 8 of 128: 64 sequences of up to 1000 tokens behind 8192: 46 us (183 MB:
-// 27 us of HBM's time); of up to 2500 behind 65536: 110 us (566 MB: 85 us). With one table a
+// 27 us of HBM's time); of up to 2500 behind 65536: 107 us (566 MB: 85 us). With one table a
 // sequence, every one of them with the prefix's pages in front, the paged decode takes 193
 // and 1455 us. Of a launch, 5 us are the way to the first product, and 6 the join with its two
 // hand-overs.

@@ -106,35 +106,57 @@ constexpr int kUnitBytesCost = 12;  // a unit's bytes, when all SMs share HBM
 // 8, 8192, 1000: 54.5 / 46.4; 64, 32 / 8, 65536, 2500: 119 / 111; 8, 32 / 8, 32768, 8192: 76.9 /
 // 63.8; 4, 8 / 1, 100000, 3000: 53.3 / 42.7; and where the rule keeps them apart, forced:
 // 64, 64 / 4, 16384, 1000: 62 / 71; 256, 32 / 8, 16384, 512: 130 / 154.
-__device__ __forceinline__ int prefix_ctas(const PrefixLaunch& x, int64_t steps, int64_t units) {
-  const int64_t own = kItemCost * static_cast<int64_t>(x.batch) * x.per_seq + x.unit_cost * units;
-  if (x.bytes_cost * units <= own) return x.sms;
-  return static_cast<int>(x.sms * (x.step_cost * steps) / (x.step_cost * steps + own));
+__device__ __forceinline__ int prefix_ctas(const PrefixLaunch& x, float steps, float units) {
+  const float own = static_cast<float>(kItemCost * x.per_seq) * static_cast<float>(x.batch) + static_cast<float>(x.unit_cost) * units;
+  if (static_cast<float>(x.bytes_cost) * units <= own) return x.sms;
+  const float mine = static_cast<float>(x.step_cost) * steps;
+  return static_cast<int>(static_cast<float>(x.sms) * __fdividef(mine, mine + own));
 }
 
-// One warp, converged. s: of this lane's group, or without tiles; units: of all own tokens.
-__device__ __forceinline__ PrefixDivision divide_prefix(const PrefixLaunch& x, PackedSeq s, int64_t units) {
+// One warp, converged. s: of this lane's group, or without tiles (one group: the same for all
+// lanes); units: of all own tokens. This runs at the front of both kernels, where every
+// instruction is fetched for the first time: the split of the SMs in floats, no scans for
+// one group (3.2 us of a launch with 64-bit divisions and scans in any case).
+__device__ __forceinline__ PrefixDivision divide_prefix(const PrefixLaunch& x, PackedSeq s, float units) {
   constexpr uint32_t kAll = 0xffffffffu;
+  const bool one = x.tables.groups == 1;
   PrefixDivision d;
   d.places = kTileWeight + kv_tiles(s, 0, x.pos_shift, false);
   const int32_t tiles = s.tiles;
-  d.count = lane_count(max(1, __reduce_max_sync(kAll, tiles)));
+  d.count = lane_count(max(1, one ? tiles : __reduce_max_sync(kAll, tiles)));
   s.tiles = (tiles + d.count - 1) / d.count;
-  const int64_t real = __shfl_sync(kAll, warp_scan(static_cast<int64_t>(tiles) * d.places), 31);
-  d.upto = warp_scan(static_cast<int64_t>(s.tiles) * d.places);
-  if (too_many_lanes(d.count, x.sms, real, __shfl_sync(kAll, d.upto, 31) * d.count)) {
+  int64_t real = static_cast<int64_t>(tiles) * d.places;
+  d.upto = static_cast<int64_t>(s.tiles) * d.places;
+  d.total = d.upto;
+  if (!one) {
+    real = __shfl_sync(kAll, warp_scan(real), 31);
+    d.upto = warp_scan(d.upto);
+    d.total = __shfl_sync(kAll, d.upto, 31);
+  }
+  if (too_many_lanes(d.count, x.sms, real, d.total * d.count)) {
     d.count = 1;
     s.tiles = tiles;
-    d.upto = warp_scan(static_cast<int64_t>(tiles) * d.places);
+    d.upto = d.total = static_cast<int64_t>(tiles) * d.places;
+    if (!one) {
+      d.upto = warp_scan(d.upto);
+      d.total = real;
+    }
   }
   d.s = s;
-  d.total = __shfl_sync(kAll, d.upto, 31) * x.packs;
-  const int ctas = prefix_ctas(x, d.total * d.count, units);
+  d.total *= x.packs;
+  const int ctas = prefix_ctas(x, static_cast<float>(d.total) * static_cast<float>(d.count), units);
   d.split = ctas < x.sms;
   d.sets = static_cast<uint32_t>(max(1, min((ctas + d.count / 2) / d.count, x.sms / d.count)));
-  const int64_t items = static_cast<int64_t>(__reduce_add_sync(kAll, static_cast<uint32_t>(s.tiles))) * x.packs;
-  d.cut = share_cut(d.total, share_count(d.total, items, d.sets, 1, kPrefixShareShift));
+  const uint32_t all_tiles = one ? static_cast<uint32_t>(s.tiles) : __reduce_add_sync(kAll, static_cast<uint32_t>(s.tiles));
+  d.cut = share_cut(d.total, share_count(d.total, static_cast<int64_t>(all_tiles) * x.packs, d.sets, 1, kPrefixShareShift));
   return d;
+}
+
+// Sum over a warp, in every lane.
+__device__ __forceinline__ float sum_of_warp(float x) {
+  OSS_ROLLED
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
 }
 
 }  // namespace oss
