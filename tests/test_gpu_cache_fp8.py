@@ -2,6 +2,7 @@
 definitions in 64 bits (GPU)."""
 
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -597,4 +598,76 @@ def test_a_step_in_a_graph_follows_the_cache():
         assert kv_len.tolist() == [53, 4020]
         check_decode_fp8(o, lse, new[0], *cache, table, kv_len, 1 / math.sqrt(d))
         assert torch.equal(o, oss.attention_decode_paged_fp8(new[0], *cache, table, kv_len)[0])
+    assert oss.check_device_error() == 0
+
+
+def test_on_other_streams_and_from_several_threads():
+    # calls on streams of their own, and threads that share one: the same bytes from all
+    lens = [1500, 20, 700]
+    q, cache = make(lens, 8, 2, page=32, seed=33)
+    cu, total = ints([0, 1500, 1520, 2220]), 2220
+    want = (*oss.attention_decode_paged_fp8(q, *cache), *oss.kv_cache_read_fp8(*cache, cu, total))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(stream):
+        out = pools(cache[0].shape[0], 2, 32, 128, "head")
+        for _ in range(20):
+            got = (*oss.attention_decode_paged_fp8(q, *cache, stream=stream),
+                   *oss.kv_cache_read_fp8(*cache, cu, total, stream=stream))
+            oss.kv_cache_append_fp8(want[2], want[3], *out, *cache[4:], cu, stream=stream)
+            torch.cuda.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                wrong.append(stream)
+        k, _ = oss.kv_cache_read_fp8(*out, *cache[4:], cu, total)
+        if not torch.equal(k, want[2]):
+            wrong.append("append")
+
+    shared = torch.cuda.Stream()
+    threads = [threading.Thread(target=work, args=(s,)) for s in (None, shared, shared, torch.cuda.Stream())]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert oss.check_device_error() == 0
+
+
+def test_a_captured_read_follows_the_lengths():
+    q, cache = make([300, 40], 4, 2, seed=34)
+    kv_len, cu = cache[5], ints([0, 300, 340])
+    full = oss.kv_cache_read_fp8(*cache, cu, 340)
+    torch.cuda.synchronize()
+    k, v = (torch.zeros((340, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        oss.kv_cache_read_fp8(*cache, cu, 340, k=k, v=v)
+    for n in ([300, 40], [17, 3], [0, 40]):
+        kv_len.copy_(ints(n))
+        cu.copy_(ints([0, n[0], sum(n)]))
+        k.fill_(5.0)
+        v.fill_(5.0)
+        graph.replay()
+        for got, ref in ((k, full[0]), (v, full[1])):
+            assert torch.equal(got[:n[0]], ref[:n[0]]) and torch.equal(got[n[0]:sum(n)], ref[300:300 + n[1]])
+            assert torch.all(got[sum(n):] == 5.0)
+    assert oss.check_device_error() == 0
+
+
+def test_outputs_have_guards():
+    # nothing around o and lse, and around the rows read back, is written
+    q, cache = make([70, 0, 333], 12, 4, d=64, seed=35)
+    cu = ints([0, 70, 70, 403])
+    for n, call in (((3, 12, 64), "o"), ((403, 4, 64), "k")):
+        size = math.prod(n)
+        flat = [torch.full((size + 256,), 7.0, dtype=q.dtype, device="cuda") for _ in range(2)]
+        x, y = (f[128:128 + size].view(n) for f in flat)
+        lse = torch.full((3 * 12 + 64,), 7.0, device="cuda")
+        if call == "o":
+            oss.attention_decode_paged_fp8(q, *cache, o=x, lse=lse[32:32 + 36].view(3, 12))
+            assert torch.all(lse[:32] == 7.0) and torch.all(lse[68:] == 7.0) and not torch.any(lse[32:68] == 7.0)
+        else:
+            oss.kv_cache_read_fp8(*cache, cu, 403, k=x, v=y)
+        for f in flat:
+            assert torch.all(f[:128] == 7.0) and torch.all(f[128 + size:] == 7.0)
     assert oss.check_device_error() == 0

@@ -304,6 +304,35 @@ def test_from_several_threads():
     assert oss.check_device_error() == 0
 
 
+def test_outputs_have_guards():
+    c = Case([2, 3], [300, 20], [0, 1, 40, 0, 333], 12, 4, d=64, seed=18)
+    flat, lse = torch.full((5 * 12 * 64 + 256,), 7.0, dtype=c.q.dtype, device="cuda"), torch.full((5 * 12 + 64,), 7.0, device="cuda")
+    o, l = flat[128:-128].view(5, 12, 64), lse[32:-32].view(5, 12)
+    c.run(o=o, lse=l)
+    c.check(o, l)
+    assert torch.all(flat[:128] == 7.0) and torch.all(flat[-128:] == 7.0)
+    assert torch.all(lse[:32] == 7.0) and torch.all(lse[-32:] == 7.0)
+
+
+def test_behind_kernels_that_write_what_it_reads():
+    # lengths, tables, queries and cached rows come from kernels right before the call, and
+    # what the buffers held before is the last step's
+    c = Case([5, 4], [900, 300], [100, 0, 31, 64, 17, 1, 1, 80, 5], 8, 2, page=32, seed=19)
+    names = ("q", "kp", "vp", "prefix_table", "prefix_len", "table", "kv_len", "cu")
+    want, good = c.run(), {n: getattr(c, n).clone() for n in names}
+    torch.cuda.synchronize()
+    for i in range(10):
+        for n in names:  # empty groups and sequences, other values
+            x = getattr(c, n)
+            x.zero_() if n in ("kv_len", "prefix_len", "cu") else x.fill_(0 if "table" in n else i)
+        c.run()
+        for n in names:
+            getattr(c, n).copy_(good[n])
+        o, lse = c.run()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert oss.check_device_error() == 0
+
+
 def test_the_binding_refuses():
     c = Case([2, 2], [64, 40], [16, 30, 0, 5], 4, 2, seed=9)
     q, kp, vp, pt, pn, table, kv_len = c.args()
