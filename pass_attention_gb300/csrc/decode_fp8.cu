@@ -27,9 +27,9 @@
 // time: 711 cycles of a scheduler for 16 keys of 128. It takes about 344 instructions (436
 // with addresses formed anew for every tile, masks and guards in every weight), so three CTAs
 // an SM (two: 129 against 116 us at that point) and the next tile's products beside this one's
-// softmax (106.5 -> 104.5). 64 sequences of up to 8192 tokens, 32 heads over 8: 104.5 us (5.9 TB/s, 0.88 of
-// the copy peak, 8 us of it the launch's beginning and end); 6 of up to 32768, 16 heads of 64 in
-// fp16: 61.7 us (0.80: instructions; a tile there has 32 keys, 68.6 with 16); one of 777 tokens
+// softmax (106.5 -> 104.5). 64 sequences of up to 8192 tokens, 32 heads over 8: 102 us (6.0 TB/s, 0.90 of
+// the copy peak, 6 us of it the launch's beginning and end); 6 of up to 32768, 16 heads of 64 in
+// fp16: 58 us (0.85: instructions; a tile there has 32 keys, 7 us more with 16); one of 777 tokens
 // 7.2 us from a graph.
 
 #include <atomic>

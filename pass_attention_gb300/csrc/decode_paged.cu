@@ -216,13 +216,15 @@ decode_finish_kernel(const DecodeParams p, int adds, int chunks, float* weights,
   }
   i -= adds;
   wait_for_previous_kernel();
-  join_head<kF16, D>(p, i / p.block_heads, i % p.block_heads);
+  const int heads = min(p.group, p.block_heads);
+  join_head<kF16, D>(p, i / heads, i % heads);
 }
 
 template <bool kF16, int D>
 cudaError_t launch_finish(const DecodeParams& p, int shares, float* weights, int64_t ld_w_batch, int64_t ld_w_head,
                           cudaStream_t stream) {
-  const int64_t joins = p.unit_tiles == kUnitTiles ? static_cast<int64_t>(shares) * p.block_heads : 0;
+  const int heads = p.group < p.block_heads ? p.group : p.block_heads;
+  const int64_t joins = p.unit_tiles == kUnitTiles ? static_cast<int64_t>(shares) * heads : 0;
   const int64_t chunks = weights ? ((static_cast<int64_t>(p.c.max_pages) << p.c.page_shift) + kAddKeys - 1) / kAddKeys : 0;
   const int64_t adds = chunks * p.c.heads * p.c.batch, ctas = adds + joins;
   if (ctas > 0x7fffffff) return cudaErrorNotSupported;
