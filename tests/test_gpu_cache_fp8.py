@@ -2,6 +2,7 @@
 definitions in 64 bits (GPU)."""
 
 import math
+import random
 import threading
 
 import numpy as np
@@ -122,6 +123,16 @@ def test_decode_pages_and_layouts(page, layout, d):
 ])
 def test_decode_long_and_many(lens, hq, hkv, d, dtype):
     decode(lens, hq, hkv, page=64, d=d, dtype=dtype, seed=len(lens))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_decode_random_batches(seed):
+    r = random.Random(seed)
+    lens = [r.choice((0, 1, 16, r.randint(1, 300), r.randint(1, 3000))) for _ in range(r.choice((1, 2, 5, 12)))]
+    hkv = r.choice((1, 1, 2, 3, 5))
+    hq = hkv * r.choice((1, 2, 3, 4, 6, 8, 9, 16, 17, 40))
+    decode(lens, hq, hkv, d=r.choice((64, 128)), dtype=r.choice(("bf16", "f16")), page=r.choice((16, 32, 128, 256)),
+           layout=r.choice(("head", "slot", "joint")), columns=r.choice((None, 250)), seed=seed)
 
 
 def test_decode_one_heavy_key():

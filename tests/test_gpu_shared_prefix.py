@@ -2,6 +2,7 @@
 attention_decode_paged (GPU)."""
 
 import math
+import random
 import threading
 
 import numpy as np
@@ -257,6 +258,22 @@ def test_offsets_that_do_not_fit_are_reported(cu):
     with pytest.raises(oss.OssError, match="OS_ERR_BAD_INDEX"):
         oss.check_device_error()
     assert oss.check_device_error() == 0
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed):
+    r = random.Random(seed)
+    sizes = [r.choice((0, 1, 1, 2, 7, r.randint(1, 40))) for _ in range(r.choice((1, 1, 2, 5, 34)))]
+    sizes[-1] = max(sizes[-1], 1)
+    outside = r.choice((0, 0, 2))
+    n = sum(sizes) + outside
+    prefixes = [r.choice((0, 1, 100, 128, r.randint(1, 3000))) for _ in sizes]
+    own = [r.choice((0, 1, r.randint(1, 100), r.randint(1, 900))) for _ in range(n)]
+    hkv = r.choice((1, 1, 2, 3, 4))
+    hq = hkv * r.choice((1, 2, 3, 4, 6, 8, 9, 16, 17, 40))
+    c = Case(sizes, prefixes, own, hq, hkv, d=r.choice((64, 128)), dtype=r.choice(("bf16", "f16")),
+             page=r.choice((16, 32, 128, 256)), layout=r.choice(("head", "slot", "joint")), outside=outside, seed=seed)
+    c.go(rows=sorted(set(r.sample(range(n), min(n, 3)) + [n - 1])))
 
 
 def test_as_the_paged_decode_over_the_same_tokens():
