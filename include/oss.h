@@ -782,9 +782,10 @@ OSS_API os_status os_kv_cache_read_fp8(const os_paged_cache_fp8* cache, const in
  * os_attention_decode_paged_fp8 -- os_attention_decode_paged (without the sums of
  * weights) over a cache in 8 bits: k_t and v_t are the values that the cached rows
  * stand for. The products run in fp16 with fp32 sums, with the rows' scales as
- * exponents beside them: codes are exact in fp16, q is (a bf16 q by its head's
- * power of two, elements below 2^-39 of the head's largest aside), and
- * the weights are rounded to fp16. A key row that is NaN gives NaN in o and lse,
+ * exponents beside them: codes are exact in fp16, and so is q (a bf16 q by its head's
+ * power of two; elements below 2^-32 of the head's largest are off by up to 2^-40 of
+ * it). The weights, times their value row's scale, are rounded to fp16 (what is below
+ * 2^-25 of the largest, to 0). A key row that is NaN gives NaN in o and lse,
  * a value row that is NaN in o.
  * q, o, lse, scale, H, workspace, alignment and errors as in
  * os_attention_decode_paged.

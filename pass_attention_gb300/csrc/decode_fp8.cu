@@ -8,8 +8,9 @@
 // Products. Codes are exact in fp16 (4 significant bits, 2^-9 to 448), so both products
 // run as fp16 mma.sync with fp32 sums, whatever the type of q and o. (An e4m3 MMA would want q
 // and the weights in 8 bits.) A bf16 q is brought into fp16's range by a power of two per
-// head: its largest element comes to 2^14 .. 2^15, and what then falls below fp16's
-// normal range is below 2^-28 of it.
+// head: its largest element comes to 2^15 .. 2^16 (255/128 2^15 at most, fp16 ends at 2047/1024 2^15). All
+// 8 bits of an element then fit down to 2^-17, 2^-32 of the largest; below that it is off by up to 2^-25,
+// half of fp16's least step and 2^-40 of the largest.
 //
 // Scales. The key's is a factor on the score. The value's goes into the weight's
 // exponent, 2^(s + ev - m'), so V needs no multiplication. Weights of values far larger
@@ -212,12 +213,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // exponent field n of the largest: times 2^(127 + 14 - n); NaN, infinity and 0 as
+        // exponent field n of the largest: times 2^(127 + 15 - n); NaN, infinity and 0 as
         // they are, and below 2^-100 no further up than from there
         const uint32_t n = max(top >> 7, 27u);
         const bool plain = top >= 0x7f80u;
-        const float to = plain ? 1.f : __uint_as_float((127u + 127u + 14u - n) << 23);
-        up = plain ? 1.f : __uint_as_float((n - 14u) << 23);  // 1 / to
+        const float to = plain ? 1.f : __uint_as_float((127u + 127u + 15u - n) << 23);
+        up = plain ? 1.f : __uint_as_float((n - 15u) << 23);  // 1 / to
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
