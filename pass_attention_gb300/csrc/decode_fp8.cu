@@ -67,6 +67,15 @@ struct Shape {
 // a special case (-inf - kNone is -inf still).
 constexpr float kNone = -3.402823466e+38f;
 
+// A score is its sum times one factor, of the query's and the key's powers of two: a large query over
+// small keys would leave fp32's range between them. Where the factor itself does, every sum
+// but 0 is far beyond it too, and 0 is to stay 0. (NaN stays NaN.)
+__device__ __forceinline__ float finite(float x) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(3.402823466e+38f));
+  return y;
+}
+
 // Byte offset of 16-byte chunk c of row r of a tile, so that eight rows of a chunk
 // touch all banks.
 template <int D>
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_fp8_kernel(c
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[b][nt][e] = (sc[b][nt][0][e] + sc[b][nt][1][e]) * qs[nt][e & 1] * kf[e >> 1];
+            x[b][nt][e] = (sc[b][nt][0][e] + sc[b][nt][1][e]) * finite(qs[nt][e & 1] * kf[e >> 1]);
             y[b][nt][e] = x[b][nt][e] + vf[e >> 1];
           }
       }
