@@ -138,7 +138,7 @@ __device__ __forceinline__ void join_head(const DecodeParams& p, int share, int 
 // has one thread and a fixed order. A cut item's lse is formed here from its
 // parts, so that this does not wait for the join; the scores are on their way
 // meanwhile.
-__device__ __forceinline__ void add_weights(const DecodeParams& p, int b, int g, int chunk, float* __restrict__ weights) {
+__device__ __forceinline__ void add_weights(const DecodeParams& p, int b, int g, int chunk, float* weights) {
   __shared__ float lse2[kMaxHeadBlock];
   // (the lengths too may come from a kernel that still runs, one before the first
   // kernel: an eviction writes them)

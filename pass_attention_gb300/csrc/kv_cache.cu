@@ -50,9 +50,8 @@ constexpr int kAppendThreads = 256;
 // One 16-byte chunk of K and of V per thread; a token's chunks are contiguous
 // over the threads.
 __global__ void __launch_bounds__(kAppendThreads)
-kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t ld_token,
-                 int64_t ld_head, int64_t tokens, const int32_t* __restrict__ cu, PagedCache c,
-                 uint16_t* k_pages, uint16_t* v_pages, int chunks_per_head, unsigned int* err) {
+kv_append_kernel(const uint16_t* k, const uint16_t* v, int64_t ld_token, int64_t ld_head, int64_t tokens, const int32_t* cu,
+                 PagedCache c, uint16_t* k_pages, uint16_t* v_pages, int chunks_per_head, unsigned int* err) {
   let_next_kernel_start();
   wait_for_previous_kernel();
   // offsets that do not fit the rows: tokens that kv_len counts are not written
@@ -89,8 +88,9 @@ kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
     const int slot = static_cast<int>(pos) & ((1 << c.page_shift) - 1);
     const int64_t from = token * ld_token + head * ld_head + chunk * 8;
     const int64_t to = pool_offset(page, head, slot, c.ld_page, c.ld_head, c.ld_slot) + chunk * 8;
-    *reinterpret_cast<uint4*>(k_pages + to) = *reinterpret_cast<const uint4*>(k + from);
-    *reinterpret_cast<uint4*>(v_pages + to) = *reinterpret_cast<const uint4*>(v + from);
+    const uint4 key = *reinterpret_cast<const uint4*>(k + from), value = *reinterpret_cast<const uint4*>(v + from);
+    *reinterpret_cast<uint4*>(k_pages + to) = key;
+    *reinterpret_cast<uint4*>(v_pages + to) = value;
   }
 }
 

@@ -35,7 +35,7 @@ __device__ __forceinline__ void check_offsets(const int32_t* cu, int32_t batch, 
 
 // Page and slot of packed row `token` (cu null: the last token of sequence `token`);
 // false for a row without one.
-__device__ __forceinline__ bool locate(int32_t token, const int32_t* __restrict__ cu, const PagedCache& c, int* page,
+__device__ __forceinline__ bool locate(int32_t token, const int32_t* cu, const PagedCache& c, int* page,
                                        int* slot, unsigned int* err) {
   int seq = token;
   int64_t behind = 1;  // tokens of the sequence from this one on
@@ -121,8 +121,8 @@ struct Piece {
 // D / 16 threads a row.
 template <bool kF16, int kLanes, int kHeads>
 __global__ void __launch_bounds__(kThreads)
-kv_append_fp8_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t ld_token, int64_t ld_head,
-                     int64_t tokens, const int32_t* __restrict__ cu, PagedCache c, Fp8Pools f, unsigned int* err) {
+kv_append_fp8_kernel(const uint16_t* k, const uint16_t* v, int64_t ld_token, int64_t ld_head,
+                     int64_t tokens, const int32_t* cu, PagedCache c, Fp8Pools f, unsigned int* err) {
   using Piece = Piece<kLanes, kHeads>;
   constexpr int kHalf = kLanes * 8;
   let_next_kernel_start();
@@ -176,8 +176,8 @@ __device__ __forceinline__ uint4 values(uint2 codes, float scale) {
 
 template <bool kF16, int kLanes, int kHeads>
 __global__ void __launch_bounds__(kThreads)
-kv_read_fp8_kernel(PagedCache c, Fp8Pools f, const int32_t* __restrict__ cu, int64_t tokens, uint16_t* __restrict__ k,
-                   uint16_t* __restrict__ v, int64_t ld_token, int64_t ld_head, unsigned int* err) {
+kv_read_fp8_kernel(PagedCache c, Fp8Pools f, const int32_t* cu, int64_t tokens, uint16_t* k,
+                   uint16_t* v, int64_t ld_token, int64_t ld_head, unsigned int* err) {
   using Piece = Piece<kLanes, kHeads>;
   constexpr int kHalf = kLanes * 8;
   let_next_kernel_start();

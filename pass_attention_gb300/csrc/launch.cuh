@@ -4,6 +4,9 @@
 // reads or writes. Every CTA calls it, also one that has nothing to do: a kernel
 // that ended without waiting would let the next one start before the one
 // before it has ended. (begin_behind_waiting_kernel() is the exception.)
+// Pointers of these kernels carry no __restrict__: it says that nobody else writes what they
+// point to while the kernel runs, and lets the compiler move loads across the wait or through
+// the path for data that does not change. Until the wait that is not so.
 #pragma once
 
 #include <cuda_runtime.h>
