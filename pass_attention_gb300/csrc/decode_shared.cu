@@ -27,6 +27,7 @@
 #include "device_common.cuh"
 #include "launch.cuh"
 #include "oss_internal.h"
+#include "prefix_rule.h"
 
 namespace oss {
 namespace {
@@ -174,23 +175,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_shared_join_kernel(const 
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Prefixes that cost little to read again are read by every sequence: the paged decode's
-// kernel, over two sequences for each of the batch, and the join, two launches for three. The
-// rule goes by the bytes that are read again if every prefix fills its row of the table.
-// From a graph, read again / on the tensor cores (sequences, heads, prefix): 4, 32 / 8, 1000 (12 MB):
-// 10.5 / 15.6 us; 16, 8 / 1, 4000 (31): 13.1 / 16.8; 4, 32 / 8, 4000 (49): 14.8 / 17.2; 16, 32 / 8, 1000
-// (61): 15.3 / 16.8; 37 in 5 groups, 16 / 2 of 64, 5001 (82): 19.9 / 16.6; 4, 32 / 8, 8000 (98): 20.9 / 20.8;
-// 32, 32 / 8, 1000 (127): 22.2 / 17.4. Launched one by one, 24 us of the host against 30:
-// on the GPU the two meet at 65 MB or so, with the host at twice that.
-constexpr int64_t kReadAgain = int64_t(80) << 20;
-constexpr int kPairGroups = 64;  // (every sequence looks its group up)
-
-bool in_pairs(const os_paged_cache& c, int groups, int prefix_max_pages) {
-  const int64_t again = c.batch > groups ? c.batch - groups : 0;
-  return groups <= kPairGroups &&
-         again * prefix_max_pages * c.page_size <= kReadAgain / (4 * static_cast<int64_t>(c.heads) * c.head_dim);
-}
-
 // Layout of the workspace: the prefixes' part (not in pairs), the decode's, and its states.
 struct SharedPlan {
   bool pairs;
@@ -200,7 +184,10 @@ struct SharedPlan {
 };
 
 bool make_shared_plan(int H, const os_paged_cache& c, int groups, int prefix_max_pages, SharedPlan* out) {
-  out->pairs = in_pairs(c, groups, prefix_max_pages);
+  const int group = H / c.heads, block_heads = heads_of_block(group);
+  out->pairs = read_by_every_sequence(c.batch, groups, (group + block_heads - 1) / block_heads,
+                                      static_cast<int64_t>(prefix_max_pages) * c.page_size,
+                                      4 * static_cast<int64_t>(c.heads) * c.head_dim);
   os_paged_cache walked = c;  // the sequences of the decode's kernel
   if (out->pairs) {
     walked.batch = 2 * c.batch;

@@ -1,0 +1,30 @@
+// Which way os_attention_decode_shared reads its prefixes. Host code, from what the host knows: the
+// sizes of the tables.
+#pragma once
+
+#include <cstdint>
+
+namespace oss {
+
+// Prefixes that cost little to read again are read by every sequence: the paged decode's
+// kernel, over two sequences for each of the batch, and the join, two launches for three. The
+// rule goes by the bytes that are read again if every prefix fills its row of the table.
+// From a graph, read again / on the tensor cores (sequences, heads, prefix): 4, 32 / 8, 1000 (12 MB):
+// 10.5 / 15.6 us; 16, 8 / 1, 4000 (31): 13.1 / 16.8; 4, 32 / 8, 4000 (49): 14.8 / 17.2; 16, 32 / 8, 1000
+// (61): 15.3 / 16.8; 37 in 5 groups, 16 / 2 of 64, 5001 (82): 19.9 / 16.6; 4, 32 / 8, 8000 (98): 20.9 / 20.8;
+// 32, 32 / 8, 1000 (127): 22.2 / 17.4. Launched one by one, 24 us of the host against 30:
+// on the GPU the two meet at 65 MB or so, with the host at twice that.
+constexpr int64_t kReadAgain = int64_t(80) << 20;
+constexpr int kPairGroups = 64;  // (every sequence looks its group up)
+
+// blocks: of up to 16 query heads of a key head, each of which reads the keys and values; tokens: that a
+// row of the prefix table has room for; token_bytes: of its keys and values. With blocks
+// (from a graph, again / tensor cores): 1 sequence, 128 / 1 heads, 16000 tokens (57 MB): 19.2 / 16.8; 4, 128 / 1,
+// 8000 (127): 23.6 / 16.6; 16, 64 / 1, 4000 (129): 24.5 / 16.4; 1, 128 / 1, 65536 (235): 37.0 / 28.6; 4, 128 / 1,
+// 40000 (635): 71.6 / 29.9.
+inline bool read_by_every_sequence(int64_t batch, int64_t groups, int64_t blocks, int64_t tokens, int64_t token_bytes) {
+  const int64_t again = batch * blocks > groups ? batch * blocks - groups : 0;
+  return groups <= kPairGroups && again * tokens <= kReadAgain / token_bytes;
+}
+
+}  // namespace oss
