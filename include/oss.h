@@ -680,8 +680,8 @@ OSS_API os_status os_kv_cache_evict(const os_paged_cache* cache, const float* we
  *     s_t = scale * q . k_t;  lse = ln sum_t exp(s_t);  o = sum_t exp(s_t - lse) v_t
  * A prefix is read once for 128 rows (queries of its group times query heads of a key
  * head), on the tensor cores, and not once a sequence, unless reading it again costs
- * little: up to 80 MB of it in all, by what prefix_table has room for, and up to
- * 64 groups. The two parts' states (m, l, O) are joined in fp32 with the merge
+ * little: by what prefix_table has room for, up to 80 MB in all where no group is empty,
+ * up to 256 MB wherever the sequences are, and up to 64 groups. The two parts' states (m, l, O) are joined in fp32 with the merge
  * identity, in a fixed order, so every run gives the same bits. A sequence
  * that no group names has its own tokens only; one without any key gives o = 0,
  * lse = -inf. Rounding and NaN as in os_attention_decode_paged; k and v of a prefix

@@ -39,3 +39,21 @@ def test_one_sequence(hq, hkv, prefix, tensor):
     c = Case([1], [prefix], [5], hq, hkv, page=64, seed=2)
     assert on_tensor_cores(c) == tensor
     shared(c)
+
+
+@pytest.mark.parametrize("n,prefix,tensor", [(20, 900, False), (20, 9000, True), (64, 2000, True)])
+@pytest.mark.parametrize("at", [0, 1, -1])
+def test_as_many_groups_as_sequences_and_all_in_one(n, prefix, tensor, at):
+    # a slot for every sequence, and only one in use
+    sizes, prefixes = [0] * n, [0] * n
+    sizes[at], prefixes[at] = n, prefix
+    c = Case(sizes, prefixes, [(5 * i) % 70 for i in range(n)], 16, 8, page=64, seed=n)
+    assert on_tensor_cores(c) == tensor
+    shared(c, rows=[0, 1, n - 1])
+
+
+@pytest.mark.parametrize("n,prefix,tensor", [(5, 2000, False), (20, 9000, True), (64, 2000, True)])
+def test_as_many_groups_as_sequences_and_one_in_each(n, prefix, tensor):
+    c = Case([1] * n, [prefix - 31 * i for i in range(n)], [(5 * i) % 70 for i in range(n)], 16, 8, page=64, seed=n)
+    assert on_tensor_cores(c) == tensor
+    shared(c, rows=[0, n // 2, n - 1])

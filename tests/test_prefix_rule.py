@@ -12,6 +12,7 @@ from pass_attention_gb300 import build_lib
 
 CSRC = os.path.join(os.path.dirname(build_lib.__file__), "csrc")
 LITTLE = 80 << 20   # where no group is empty
+MOST = 256 << 20    # wherever the sequences are
 PROBE = r"""
 #include <cstdio>
 #include "prefix_rule.h"
@@ -60,6 +61,17 @@ def test_groups_that_all_hold_a_sequence(rule):
         batch, groups, blocks, tokens, token_bytes = c
         if pairs:
             assert again([1] * (groups - 1) + [batch - groups + 1], blocks, tokens, token_bytes) <= LITTLE, c
+
+
+def test_groups_of_which_all_but_one_are_empty(rule):
+    # slots for 64 groups, one of them in use: 64 sequences behind 65536 tokens of 8 key heads read 17 GB
+    assert rule([(64, 64, 1, 65536, 4096), (16, 16, 1, 4000, 4096), (16, 16, 1, 16000, 4096)]) == [False, True, False]
+    r = random.Random(2)
+    cases = [draw(r) for _ in range(2000)]
+    for c, pairs in zip(cases, rule(cases)):
+        batch, groups, blocks, tokens, token_bytes = c
+        if pairs:
+            assert again([batch] + [0] * (min(groups, 9) - 1), blocks, tokens, token_bytes) <= MOST, c
 
 
 def test_a_block_of_query_heads_reads_by_itself(rule):
