@@ -981,7 +981,8 @@ def attention_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
 
 # -- the cache in 8 bits ---------------------------------------------------------------------
 
-_F8, _E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+# (None on a PyTorch before 2.7, which has everything else that this file uses)
+_F8, _E8 = getattr(torch, "float8_e4m3fn", None), getattr(torch, "float8_e8m0fnu", None)
 
 
 def _scale_strides(t: torch.Tensor, name: str, shape, device: torch.device):
@@ -1036,6 +1037,8 @@ def _cache_fp8(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype):
 def _cache_fp8_checked(k_pages, v_pages, k_scales, v_scales, page_table, kv_len, dtype):
     """The device and strides of a cache that the quick check has not passed: a view
     off the common path, or what is wrong with it is raised."""
+    if _F8 is None or _E8 is None:
+        raise RuntimeError("the 8-bit cache needs a PyTorch with float8_e4m3fn and float8_e8m0fnu")
     if not isinstance(k_pages, torch.Tensor) or k_pages.dtype is not _F8:
         raise TypeError("k_pages must be a float8_e4m3fn torch.Tensor")
     if not k_pages.is_cuda:
