@@ -57,3 +57,11 @@ def test_as_many_groups_as_sequences_and_one_in_each(n, prefix, tensor):
     c = Case([1] * n, [prefix - 31 * i for i in range(n)], [(5 * i) % 70 for i in range(n)], 16, 8, page=64, seed=n)
     assert on_tensor_cores(c) == tensor
     shared(c, rows=[0, n // 2, n - 1])
+
+
+def test_one_tile_of_rows_over_the_whole_gpu():
+    # 16 rows of a tile (two sequences of 8 heads), whose 1251 KV steps are cut over all SMs and joined
+    # from their parts. (In a table of its own width the prefix would be read twice, 82 MB.)
+    c = Case([2], [160001], [5, 40], 8, 1, page=64, seed=3, prefix_columns=3000)
+    assert on_tensor_cores(c)
+    shared(c)
