@@ -926,7 +926,8 @@ def attention_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     """``attention_decode_paged`` for sequences that share prefixes: the keys of a
     sequence of group g are the prefix_len[g] tokens in the pages of row g of
     prefix_table [groups, max_prefix_pages], then its own (page_table, kv_len) in
-    the same pools. A prefix is read once for its whole group. cu_groups [groups + 1]:
+    the same pools. A long prefix is read once for up to 128 rows of its group's queries
+    and heads, a short one by every sequence. cu_groups [groups + 1]:
     group g is sequences cu_groups[g] .. cu_groups[g + 1] - 1 (None: one group of all).
     All of them int32 on the device. Returns ``(o, lse)``, [batch, Hq, D] and fp32
     [batch, Hq]. See ``os_attention_decode_shared``."""
