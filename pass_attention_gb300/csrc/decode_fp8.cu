@@ -31,7 +31,8 @@
 // softmax (106.5 -> 104.5). 64 sequences of up to 8192 tokens, 32 heads over 8: 102 us (6.0 TB/s, 0.90 of
 // the copy peak, 6 us of it the launch's beginning and end); 6 of up to 32768, 16 heads of 64 in
 // fp16: 58 us (0.85: instructions; a tile there has 32 keys, 7 us more with 16); one of 777 tokens
-// 7.2 us from a graph.
+// 7.2 us from a graph. Groups of 9 to 16 heads (236 registers, two CTAs an SM) wait for their instructions'
+// latencies, not for HBM: 64 of up to 8192, 128 heads over 8, 145 us where 32 over 8 take 92 (16-bit: 218 and 178).
 
 #include <atomic>
 #include <cstdint>
