@@ -680,10 +680,10 @@ OSS_API os_status os_kv_cache_evict(const os_paged_cache* cache, const float* we
  *     s_t = scale * q . k_t;  lse = ln sum_t exp(s_t);  o = sum_t exp(s_t - lse) v_t
  * A prefix is read on the tensor cores, once for a tile of up to 128 rows and not once a
  * sequence: queries of its group times 2^n query heads of a key head, the largest power
- * of two that divides H / heads (of 8 heads all, of 12 four, of 7 one: a tile for each four, or each
- * one, of them). Unless reading it again costs little: by what prefix_table has room
- * for, up to 80 MB in all where no group is empty, up to 256 MB wherever the sequences
- * are, and up to 64 groups. The two parts' states (m, l, O) are joined in fp32 with the merge
+ * of two that divides H / heads (of 8 heads all, of 12 four, of 7 one; each four, or each one,
+ * have tiles of their own). Where reading it again costs little, every sequence reads it:
+ * by what prefix_table has room for, up to 80 MB again in all where no group is empty, and
+ * up to 256 MB wherever the sequences are, for up to 64 groups. The two parts' states (m, l, O) are joined in fp32 with the merge
  * identity, in a fixed order, so every run gives the same bits. A sequence
  * that no group names has its own tokens only; one without any key gives o = 0,
  * lse = -inf. Rounding and NaN as in os_attention_decode_paged; k and v of a prefix

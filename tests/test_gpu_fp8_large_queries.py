@@ -58,8 +58,12 @@ def test_large_queries_beside_large_keys(d):
     codes[:, 2] = 0x7e
     q = torch.zeros((1, 8, d), dtype=torch.bfloat16, device="cuda")
     q[0, :, 1] = TOP
-    o, lse = run(q, cache(codes, torch.full((20,), 246, dtype=torch.uint8)))
+    o, lse = oss.attention_decode_paged_fp8(q, *cache(codes, torch.full((20,), 246, dtype=torch.uint8)))
+    assert oss.check_device_error() == 0
+    # equal weights of 20 keys; the values are 1, 2, 4 and 8, of which every sum is exact, and o
+    # rounds once more to bf16 (3.75 is one)
     assert (lse - math.log(20)).abs().max() <= 2.0 ** -20
+    assert (o.float() - 3.75).abs().max() <= 3.75 * torch.finfo(torch.bfloat16).eps / 2
 
 
 def test_scales_of_nan_beside_large_factors():
