@@ -683,10 +683,10 @@ OSS_API os_status os_kv_cache_evict(const os_paged_cache* cache, const float* we
  * of two that divides H / heads (of 8 heads all, of 12 four, of 7 one; each four, or each one,
  * have tiles of their own). Where reading it again costs little, every sequence reads it:
  * by what prefix_table has room for, up to 80 MB again in all where no group is empty, and
- * up to 256 MB wherever the sequences are, for up to 64 groups. The two parts' states (m, l, O) are joined in fp32 with the merge
- * identity, in a fixed order, so every run gives the same bits. A sequence
- * that no group names has its own tokens only; one without any key gives o = 0,
- * lse = -inf. Rounding and NaN as in os_attention_decode_paged; k and v of a prefix
+ * up to 256 MB wherever the sequences are, for up to 64 groups. The two parts' states
+ * (m, l, O) are joined in fp32 with the merge identity, in a fixed order, so every run
+ * gives the same bits. A sequence that no group names has its own tokens only; one
+ * without any key gives o = 0, lse = -inf. Rounding and NaN as in os_attention_decode_paged; k and v of a prefix
  * are finite.
  *
  *   cache       the pools, and the sequences' own tokens (their new ones among

@@ -982,7 +982,7 @@ def attention_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
 
 # -- the cache in 8 bits ---------------------------------------------------------------------
 
-# (None on a PyTorch before 2.7, which has everything else that this file uses)
+# (None on a PyTorch before 2.7: the 8-bit cache is not there, the rest is)
 _F8, _E8 = getattr(torch, "float8_e4m3fn", None), getattr(torch, "float8_e8m0fnu", None)
 
 

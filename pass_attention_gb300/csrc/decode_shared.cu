@@ -11,7 +11,8 @@
 // group's others are tiles that walk the prefix for themselves: with 12 heads a key head
 // three, with 7 seven. 64 sequences behind 65536 tokens of 8 key heads, 24 query heads 178 us, 32: 110,
 // 40: 258; of 4 key heads, 28: 171, 48: 131; 16 behind 32768 of 4 key heads, 28: 63, 48: 43.)
-// (2) The sequences' own tokens, by the paged decode's first kernel (decode_paged.cu). (3) The join below, of the parts and states that the two have left.
+// (2) The sequences' own tokens, by the paged decode's first kernel (decode_paged.cu). (3) The join
+// below, of the parts and states that the two have left.
 //
 // What bounds it: the first kernel the chain of a KV step (0.9 us for 128 rows of 128 keys),
 // from about two tiles of rows on, HBM below that; the second HBM. They run side by side
